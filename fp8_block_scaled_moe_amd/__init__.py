@@ -16,4 +16,7 @@ from .ops import (  # noqa: F401
     fused_bf16_workspace_size, alloc_workspace_bf16, moe_fused_bf16, gemm1_swiglu_bf16, gemm2_weighted_bf16,
     tune_tiles_fp8, moe_fused_fp8_small, fused_small_workspace_size, small_layer_flag,
     moe_fused_fp8_noalloc, NOALLOC_SCRATCH_BYTES,
+    fused_int8_workspace_size, alloc_workspace_int8, moe_fused_int8, gemm1_swiglu_int8, quant_rows_int8,
+    gemm2_weighted_int8, add_rmsnorm_quant, NORM_BF16, NORM_FP8, NORM_MXFP8, NORM_INT8, moe_router_topk,
+    SCORE_SOFTMAX, SCORE_SIGMOID,
 )

@@ -8,7 +8,7 @@ import os
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp8moe.so")
 
-_i32, _i64, _sz, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
+_i32, _i64, _sz, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
 _pi32 = ctypes.POINTER(ctypes.c_int32)
 _psz = ctypes.POINTER(ctypes.c_size_t)
 _pi32, _pf32 = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_float)
@@ -72,6 +72,25 @@ SIGNATURES = {
     "moe_pack_mx_scales": (ctypes.c_int, [_vp, _i64, _i32, _i32, _vp, _vp]),
     "moe_combine": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp]),
     "gated_act_fp8_quant": (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _i32, _vp]),
+    # x, residual, residual_f32, weight, weight_f32, eps, T, H, format, residual_out, norm_out, q, scale, stream
+    "add_rmsnorm_quant": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i32, _f32, _i64, _i32, _i32, _vp, _vp, _vp, _vp,
+                                         _vp]),
+    # logits, logits_bf16, bias, T, E, K, score, n_group, topk_group, group_top, renormalize, scale, ids, weights, stream
+    "moe_router_topk": (ctypes.c_int, [_vp, _i32, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp,
+                                       _vp, _vp]),
+    "moe_fused_int8_workspace_size": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _psz]),
+    # x, x_scale, w13, w13_scale, w2, w2_scale, ids, weights, T, H, I, E, K, out, ws, bytes, tile_m, layout, stream
+    "moe_fused_int8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32,
+                                      _vp, _vp, _sz, _i32, _i32, _vp]),
+    # x, x_scale, w13, w13_scale, padded_indptr, sorted_src, T, H, I, E, K, align, act, cap, tile_m, layout, stream
+    "moe_gemm1_swiglu_int8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _vp,
+                                             _i64, _i32, _i32, _vp]),
+    # in, sorted_src, rows, N, q, scale, stream
+    "moe_quant_rows_int8": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _vp, _vp]),
+    # q, q_scale, w2, w2_scale, padded_indptr, sorted_src, topk_weights, T, H, I, E, K, align, Y, cap, tile_m,
+    # layout, stream
+    "moe_gemm2_weighted_int8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32,
+                                               _i32, _vp, _i64, _i32, _i32, _vp]),
     "moe_select_tile": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, _pi32, _pi32]),
     "moe_auto_tiles": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, _pi32, _pi32]),
     "moe_select_tile_classes": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _pi32]),

@@ -4,10 +4,12 @@
 // memory or synchronises the host.
 #include <hip/hip_runtime.h>
 
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <string>
 #include <type_traits>
 
@@ -56,16 +58,18 @@ size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 // Workspace layout of the fused layer in every operand format (each part
 // 256-byte aligned); the small-T call adds one aligned block of barrier words.
 struct WsLayout {
-  size_t counts, m_indptr, padded, sorted_src, src_to_sorted, q, q_scale, Y, total;
+  size_t counts, m_indptr, padded, sorted_src, src_to_sorted, q, q_scale, Y, act, total;
 };
 
 // Operand formats of the layer: FP8 with fp32 block scales, MXFP8 and MXFP4
-// (W4A4), both with E8M0 scales per 32 elements, and unquantised bf16.
-enum Fmt { kFmtFp8 = 0, kFmtMx8 = 1, kFmtMx4 = 2, kFmtBf16 = 3 };
+// (W4A4), both with E8M0 scales per 32 elements, unquantised bf16, and int8
+// with a scale per token and channel.
+enum Fmt { kFmtFp8 = 0, kFmtMx8 = 1, kFmtMx4 = 2, kFmtBf16 = 3, kFmtInt8 = 4 };
 
 // MX: q_scale holds one E8M0 byte per 32 columns instead of a float per 128;
 // MXFP4: q holds two e2m1 codes per byte; bf16: q holds 2 bytes per element
-// and there is no q_scale.
+// and there is no q_scale; int8: a float per row, and act holds the bf16
+// intermediate ahead of its quantisation.
 WsLayout ws_layout(int64_t T, int H, int I, int E, int K, int fmt) {
   const int64_t R = T * K;
   const int64_t cap = R + (int64_t)E * (kFusedAlign - 1);
@@ -79,9 +83,11 @@ WsLayout ws_layout(int64_t T, int H, int I, int E, int K, int fmt) {
   w.src_to_sorted = take(sizeof(int32_t) * (R > 0 ? R : 1));
   w.q = take((size_t)cap * (fmt == kFmtMx4 ? I / 2 : fmt == kFmtBf16 ? 2 * (size_t)I : I));
   w.q_scale = take(fmt == kFmtBf16  ? 0
+                   : fmt == kFmtInt8 ? sizeof(float) * (size_t)cap
                    : fmt != kFmtFp8 ? (size_t)cap * (I / 32)
                                     : sizeof(float) * (size_t)cap * (I / 128));
   w.Y = take(sizeof(uint16_t) * (size_t)(R > 0 ? R : 1) * H);
+  w.act = take(fmt == kFmtInt8 ? sizeof(uint16_t) * (size_t)cap * I : 0);
   w.total = off;
   return w;
 }
@@ -144,10 +150,10 @@ int pick_tile_m(int requested, int64_t T, int K, int n, int k, int E, bool gated
   return auto_tile_m(T, K, n, k, E, device_num_cu(), gated);
 }
 
-// Scale pointer type of each format: fp32 block scales (FP8) or E8M0 codes
+// Scale pointer type of each format: fp32 scales (FP8, int8) or E8M0 codes
 // (MX; bf16 passes null scale pointers of this type).
 template <int F>
-using scale_ptr_t = std::conditional_t<F == kFmtFp8, float, uint8_t>;
+using scale_ptr_t = std::conditional_t<F == kFmtFp8 || F == kFmtInt8, float, uint8_t>;
 
 // MXFP4 rows are 256-element K steps: H and I multiples of 256
 template <int F>
@@ -185,7 +191,7 @@ struct FusedPlan {
   int32_t *counts, *m_indptr, *padded, *sorted_src, *src_to_sorted;
   uint8_t* q;
   scale_ptr_t<F>* q_scale;
-  uint16_t* Y;
+  uint16_t *Y, *act;
   int64_t R, cap;
   int align;
   bool packed;
@@ -227,6 +233,7 @@ int fused_prepare(const void* x, const scale_ptr_t<F>* x_scale, const void* w13,
   P.q = ws + L.q;
   P.q_scale = reinterpret_cast<scale_ptr_t<F>*>(ws + L.q_scale);
   P.Y = reinterpret_cast<uint16_t*>(ws + L.Y);
+  P.act = reinterpret_cast<uint16_t*>(ws + L.act);
   return FP8MOE_OK;
 }
 
@@ -431,6 +438,7 @@ const char* moe_status_string(int status) {
     case FP8MOE_ERR_WORKSPACE: return "workspace missing, too small or misaligned";
     case FP8MOE_ERR_HIP: return "HIP runtime error";
     case FP8MOE_ERR_LIMIT: return "beyond a library limit";
+    case FP8MOE_ERR_ARG: return "argument outside its documented values";
     default: return "unknown status";
   }
 }
@@ -826,6 +834,204 @@ int moe_select_tile_classes(int64_t total_rows, int32_t n, int32_t k, int32_t E,
   if (!tile_m) return fail(FP8MOE_ERR_NULL, "null output");
   const TileClasses tc{narrow, tile_n_narrow, tile_n_32, tile_n_64, tile_n_128};
   *tile_m = select_tile_m(total_rows, n, k, E, num_cu, tc);
+  return ok();
+}
+
+}  // extern "C"
+
+namespace {
+
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  if (!a || !b || na <= 0 || nb <= 0) return false;
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
+
+// Tile height of the int8 products: the smallest that holds an even share of
+// the routed rows over the experts they can reach.
+int int8_tile_m(int requested, int64_t R, int E) {
+  if (requested != -1) return requested;
+  const int64_t active = R < E ? R : E, rows = active > 0 ? (R + active - 1) / active : 0;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+int check_int8_stage(int64_t T, int32_t H, int32_t I, int32_t E, int32_t K, int32_t align, int64_t cap,
+                     int32_t tile_m, int32_t weight_layout) {
+  int st = check_dims(T, H, I, E, K);
+  if (st) return st;
+  if (!valid_layout(weight_layout)) return fail(FP8MOE_ERR_SHAPE, "weight_layout %d not 0 or 1", weight_layout);
+  if (!valid_align(align)) return fail(FP8MOE_ERR_ALIGN, "align %d not in {16,32,64,128}", align);
+  if (tile_m != -1 && tile_m != 16 && tile_m != 32 && tile_m != 64)
+    return fail(FP8MOE_ERR_TILE, "tile_m %d not in {-1,16,32,64}", tile_m);
+  if (cap < 0 || cap >= kMaxRows) return fail(FP8MOE_ERR_SHAPE, "invalid cap %lld", (long long)cap);
+  return FP8MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int add_rmsnorm_quant(const void* x, const void* residual, int32_t residual_f32, const void* weight,
+                      int32_t weight_f32, float eps, int64_t T, int32_t H, int32_t format, void* residual_out,
+                      void* norm_out, void* q, void* scale, void* stream) {
+  if (T < 0 || H <= 0) return fail(FP8MOE_ERR_SHAPE, "invalid T=%lld H=%d", (long long)T, H);
+  if (format < FP8MOE_NORM_BF16 || format > FP8MOE_NORM_INT8)
+    return fail(FP8MOE_ERR_ARG, "format %d not in {0,1,2,3}", format);
+  const int step = format == FP8MOE_NORM_FP8 ? 128 : format == FP8MOE_NORM_MXFP8 ? 32 : 8;
+  if (H % step) return fail(FP8MOE_ERR_ALIGN, "H=%d must be a multiple of %d in this format", H, step);
+  if (H > FP8MOE_MAX_DIM || T >= ((int64_t)1 << 24))
+    return fail(FP8MOE_ERR_LIMIT, "H=%d must be at most %d and T=%lld below 2^24", H, FP8MOE_MAX_DIM, (long long)T);
+  if (!(eps > 0.f) || !isfinite(eps)) return fail(FP8MOE_ERR_ARG, "eps must be finite and positive");
+  if (!residual != !residual_out) return fail(FP8MOE_ERR_NULL, "residual and residual_out go together");
+  if (T == 0) return ok();
+  const bool codes = format != FP8MOE_NORM_BF16;
+  if (!x || !weight || (codes ? !q || !scale : !norm_out)) return fail(FP8MOE_ERR_NULL, "null tensor argument");
+  for (const void* p : {x, residual, weight, (const void*)residual_out, (const void*)norm_out})
+    if (!aligned16(p)) return fail(FP8MOE_ERR_ALIGN, "tensors must be 16-byte aligned");
+  if (codes && (!aligned16(q) || !aligned16(scale))) return fail(FP8MOE_ERR_ALIGN, "tensors must be 16-byte aligned");
+  const int64_t n = T * H, rn = n * (residual_f32 ? 4 : 2);
+  const int64_t sn = format == FP8MOE_NORM_FP8 ? n / 128 * 4 : format == FP8MOE_NORM_MXFP8 ? n / 32 : T * 4;
+  struct Range { const void* p; int64_t bytes; };
+  const Range in[] = {{x, 2 * n}, {weight, (int64_t)H * (weight_f32 ? 4 : 2)}, {residual, rn}};
+  const Range out[] = {{residual_out, rn}, {norm_out, 2 * n}, {codes ? q : nullptr, n}, {codes ? scale : nullptr, sn}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 3; ++j)
+      if (overlap(out[i].p, out[i].bytes, in[j].p, in[j].bytes) && !(i == 0 && j == 2 && residual_out == residual))
+        return fail(FP8MOE_ERR_SHAPE, "an output overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+        return fail(FP8MOE_ERR_SHAPE, "two outputs overlap");
+  }
+  hipError_t err = launch_add_rmsnorm(static_cast<const uint16_t*>(x), residual, residual_f32 != 0, weight,
+                                      weight_f32 != 0, eps, T, H, format, residual_out,
+                                      static_cast<uint16_t*>(norm_out), static_cast<uint8_t*>(q), scale,
+                                      (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "add_rmsnorm launch");
+  return ok();
+}
+
+int moe_router_topk(const void* logits, int32_t logits_bf16, const float* bias, int64_t T, int32_t E, int32_t K,
+                    int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top, int32_t renormalize,
+                    float scale, int32_t* topk_ids, float* topk_weights, void* stream) {
+  if (T < 0 || E < 1) return fail(FP8MOE_ERR_SHAPE, "invalid T=%lld E=%d", (long long)T, E);
+  if (E > FP8MOE_MAX_EXPERTS || T >= ((int64_t)1 << 26))
+    return fail(FP8MOE_ERR_LIMIT, "E=%d must be at most %d and T=%lld below 2^26", E, FP8MOE_MAX_EXPERTS,
+                (long long)T);
+  if (score != FP8MOE_SCORE_SOFTMAX && score != FP8MOE_SCORE_SIGMOID)
+    return fail(FP8MOE_ERR_ARG, "score %d not 0 or 1", score);
+  if (n_group < 1 || n_group > FP8MOE_MAX_ROUTER_GROUPS || E % n_group)
+    return fail(FP8MOE_ERR_ARG, "n_group %d must divide E=%d and be at most %d", n_group, E,
+                FP8MOE_MAX_ROUTER_GROUPS);
+  if (topk_group < 1 || topk_group > n_group)
+    return fail(FP8MOE_ERR_ARG, "topk_group %d not in [1, n_group=%d]", topk_group, n_group);
+  if (group_top < 1 || group_top > 2 || (n_group > 1 && group_top > E / n_group))
+    return fail(FP8MOE_ERR_ARG, "group_top %d not 1 or 2, or beyond a group's experts", group_top);
+  if (!isfinite(scale)) return fail(FP8MOE_ERR_ARG, "scale must be finite");
+  if (K < 1 || K > FP8MOE_MAX_ROUTER_TOPK || K > E / n_group * topk_group)
+    return fail(FP8MOE_ERR_TOPK, "K=%d not in [1, %d] or beyond the %d experts of the kept groups", K,
+                FP8MOE_MAX_ROUTER_TOPK, E / n_group * topk_group);
+  if (T == 0) return ok();
+  if (!logits || !topk_ids || !topk_weights) return fail(FP8MOE_ERR_NULL, "null tensor argument");
+  hipError_t err = launch_router_topk(logits, logits_bf16 != 0, bias, (int)T, E, K, score, n_group, topk_group,
+                                      group_top, renormalize != 0, scale, topk_ids, topk_weights,
+                                      (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "router launch");
+  return ok();
+}
+
+int moe_fused_int8_workspace_size(int64_t T, int32_t H, int32_t I, int32_t E, int32_t K, size_t* bytes) {
+  int st = check_dims(T, H, I, E, K);
+  if (st) return st;
+  if (!bytes) return fail(FP8MOE_ERR_NULL, "bytes is null");
+  *bytes = ws_layout(T, H, I, E, K, kFmtInt8).total;
+  return ok();
+}
+
+int moe_fused_int8(const void* x, const float* x_scale, const void* w13, const float* w13_scale, const void* w2,
+                   const float* w2_scale, const int32_t* topk_ids, const float* topk_weights, int64_t T, int32_t H,
+                   int32_t I, int32_t E, int32_t K, void* out, void* workspace, size_t workspace_bytes,
+                   int32_t tile_m, int32_t weight_layout, void* stream) {
+  FusedPlan<kFmtInt8> P{};
+  int st = fused_prepare<kFmtInt8>(x, x_scale, w13, w13_scale, w2, w2_scale, topk_ids, topk_weights, T, H, I, E, K,
+                                   true, out, workspace, workspace_bytes, weight_layout, P);
+  if (st) return st;
+  if ((st = check_int8_stage(T, H, I, E, K, kFusedAlign, 0, tile_m, weight_layout))) return st;
+  if (T == 0) return ok();
+  if (!aligned16(x) || !aligned16(w13) || !aligned16(w2) || !aligned16(out))
+    return fail(FP8MOE_ERR_ALIGN, "tensors must be 16-byte aligned");
+  const int tm = int8_tile_m(tile_m, P.R, E);
+  hipStream_t s = (hipStream_t)stream;
+  hipError_t err = launch_route_permute(topk_ids, (int)P.R, E, P.align, (int)P.cap, P.counts, P.m_indptr, P.padded,
+                                        P.sorted_src, P.src_to_sorted, s);
+  if (err != hipSuccess) return hip_fail(err, "route_permute launch");
+  GroupedRows g{P.padded, P.sorted_src, P.cap, E, K, P.R, device_num_cu()};
+  err = launch_gemm1_int8(static_cast<const uint8_t*>(x), x_scale, static_cast<const uint8_t*>(w13), w13_scale, g, H,
+                          I, P.act, tm, P.packed, s);
+  if (err != hipSuccess) return hip_fail(err, "gemm1 launch");
+  err = launch_quant_rows_int8(P.act, P.sorted_src, P.cap, I, P.q, P.q_scale, s);
+  if (err != hipSuccess) return hip_fail(err, "quant_rows launch");
+  err = launch_gemm2_int8(P.q, P.q_scale, static_cast<const uint8_t*>(w2), w2_scale, topk_weights, g, H, I, P.Y, tm,
+                          P.packed, s);
+  if (err != hipSuccess) return hip_fail(err, "gemm2 launch");
+  err = launch_combine(P.Y, topk_ids, (int)T, H, E, K, static_cast<uint16_t*>(out), s);
+  if (err != hipSuccess) return hip_fail(err, "combine launch");
+  return ok();
+}
+
+int moe_gemm1_swiglu_int8(const void* x, const float* x_scale, const void* w13, const float* w13_scale,
+                          const int32_t* padded_indptr, const int32_t* sorted_src, int64_t T, int32_t H, int32_t I,
+                          int32_t E, int32_t K, int32_t align, void* act, int64_t cap, int32_t tile_m,
+                          int32_t weight_layout, void* stream) {
+  int st = check_int8_stage(T, H, I, E, K, align, cap, tile_m, weight_layout);
+  if (st) return st;
+  if (T == 0 || cap == 0) return ok();
+  if (!x || !x_scale || !w13 || !w13_scale || !padded_indptr || !sorted_src || !act)
+    return fail(FP8MOE_ERR_NULL, "null tensor argument");
+  if (!aligned16(x) || !aligned16(w13) || !aligned16(act))
+    return fail(FP8MOE_ERR_ALIGN, "tensors must be 16-byte aligned");
+  GroupedRows g{padded_indptr, sorted_src, cap, E, K, T * K, device_num_cu()};
+  hipError_t err = launch_gemm1_int8(static_cast<const uint8_t*>(x), x_scale, static_cast<const uint8_t*>(w13),
+                                     w13_scale, g, H, I, static_cast<uint16_t*>(act), int8_tile_m(tile_m, T * K, E),
+                                     weight_layout == FP8MOE_WEIGHTS_MFMA_TILED, (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "gemm1 launch");
+  return ok();
+}
+
+int moe_quant_rows_int8(const void* in, const int32_t* sorted_src, int64_t rows, int32_t N, void* q, float* scale,
+                        void* stream) {
+  if (rows < 0 || N <= 0) return fail(FP8MOE_ERR_SHAPE, "invalid rows=%lld N=%d", (long long)rows, N);
+  if (N % 8) return fail(FP8MOE_ERR_ALIGN, "N=%d must be a multiple of 8", N);
+  if (rows == 0) return ok();
+  if (!in || !q || !scale) return fail(FP8MOE_ERR_NULL, "null tensor argument");
+  if (!aligned16(in) || !aligned16(q)) return fail(FP8MOE_ERR_ALIGN, "tensors must be 16-byte aligned");
+  if (overlap(in, 2 * rows * N, q, rows * N) || overlap(in, 2 * rows * N, scale, 4 * rows) ||
+      overlap(q, rows * N, scale, 4 * rows))
+    return fail(FP8MOE_ERR_SHAPE, "in, q and scale overlap");
+  hipError_t err = launch_quant_rows_int8(static_cast<const uint16_t*>(in), sorted_src, rows, N,
+                                          static_cast<uint8_t*>(q), scale, (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "quant_rows launch");
+  return ok();
+}
+
+int moe_gemm2_weighted_int8(const void* q, const float* q_scale, const void* w2, const float* w2_scale,
+                            const int32_t* padded_indptr, const int32_t* sorted_src, const float* topk_weights,
+                            int64_t T, int32_t H, int32_t I, int32_t E, int32_t K, int32_t align, void* Y,
+                            int64_t cap, int32_t tile_m, int32_t weight_layout, void* stream) {
+  int st = check_int8_stage(T, H, I, E, K, align, cap, tile_m, weight_layout);
+  if (st) return st;
+  if (T == 0 || cap == 0) return ok();
+  if (!q || !q_scale || !w2 || !w2_scale || !padded_indptr || !sorted_src || !topk_weights || !Y)
+    return fail(FP8MOE_ERR_NULL, "null tensor argument");
+  if (!aligned16(q) || !aligned16(w2) || !aligned16(Y))
+    return fail(FP8MOE_ERR_ALIGN, "tensors must be 16-byte aligned");
+  GroupedRows g{padded_indptr, sorted_src, cap, E, K, T * K, device_num_cu()};
+  hipError_t err = launch_gemm2_int8(static_cast<const uint8_t*>(q), q_scale, static_cast<const uint8_t*>(w2),
+                                     w2_scale, topk_weights, g, H, I, static_cast<uint16_t*>(Y),
+                                     int8_tile_m(tile_m, T * K, E), weight_layout == FP8MOE_WEIGHTS_MFMA_TILED,
+                                     (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "gemm2 launch");
   return ok();
 }
 

@@ -86,6 +86,28 @@ hipError_t launch_gemm1_bf16(const uint16_t* x, const uint16_t* w13, const Group
 hipError_t launch_gemm2_bf16(const uint16_t* q, const uint16_t* w2, const float* topk_weights, const GroupedRows& g,
                              int H, int I, uint16_t* Y, int tile_m, int tile_n, bool packed, hipStream_t stream);
 
+// Int8 variants: one scale per token row and per weight row.  GEMM1 writes the
+// SwiGLU output as bf16 (act [cap][I]), launch_quant_rows_int8 quantises its
+// rows (those with sorted_src >= 0; every row if NULL), GEMM2 takes the codes
+// and row scales.  tile_m in {16, 32, 64}.
+hipError_t launch_gemm1_int8(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
+                             const GroupedRows& g, int H, int I, uint16_t* act, int tile_m, bool packed,
+                             hipStream_t stream);
+hipError_t launch_quant_rows_int8(const uint16_t* in, const int32_t* sorted_src, int64_t rows, int N, uint8_t* q,
+                                  float* scale, hipStream_t stream);
+hipError_t launch_gemm2_int8(const uint8_t* q, const float* q_scale, const uint8_t* w2, const float* w2_scale,
+                             const float* topk_weights, const GroupedRows& g, int H, int I, uint16_t* Y, int tile_m,
+                             bool packed, hipStream_t stream);
+
+// Residual addition + RMS norm + quantisation (format: FP8MOE_NORM_*), and the
+// router's choice of experts (score: FP8MOE_SCORE_*).
+hipError_t launch_add_rmsnorm(const uint16_t* x, const void* residual, bool residual_f32, const void* weight,
+                              bool weight_f32, float eps, int64_t T, int H, int format, void* residual_out,
+                              uint16_t* norm_out, uint8_t* q, void* scale, hipStream_t stream);
+hipError_t launch_router_topk(const void* logits, bool bf16, const float* bias, int T, int E, int K, int score,
+                              int n_group, int topk_group, int group_top, bool renormalize, float scale,
+                              int32_t* ids, float* weights, hipStream_t stream);
+
 // Device address, on the current device, of the allocation-free layer's
 // scratch array (FP8MOE_NOALLOC_SCRATCH_BYTES; noalloc.hip).
 hipError_t noalloc_scratch(void** ptr);

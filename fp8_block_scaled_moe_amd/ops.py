@@ -5,6 +5,7 @@ check dtypes/shapes/devices, allocate outputs with torch, pass raw pointers
 and the current HIP stream, and raise Fp8MoeError on a non-zero status.
 """
 
+import contextlib
 import ctypes
 
 import torch
@@ -40,6 +41,34 @@ def _u8(t):
     scale tensors as torch.float8_e8m0fnu or as uint8 codes."""
     if t is not None and t.dtype in (torch.float8_e4m3fn, torch.float8_e8m0fnu):
         return t.view(torch.uint8)
+    return t
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+@contextlib.contextmanager
+def _on(dev):
+    """The launches of a call go to its tensors' device, whichever is current."""
+    if torch.cuda.current_device() == dev.index:
+        yield
+    else:
+        with torch.cuda.device(dev):
+            yield
+
+
+def _out(t, shape, dtype, name, dev):
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(t, dtype, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
     return t
 
 
@@ -86,14 +115,14 @@ WEIGHTS_ROW_MAJOR, WEIGHTS_MFMA_TILED = 0, 1
 def pack_weights(w, out=None):
     """Expert weights e4m3 [E, N, K] row-major -> the MFMA-tiled layout (same shape and byte
     count, bytes permuted; see moe_pack_weights in include/fp8moe.h).  bf16 weights are packed
-    as their bytes and returned as bf16 of the same shape."""
-    if w.dtype == torch.bfloat16:
+    as their bytes and returned as bf16 of the same shape, int8 weights likewise."""
+    if w.dtype in (torch.bfloat16, torch.int8):
         if out is not None:
-            _need(out, torch.bfloat16, "out", 3)
+            _need(out, w.dtype, "out", 3)
             if tuple(out.shape) != tuple(w.shape):
                 raise ValueError("out must have the shape of w")
         packed = pack_weights(w.view(torch.uint8), None if out is None else out.view(torch.uint8))
-        return packed.view(torch.bfloat16)
+        return packed.view(w.dtype)
     w = _u8(w)
     _need(w, torch.uint8, "w", 3)
     E, N, K = w.shape
@@ -567,6 +596,126 @@ def gemm2_weighted_bf16(q, w2, route, topk_weights, T, K, align, tile_m=-1, tile
     return Y
 
 
+# ---------------------------------------------------------------- int8 variant
+
+def fused_int8_workspace_size(T, H, I, E, K):
+    n = ctypes.c_size_t(0)
+    check(lib().moe_fused_int8_workspace_size(T, H, I, E, K, ctypes.byref(n)))
+    return int(n.value)
+
+
+def alloc_workspace_int8(T, H, I, E, K, device):
+    """A device workspace for moe_fused_int8."""
+    return torch.empty(fused_int8_workspace_size(T, H, I, E, K), dtype=torch.uint8, device=device)
+
+
+def moe_fused_int8(x, x_scale, w13, w13_scale, w2, w2_scale, topk_ids, topk_weights, out=None, workspace=None,
+                   tile_m=-1, weight_layout=WEIGHTS_ROW_MAJOR):
+    """W8A8 int8 MoE layer: x int8 [T, H] with x_scale [T], w13 int8 [E, 2I, H] with w13_scale
+    [E, 2I], w2 int8 [E, H, I] with w2_scale [E, H], scales fp32.  Returns bf16 [T, H].
+    weight_layout 1: w13 and w2 packed by pack_weights."""
+    _need(x, torch.int8, "x", 2)
+    _need(x_scale, torch.float32, "x_scale", 1)
+    _need(w13, torch.int8, "w13", 3)
+    _need(w13_scale, torch.float32, "w13_scale", 2)
+    _need(w2, torch.int8, "w2", 3)
+    _need(w2_scale, torch.float32, "w2_scale", 2)
+    _need(topk_ids, torch.int32, "topk_ids", 2)
+    _need(topk_weights, torch.float32, "topk_weights", 2)
+    T, H = x.shape
+    E, I2, H2 = w13.shape
+    I = I2 // 2
+    K = topk_ids.shape[1]
+    if H2 != H or w2.shape != (E, H, I) or I2 != 2 * I:
+        raise ValueError("inconsistent x / w13 / w2 shapes")
+    if x_scale.shape != (T,) or w13_scale.shape != (E, I2) or w2_scale.shape != (E, H):
+        raise ValueError("inconsistent scale shapes")
+    if topk_ids.shape != (T, K) or topk_weights.shape != (T, K):
+        raise ValueError("topk_ids / topk_weights must be [T, K]")
+    dev = x.device
+    _same_device(dev, x_scale=x_scale, w13=w13, w13_scale=w13_scale, w2=w2, w2_scale=w2_scale, topk_ids=topk_ids,
+                 topk_weights=topk_weights, workspace=workspace)
+    out = _out(out, (T, H), torch.bfloat16, "out", dev)
+    if workspace is None:
+        workspace = alloc_workspace_int8(T, H, I, E, K, dev)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    with _on(dev):
+        check(lib().moe_fused_int8(_p(x), _p(x_scale), _p(w13), _p(w13_scale), _p(w2), _p(w2_scale), _p(topk_ids),
+                                   _p(topk_weights), T, H, I, E, K, _p(out), _p(workspace), workspace.nbytes, tile_m,
+                                   weight_layout, _stream(dev)))
+    return out
+
+
+def gemm1_swiglu_int8(x, x_scale, w13, w13_scale, route, T, K, align, tile_m=-1, weight_layout=WEIGHTS_ROW_MAJOR,
+                      act=None):
+    """Int8 GEMM1 + SwiGLU stage.  Returns act bf16 [cap, I]; rows of padding are not written (zero
+    when act is allocated here)."""
+    _need(x, torch.int8, "x", 2)
+    _need(x_scale, torch.float32, "x_scale", 1)
+    _need(w13, torch.int8, "w13", 3)
+    _need(w13_scale, torch.float32, "w13_scale", 2)
+    E, I2, H = w13.shape
+    I = I2 // 2
+    cap = route["sorted_src"].numel()
+    dev = x.device
+    if x.shape != (T, H) or x_scale.shape != (T,) or w13_scale.shape != (E, I2) or I2 != 2 * I:
+        raise ValueError("inconsistent x / w13 / scale shapes")
+    _same_device(dev, x_scale=x_scale, w13=w13, w13_scale=w13_scale, route=route["sorted_src"])
+    act = torch.zeros((cap, I), dtype=torch.bfloat16, device=dev) if act is None else act
+    act = _out(act, (cap, I), torch.bfloat16, "act", dev)
+    with _on(dev):
+        check(lib().moe_gemm1_swiglu_int8(_p(x), _p(x_scale), _p(w13), _p(w13_scale), _p(route["padded_indptr"]),
+                                          _p(route["sorted_src"]), T, H, I, E, K, align, _p(act), cap, tile_m,
+                                          weight_layout, _stream(dev)))
+    return act
+
+
+def quant_rows_int8(x, q=None, scale=None, route=None):
+    """bf16 [rows, N] -> (int8 codes [rows, N], fp32 scale [rows]), one scale per row.  route given:
+    rows of padding are not written."""
+    _need(x, torch.bfloat16, "x", 2)
+    rows, N = x.shape
+    dev = x.device
+    src = None if route is None else route["sorted_src"]
+    if src is not None and src.numel() != rows:
+        raise ValueError("route and x disagree on the rows")
+    _same_device(dev, route=src)
+    if route is not None:      # the rows that are not written
+        q = torch.zeros((rows, N), dtype=torch.int8, device=dev) if q is None else q
+        scale = torch.zeros(rows, dtype=torch.float32, device=dev) if scale is None else scale
+    q = _out(q, (rows, N), torch.int8, "q", dev)
+    scale = _out(scale, (rows,), torch.float32, "scale", dev)
+    with _on(dev):
+        check(lib().moe_quant_rows_int8(_p(x), _p(src), rows, N, _p(q), _p(scale), _stream(dev)))
+    return q, scale
+
+
+def gemm2_weighted_int8(q, q_scale, w2, w2_scale, route, topk_weights, T, K, align, tile_m=-1,
+                        weight_layout=WEIGHTS_ROW_MAJOR, Y=None):
+    """Int8 GEMM2 + routing-weight stage.  Returns Y bf16 [T*K, H]; rows of dropped slots are not
+    written (zero when Y is allocated here)."""
+    _need(q, torch.int8, "q", 2)
+    _need(q_scale, torch.float32, "q_scale", 1)
+    _need(w2, torch.int8, "w2", 3)
+    _need(w2_scale, torch.float32, "w2_scale", 2)
+    _need(topk_weights, torch.float32, "topk_weights", 2)
+    E, H, I = w2.shape
+    cap = route["sorted_src"].numel()
+    dev = q.device
+    if q.shape != (cap, I) or q_scale.shape != (cap,) or w2_scale.shape != (E, H) or topk_weights.shape != (T, K):
+        raise ValueError("inconsistent q / w2 / scale / topk_weights shapes")
+    _same_device(dev, q_scale=q_scale, w2=w2, w2_scale=w2_scale, route=route["sorted_src"],
+                 topk_weights=topk_weights)
+    Y = torch.zeros((T * K, H), dtype=torch.bfloat16, device=dev) if Y is None else Y
+    Y = _out(Y, (T * K, H), torch.bfloat16, "Y", dev)
+    with _on(dev):
+        check(lib().moe_gemm2_weighted_int8(_p(q), _p(q_scale), _p(w2), _p(w2_scale), _p(route["padded_indptr"]),
+                                            _p(route["sorted_src"]), _p(topk_weights), T, H, I, E, K, align, _p(Y),
+                                            cap, tile_m, weight_layout, _stream(dev)))
+    return Y
+
+
 def combine(Y, topk_ids, E):
     T, K = topk_ids.shape
     H = Y.shape[1]
@@ -589,6 +738,83 @@ def gated_act_fp8_quant(x, variant=-1, out=None, scale=None):
         scale = torch.empty((M, max(N // 32, 0)), dtype=torch.uint8, device=dev)
     check(lib().gated_act_fp8_quant(_p(x), M, N, _p(out), _p(scale), variant, _stream(dev)))
     return out, scale
+
+
+# ---------------------------------------------------------------- residual addition, RMS norm, quantisation
+
+NORM_BF16, NORM_FP8, NORM_MXFP8, NORM_INT8 = 0, 1, 2, 3
+
+
+def add_rmsnorm_quant(x, weight, eps, format, residual=None, want_norm=False, q=None, scale=None, norm_out=None,
+                      residual_out=None):
+    """v = x + residual, n = v * weight / sqrt(mean(v^2) + eps) per row of x bf16 [T, H], and n quantised
+    as one of the layer's formats takes its activations: NORM_FP8 (uint8 codes, fp32 scales per 128
+    columns), NORM_MXFP8 (uint8 codes, E8M0 scales per 32), NORM_INT8 (int8 codes, fp32 scale per
+    row), or NORM_BF16 (no codes).  residual and weight are bf16 or fp32.
+    Returns (q, scale, norm, v): norm is bf16(n) if want_norm or norm_out is given or the format is
+    NORM_BF16, v the new residual stream if a residual is given; None where there is none.
+    residual_out may be `residual`."""
+    _need(x, torch.bfloat16, "x", 2)
+    T, H = x.shape
+    dev = x.device
+    _need(weight, torch.float32 if weight.dtype == torch.float32 else torch.bfloat16, "weight", 1)
+    if weight.shape != (H,):
+        raise ValueError("weight must be [H]")
+    _same_device(dev, weight=weight, residual=residual)
+    if residual is not None:
+        _need(residual, torch.float32 if residual.dtype == torch.float32 else torch.bfloat16, "residual", 2)
+        if residual.shape != (T, H):
+            raise ValueError("residual must be [T, H]")
+        residual_out = _out(residual_out, (T, H), residual.dtype, "residual_out", dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if want_norm or norm_out is not None or format == NORM_BF16:
+        norm_out = _out(norm_out, (T, H), torch.bfloat16, "norm_out", dev)
+    if format == NORM_FP8:
+        q = _out(q, (T, H), torch.uint8, "q", dev)
+        scale = _out(scale, (T, H // 128), torch.float32, "scale", dev)
+    elif format == NORM_MXFP8:
+        q = _out(q, (T, H), torch.uint8, "q", dev)
+        scale = _out(scale, (T, H // 32), torch.uint8, "scale", dev)
+    elif format == NORM_INT8:
+        q = _out(q, (T, H), torch.int8, "q", dev)
+        scale = _out(scale, (T,), torch.float32, "scale", dev)
+    elif q is not None or scale is not None:
+        raise ValueError("NORM_BF16 has no codes")
+    with _on(dev):
+        check(lib().add_rmsnorm_quant(_p(x), _p(residual), int(residual is not None and
+                                                               residual.dtype == torch.float32),
+                                      _p(weight), int(weight.dtype == torch.float32), eps, T, H, format,
+                                      _p(residual_out), _p(norm_out), _p(q), _p(scale), _stream(dev)))
+    return q, scale, norm_out, residual_out
+
+
+# ---------------------------------------------------------------- router
+
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+
+
+def moe_router_topk(logits, K, score=SCORE_SOFTMAX, bias=None, n_group=1, topk_group=1, group_top=1,
+                    renormalize=True, scale=1.0, ids=None, weights=None):
+    """Each token's K experts and their weights from the router's logits [T, E] (fp32 or bf16): scores by
+    softmax or sigmoid, chosen by score + bias (fp32 [E]) among the topk_group best of n_group expert
+    groups, ties to the lower index; weights are the scores, renormalised and scaled (see
+    moe_router_topk in include/fp8moe.h).  Returns (ids int32 [T, K], weights fp32 [T, K])."""
+    _need(logits, torch.bfloat16 if logits.dtype == torch.bfloat16 else torch.float32, "logits", 2)
+    T, E = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _need(bias, torch.float32, "bias", 1)
+        if bias.shape != (E,):
+            raise ValueError("bias must be [E]")
+        _same_device(dev, bias=bias)
+    ids = _out(ids, (T, max(K, 0)), torch.int32, "ids", dev)
+    weights = _out(weights, (T, max(K, 0)), torch.float32, "weights", dev)
+    with _on(dev):
+        check(lib().moe_router_topk(_p(logits), int(logits.dtype == torch.bfloat16), _p(bias), T, E, K, score,
+                                    n_group, topk_group, group_top, int(bool(renormalize)), scale, _p(ids),
+                                    _p(weights), _stream(dev)))
+    return ids, weights
 
 
 # ---------------------------------------------------------------- cost model (host only)

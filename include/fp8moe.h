@@ -53,6 +53,7 @@ extern "C" {
 #define FP8MOE_ERR_HIP         -7  /* a HIP runtime call or kernel launch failed      */
 #define FP8MOE_ERR_LIMIT       -8  /* beyond a library limit (E > FP8MOE_MAX_EXPERTS,
                                       H or I > FP8MOE_MAX_DIM)                        */
+#define FP8MOE_ERR_ARG         -9  /* a flag or number outside its documented values  */
 
 #define FP8MOE_MAX_EXPERTS   1024
 #define FP8MOE_MAX_DIM      16384  /* largest H and I */
@@ -360,6 +361,126 @@ int moe_gemm2_weighted_bf16(const void* q, const void* w2,
                             int64_t T, int32_t H, int32_t I, int32_t E, int32_t K, int32_t align,
                             void* Y, int64_t cap, int32_t tile_m, int32_t tile_n,
                             int32_t weight_layout, void* stream);
+
+/* ---------------------------------------------------------------- residual addition + RMS norm + quantisation
+ * add_rmsnorm_quant: the step ahead of the layer, which makes its activations
+ * and the router's input from the residual stream.  Per token row of H values,
+ * in fp32:
+ *   v = x, or x + residual rounded to the residual's type (residual_out),
+ *   n = v * weight / sqrt(mean(v^2) + eps),
+ *   norm_out = bf16(n), and by `format`
+ *   FP8MOE_NORM_BF16   no codes (norm_out is required)
+ *   FP8MOE_NORM_FP8    s = amax / 448 (1 if zero) per 128 columns, q = e4m3(n / s):
+ *                      x and x_scale of moe_fused_fp8
+ *   FP8MOE_NORM_MXFP8  per 32 columns the smallest e with amax <= 448 * 2^e, clamped
+ *                      to [-127, 127] (-127 for a zero block), q = e4m3(n * 2^-e), code
+ *                      e + 127: x and x_sf of moe_fused_mxfp8
+ *   FP8MOE_NORM_INT8   s = amax / 127 (1 if zero) over the row, q = round(n / s),
+ *                      ties to even: x and x_scale of moe_fused_int8
+ * The codes come from n in fp32, not from norm_out.
+ *
+ *   x            bf16 [T, H]
+ *   residual     bf16 or fp32 (residual_f32 != 0) [T, H], or NULL: then
+ *                residual_out is NULL too
+ *   weight       bf16 or fp32 (weight_f32 != 0) [H]
+ *   eps          finite and > 0
+ *   residual_out [T, H] of the residual's type; may be `residual` itself
+ *   norm_out     bf16 [T, H] or NULL
+ *   q            fp8 / int8 [T, H]
+ *   scale        fp32 [T, H/128] (FP8), uint8 [T, H/32] (MXFP8), fp32 [T] (INT8)
+ * Every pointer is 16-byte aligned (FP8MOE_ERR_ALIGN); no output overlaps an
+ * input or another output, but for residual_out == residual (FP8MOE_ERR_SHAPE).
+ * H is a multiple of 8 (BF16, INT8), 32 (MXFP8) or 128 (FP8), at most
+ * FP8MOE_MAX_DIM; T < 2^24 (FP8MOE_ERR_LIMIT).  T == 0 launches nothing.
+ * A row whose v holds an infinity or NaN gives NaN: norm_out, e4m3 codes 0x7F,
+ * scale NaN (E8M0 code 255), int8 codes 0.  So does a block (INT8: a row) whose
+ * n does, its norm_out apart.  Squares beyond fp32's range do no harm.
+ */
+#define FP8MOE_NORM_BF16  0
+#define FP8MOE_NORM_FP8   1
+#define FP8MOE_NORM_MXFP8 2
+#define FP8MOE_NORM_INT8  3
+int add_rmsnorm_quant(const void* x, const void* residual, int32_t residual_f32, const void* weight,
+                      int32_t weight_f32, float eps, int64_t T, int32_t H, int32_t format, void* residual_out,
+                      void* norm_out, void* q, void* scale, void* stream);
+
+/* ---------------------------------------------------------------- the router's choice of experts
+ * moe_router_topk: each token's experts and their weights from the router's
+ * logits, as every entry point of the layer takes them.
+ *   score_e  = softmax(logits)_e (FP8MOE_SCORE_SOFTMAX) or 1 / (1 + exp(-logit_e))
+ *              (FP8MOE_SCORE_SIGMOID)
+ *   choice_e = score_e + bias_e with a bias; without one the logits' own order
+ *   groups   (n_group > 1): the E experts are n_group runs of E / n_group; a
+ *            group counts as the sum of its group_top (1 or 2) largest choices
+ *            (scores where there is no bias); only the topk_group largest
+ *            groups' experts are chosen from, equal groups in ascending order
+ *   topk_ids     the K experts of the largest choices, in descending order,
+ *                equal ones in ascending index
+ *   topk_weights score_e (without the bias), divided by the chosen ones' sum if
+ *                renormalize != 0 (0 where that sum is 0), times scale
+ * Which experts are chosen is decided as if in 64 bits; weights are rounded to
+ * fp32 once.
+ *
+ *   logits  fp32 or bf16 (logits_bf16 != 0) [T, E]
+ *   bias    fp32 [E] or NULL
+ *   topk_ids int32 [T, K], topk_weights fp32 [T, K]   (all written)
+ * An expert whose logit is NaN or -inf, or whose biased choice is NaN or -inf,
+ * is never chosen, counts as -inf in its group and as 0 in the softmax's sum;
+ * logits of +inf share the softmax equally.  Slots that no expert is left for
+ * hold id -1 (a dropped slot of the layer) and weight 0.
+ * Limits: 1 <= E <= FP8MOE_MAX_EXPERTS; 1 <= K <= min(FP8MOE_MAX_ROUTER_TOPK,
+ * topk_group * E / n_group) (FP8MOE_ERR_TOPK); n_group divides E and is at most
+ * FP8MOE_MAX_ROUTER_GROUPS, 1 <= topk_group <= n_group, group_top at most
+ * E / n_group (FP8MOE_ERR_ARG); T < 2^26 (FP8MOE_ERR_LIMIT); scale finite.  With
+ * n_group == 1, topk_group is 1 and group_top is 1 or 2 and not used.
+ */
+#define FP8MOE_SCORE_SOFTMAX 0
+#define FP8MOE_SCORE_SIGMOID 1
+#define FP8MOE_MAX_ROUTER_TOPK   64
+#define FP8MOE_MAX_ROUTER_GROUPS 64
+int moe_router_topk(const void* logits, int32_t logits_bf16, const float* bias, int64_t T, int32_t E, int32_t K,
+                    int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top, int32_t renormalize,
+                    float scale, int32_t* topk_ids, float* topk_weights, void* stream);
+
+/* ---------------------------------------------------------------- int8 variant of the layer and its stages
+ * The layer with 8-bit integer operands and one fp32 scale per token and per
+ * output channel:
+ *   x    int8 [T, H]         x_scale   fp32 [T]
+ *   w13  int8 [E, 2I, H]     w13_scale fp32 [E, 2I]   (gate rows first)
+ *   w2   int8 [E, H, I]      w2_scale  fp32 [E, H]
+ * Products are summed exactly in int32 and scaled once, in fp32.  GEMM1 stores
+ * the SwiGLU output rounded to bf16 (act), which moe_quant_rows_int8 quantises
+ * per row: s = amax / 127 (1 if zero), q = round(act / s), ties to even; GEMM2
+ * takes q and s.  A row of act that holds an infinity or NaN gets codes 0 and
+ * scale NaN.
+ *
+ * moe_fused_int8 takes and does what moe_fused_fp8 does, with a workspace of
+ * moe_fused_int8_workspace_size bytes.  The stages follow those of the bf16
+ * layer: act bf16 [cap, I], q int8 [cap, I], q_scale fp32 [cap]; rows of
+ * padding (sorted_src < 0) are not written by any of them.
+ * moe_quant_rows_int8 also serves rows of any bf16 matrix: `in` bf16 [rows, N]
+ * -> q int8 [rows, N], scale fp32 [rows], N a multiple of 8, sorted_src NULL;
+ * no overlap (FP8MOE_ERR_SHAPE).
+ * x, w13, w2, act, in, q, Y and out are 16-byte aligned (FP8MOE_ERR_ALIGN).
+ * tile_m: -1 (auto) or 16, 32, 64: the largest number of token rows per tile.
+ * With FP8MOE_WEIGHTS_MFMA_TILED the weights are packed by moe_pack_weights.
+ * Results do not depend on tile_m or the layout.
+ */
+int moe_fused_int8_workspace_size(int64_t T, int32_t H, int32_t I, int32_t E, int32_t K, size_t* bytes);
+int moe_fused_int8(const void* x, const float* x_scale, const void* w13, const float* w13_scale, const void* w2,
+                   const float* w2_scale, const int32_t* topk_ids, const float* topk_weights, int64_t T, int32_t H,
+                   int32_t I, int32_t E, int32_t K, void* out, void* workspace, size_t workspace_bytes,
+                   int32_t tile_m, int32_t weight_layout, void* stream);
+int moe_gemm1_swiglu_int8(const void* x, const float* x_scale, const void* w13, const float* w13_scale,
+                          const int32_t* padded_indptr, const int32_t* sorted_src, int64_t T, int32_t H, int32_t I,
+                          int32_t E, int32_t K, int32_t align, void* act, int64_t cap, int32_t tile_m,
+                          int32_t weight_layout, void* stream);
+int moe_quant_rows_int8(const void* in, const int32_t* sorted_src, int64_t rows, int32_t N, void* q, float* scale,
+                        void* stream);
+int moe_gemm2_weighted_int8(const void* q, const float* q_scale, const void* w2, const float* w2_scale,
+                            const int32_t* padded_indptr, const int32_t* sorted_src, const float* topk_weights,
+                            int64_t T, int32_t H, int32_t I, int32_t E, int32_t K, int32_t align, void* Y,
+                            int64_t cap, int32_t tile_m, int32_t weight_layout, void* stream);
 
 /* ---------------------------------------------------------------- weight packing
  * moe_pack_weights: expert weights e4m3 [E, N, K] row-major (w13 with N = 2I,
