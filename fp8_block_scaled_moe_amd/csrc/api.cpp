@@ -854,7 +854,7 @@ bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 int int8_tile_m(int requested, int64_t R, int E) {
   if (requested != -1) return requested;
   const int64_t active = R < E ? R : E, rows = active > 0 ? (R + active - 1) / active : 0;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kTileMaxInt8;
 }
 
 int check_int8_stage(int64_t T, int32_t H, int32_t I, int32_t E, int32_t K, int32_t align, int64_t cap,
@@ -863,8 +863,8 @@ int check_int8_stage(int64_t T, int32_t H, int32_t I, int32_t E, int32_t K, int3
   if (st) return st;
   if (!valid_layout(weight_layout)) return fail(FP8MOE_ERR_SHAPE, "weight_layout %d not 0 or 1", weight_layout);
   if (!valid_align(align)) return fail(FP8MOE_ERR_ALIGN, "align %d not in {16,32,64,128}", align);
-  if (tile_m != -1 && tile_m != 16 && tile_m != 32 && tile_m != 64)
-    return fail(FP8MOE_ERR_TILE, "tile_m %d not in {-1,16,32,64}", tile_m);
+  if (tile_m != -1 && tile_m != 16 && tile_m != 32 && tile_m != 64 && tile_m != kTileMaxInt8)
+    return fail(FP8MOE_ERR_TILE, "tile_m %d not in {-1,16,32,64,%d}", tile_m, kTileMaxInt8);
   if (cap < 0 || cap >= kMaxRows) return fail(FP8MOE_ERR_SHAPE, "invalid cap %lld", (long long)cap);
   return FP8MOE_OK;
 }

@@ -19,19 +19,12 @@
 // four waves take every fourth 128-byte K step, load both operands straight
 // into registers in MFMA order, and add their int32 sums in LDS.
 #include "gemm_kernels.h"
+#include "int8_common.h"
 
 namespace fp8moe {
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-
 constexpr int kStreamWaves = 4;
 constexpr int kStreamUnroll = 4;   // K steps whose loads a wave issues together
-
-// One 16x16x64 int8 MFMA on the hf-th 16 bytes of each lane's operands; both
-// operands take the same bytes, so the K order within a step is immaterial.
-__device__ __forceinline__ i32x4 mfma16x16x64_i8(const v4i& a, const v4i& b, const i32x4& c) {
-  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
-}
 
 // acc[ts][w] += rows of token sub-tile ts . weight band w over the wave's K steps
 template <int TS, bool PACKED>
@@ -214,6 +207,11 @@ __global__ __launch_bounds__(64 * kStreamWaves) void gemm2_stream_int8_kernel(
 hipError_t launch_gemm1_int8(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
                              const GroupedRows& g, int H, int I, uint16_t* act, int tile_m, bool packed,
                              hipStream_t stream) {
+  if (tile_m == kTileMaxInt8) {
+    if (g.rows / g.K * H < (int64_t)1 << 32)
+      return launch_gemm1_int8_tile(x, x_scale, w13, w13_scale, g, H, I, act, packed, stream);
+    tile_m = 64;   // the tile kernel's token offsets are 32-bit
+  }
   const dim3 grid(grid_for(g, tile_m, I / 16)), block(64 * kStreamWaves);
 #define FP8MOE_LAUNCH(TM)                                                                                            \
   if (packed)                                                                                                        \
@@ -229,6 +227,8 @@ hipError_t launch_gemm1_int8(const uint8_t* x, const float* x_scale, const uint8
 hipError_t launch_gemm2_int8(const uint8_t* q, const float* q_scale, const uint8_t* w2, const float* w2_scale,
                              const float* topk_weights, const GroupedRows& g, int H, int I, uint16_t* Y, int tile_m,
                              bool packed, hipStream_t stream) {
+  if (tile_m == kTileMaxInt8)
+    return launch_gemm2_int8_tile(q, q_scale, w2, w2_scale, topk_weights, g, H, I, Y, packed, stream);
   const dim3 grid(grid_for(g, tile_m, H / 32)), block(64 * kStreamWaves);
 #define FP8MOE_LAUNCH(TM)                                                                                          \
   if (packed)                                                                                                      \

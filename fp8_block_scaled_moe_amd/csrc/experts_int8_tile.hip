@@ -1,0 +1,373 @@
+// Tile kernels of the experts' int8 products, for experts of many rows: the
+// same results as the streaming kernels of experts_int8.hip.
+//
+// A workgroup of 8 waves owns an M tile of up to 256 tokens and a run of N
+// tiles of 256 weight rows (GEMM1: the gate and up rows of 128 columns).
+// The waves form a WM x 8/WM grid: WM token parts, 8/WM weight parts of 32 WM
+// rows.  With WM = 2 each wave holds 64 weight rows x up to 128 tokens of
+// int32 sums (128 VGPRs), so a 128-byte K step reads each token row from LDS
+// four times and each weight row from L1 twice, under both pipes' share of
+// the step's MFMA time; tiles of up to 64 tokens use WM = 1, which reads
+// weights once.
+//
+// Weights go straight from memory into a register ring two K steps deep, in
+// MFMA order, with no barrier on their path.  Token rows rotate through four
+// LDS buffers, filled by direct-to-LDS loads three K steps ahead; one barrier
+// per K step hands a buffer over.  The fragment reads of a step's first two
+// sub-tiles are issued before the barrier that ends the step ahead of it.
+#include "gemm_kernels.h"
+#include "int8_common.h"
+
+namespace fp8moe {
+
+template <int TM, int WM>
+struct TileCfg {
+  static constexpr int BANDS = 2 * WM;          // 16-row weight bands of a wave
+  static constexpr int TS = TM / 16 / WM;       // token sub-tiles of a wave
+  static constexpr int NBLK = TM * kKB / 1024;  // 1 KB direct-to-LDS loads of a K step
+  static constexpr int APW = (NBLK + kWaves - 1) / kWaves;   // of them by each wave (repeats where 8 APW > NBLK)
+  static_assert(TM % (16 * WM) == 0, "whole sub-tiles");
+  __device__ static int block_of(int wave, int i) { return (wave * APW + i) % NBLK; }
+};
+
+// acc[ts][b] over a run of nn N tiles of KT K steps; band(n, b) is the first
+// weight row of the wave's band b in N tile n, epi(n) takes the sums of N tile
+// n, which are cleared after it.  Runs of more than one N tile need KT % 4 == 0.
+template <int TM, int WM, bool PACKED, typename Band, typename Epi>
+__device__ __forceinline__ void tile_mainloop(const TokenBuffers& tb, __amdgpu_buffer_rsrc_t a_rsrc,
+                                              const uint32_t (&a_off)[TileCfg<TM, WM>::APW],
+                                              __amdgpu_buffer_rsrc_t rsrc, int kdim, int nn, int wave, int lane,
+                                              i32x4 (&acc)[TileCfg<TM, WM>::TS][2 * WM], Band band, Epi epi) {
+  using C = TileCfg<TM, WM>;
+  constexpr int TS = C::TS, B = C::BANDS, APW = C::APW;
+  constexpr int kHalf = PACKED ? 1024 : 64, kStep = PACKED ? 2048 : kKB;
+  const int KT = kdim / kKB, S = nn * KT;
+  const int voff = weight_lane_offset<PACKED>(lane, kdim);
+  const int part = wave / (8 / WM) * TS * 2048;   // the wave's first sub-tile in a token buffer
+  const int o[2] = {swz(lane & 15, lane >> 4) + part, swz(lane & 15, (lane >> 4) + 4) + part};
+  auto frag = [&](int buf, int hf, int ts) __attribute__((always_inline)) -> v4i {
+    return *reinterpret_cast<const v4i*>(tb.b[buf] + o[hf] + 2048 * ts);
+  };
+
+  v4i wr[2][2][B];   // weight ring: slot j % 2 of step j, by half and band
+  int nw = 0, kw = 0;
+  auto load_w = [&](int slot, int hf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      wr[slot][hf][b] =
+          __builtin_amdgcn_raw_buffer_load_b128(rsrc, voff + hf * kHalf, band(nw, b) * kdim + kw * kStep, 0);
+  };
+  // the next step's weights, without a branch; past the run's last step the
+  // ring re-reads the last N tile
+  auto next_w = [&]() __attribute__((always_inline)) {
+    const bool end = ++kw == KT;
+    kw = end ? 0 : kw;
+    nw = end && nw + 1 < nn ? nw + 1 : nw;
+  };
+  int ka = 0;
+  auto dma_a = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < APW; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          a_rsrc, (__attribute__((address_space(3))) void*)(tb.b[buf] + C::block_of(wave, i) * 1024), 16, a_off[i],
+          ka * kKB, 0, 0);
+    ++ka;
+    ka = ka == KT ? 0 : ka;   // past the last step: valid rows that nothing reads
+  };
+
+  // Number u = 0 .. 2 TS - 1 of a step is half u / TS, sub-tile u % TS; its
+  // fragment is read two ahead.  Slots go by the sub-tile's number within the
+  // round of four steps, 8 TS of them, so all are constants.
+  constexpr int U = 2 * TS;
+  v4i af[4];
+  auto step = [&](int s, bool tail) __attribute__((always_inline)) {
+    dma_a((s + 3) & 3);                  // last read at the step before this one
+    __builtin_amdgcn_sched_barrier(0);   // the publish wait counts on these being the step's oldest
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = u + 2;
+      af[(s * U + v) & 3] = v < U ? frag(s, v / TS, v % TS) : frag((s + 1) & 3, (v - U) / TS, (v - U) % TS);
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+        acc[u % TS][b] = mfma16x16x64_i8(wr[s & 1][u / TS][b], af[(s * U + u) & 3], acc[u % TS][b]);
+      if (u == TS - 1) load_w(s & 1, 0);
+      if (u == U - 1) load_w(s & 1, 1);
+      // one fragment read per B MFMAs, in this order: left alone, the
+      // scheduler moves the products apart and spills their sums
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    next_w();
+    // the token loads of the step before this one have landed: younger are
+    // that step's 2 B weight loads and this step's APW + 2 B
+    // (in the tail the compiler drops weight loads that nothing uses)
+    if (tail) vmcnt_wait<0>();
+    else vmcnt_wait<4 * B + APW>();
+    step_barrier();
+  };
+
+  dma_a(0);
+  dma_a(1);
+  dma_a(2);
+  __builtin_amdgcn_sched_barrier(0);   // the wait below counts on the weight loads being younger
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    load_w(s, 0);
+    load_w(s, 1);
+    next_w();
+  }
+  vmcnt_wait<APW + 4 * B>();   // rows of steps 0 and 1
+  __syncthreads();
+  af[0] = frag(0, 0, 0);
+  af[1] = frag(0, 1 / TS, 1 % TS);
+
+  int k = 0, n = 0;
+  const int full = S - S % 4;
+  for (int j = 0; j < full; j += 4) {
+    step(0, false);
+    step(1, false);
+    step(2, false);
+    step(3, false);
+    k += 4;
+    if (k == KT) {
+      epi(n, acc);
+#pragma unroll
+      for (int ts = 0; ts < TS; ++ts)
+#pragma unroll
+        for (int b = 0; b < B; ++b) acc[ts][b] = i32x4{0, 0, 0, 0};
+      k = 0;
+      ++n;
+    }
+  }
+  if (full < S) {   // a run of one N tile
+    step(0, true);
+    if (full + 1 < S) step(1, true);
+    if (full + 2 < S) step(2, true);
+    epi(n, acc);
+  }
+  vmcnt_wait<0>();   // the look-ahead loads into LDS land before it is released
+}
+
+// What the epilogues need of the tile's rows, in LDS.
+struct RowInfo {
+  int src[256];       // source row, -1 for padding
+  float scale[256];   // x_scale of the token, or q_scale of the row
+  float weight[256];  // GEMM2: the slot's top-k weight
+};
+
+template <int TM, int WM, bool PACKED>
+__device__ __forceinline__ void tile_gemm1(const TokenBuffers& tb, RowInfo& ri, const TileCoord& tc,
+                                           const uint8_t* __restrict__ x, const float* __restrict__ x_scale,
+                                           const uint8_t* __restrict__ w13, const float* __restrict__ w13_scale,
+                                           const int32_t* __restrict__ sorted_src, int K, int H, int I, int NB,
+                                           uint32_t x_bytes, uint16_t* __restrict__ act) {
+  using C = TileCfg<TM, WM>;
+  constexpr int TS = C::TS, B = C::BANDS;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, l16 = lane & 15;
+  const int wm = wave / (8 / WM), wn = wave % (8 / WM);
+  const int NT = I / 128, nt0 = tc.run * NB, nn = min(NB, NT - nt0);
+  uint32_t a_off[C::APW];
+#pragma unroll
+  for (int i = 0; i < C::APW; ++i) {
+    const int qc = C::block_of(wave, i) * 64 + lane;
+    const int r = qc >> 3, c = (qc & 7) ^ swz_key(r);
+    const int src = r < tc.h ? sorted_src[tc.p0 + r] : -1;
+    a_off[i] = (uint32_t)(src >= 0 ? src / K : 0) * (uint32_t)H + c * 16;   // a pad row reads token 0, never stored
+  }
+  if (threadIdx.x < TM) {
+    const int r = threadIdx.x;
+    const int src = r < tc.h ? sorted_src[tc.p0 + r] : -1;
+    ri.src[r] = src;
+    ri.scale[r] = src >= 0 ? x_scale[src / K] : 0.f;
+  }
+  const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(w13 + (size_t)tc.e * 2 * I * H), (short)0, 2 * I * H, kWeightRsrcFlags);
+  const __amdgpu_buffer_rsrc_t xrsrc =
+      __builtin_amdgcn_make_buffer_rsrc((void*)x, (short)0, (int)x_bytes, kWeightRsrcFlags);
+  // bands 0 .. WM-1 are gate rows, WM .. 2 WM - 1 the same columns' up rows
+  auto band = [&](int n, int b) __attribute__((always_inline)) -> int {
+    return (b >= WM ? I : 0) + 128 * (nt0 + n) + 16 * WM * wn + 16 * (b % WM);
+  };
+  const float* sexp = w13_scale + (size_t)tc.e * 2 * I;
+  auto epi = [&](int n, i32x4 (&acc)[TS][B]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < WM; ++b) {
+      const int c = 128 * (nt0 + n) + 16 * WM * wn + 16 * b + 4 * g;
+      const v4f wg = *reinterpret_cast<const v4f*>(sexp + c), wu = *reinterpret_cast<const v4f*>(sexp + I + c);
+#pragma unroll
+      for (int ts = 0; ts < TS; ++ts) {
+        const int r = 16 * (wm * TS + ts) + l16;
+        if (ri.src[r] < 0) continue;
+        const float xs = ri.scale[r];
+        float a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          a[i] = silu_mul((float)acc[ts][b][i] * (xs * wg[i]), (float)acc[ts][b + WM][i] * (xs * wu[i]));
+        *reinterpret_cast<uint2*>(act + (size_t)(tc.p0 + r) * I + c) =
+            uint2{pack2_bf16(a[0], a[1]), pack2_bf16(a[2], a[3])};
+      }
+    }
+  };
+  i32x4 acc[TS][B];
+#pragma unroll
+  for (int ts = 0; ts < TS; ++ts)
+#pragma unroll
+    for (int b = 0; b < B; ++b) acc[ts][b] = i32x4{0, 0, 0, 0};
+  tile_mainloop<TM, WM, PACKED>(tb, xrsrc, a_off, rsrc, H, nn, wave, lane, acc, band, epi);
+}
+
+template <int TM, int WM, bool PACKED>
+__device__ __forceinline__ void tile_gemm2(const TokenBuffers& tb, RowInfo& ri, const TileCoord& tc,
+                                           const uint8_t* __restrict__ q, const float* __restrict__ q_scale,
+                                           const uint8_t* __restrict__ w2, const float* __restrict__ w2_scale,
+                                           const float* __restrict__ topk_weights,
+                                           const int32_t* __restrict__ sorted_src, int H, int I, int NB,
+                                           uint16_t* __restrict__ Y) {
+  using C = TileCfg<TM, WM>;
+  constexpr int TS = C::TS, B = C::BANDS;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, l16 = lane & 15;
+  const int wm = wave / (8 / WM), wn = wave % (8 / WM);
+  const int NT = (H + kTN - 1) / kTN, nt0 = tc.run * NB, nn = min(NB, NT - nt0);
+  uint32_t a_off[C::APW];
+#pragma unroll
+  for (int i = 0; i < C::APW; ++i) {
+    const int qc = C::block_of(wave, i) * 64 + lane;
+    const int r = qc >> 3, c = (qc & 7) ^ swz_key(r);
+    a_off[i] = (uint32_t)min(r, tc.h - 1) * (uint32_t)I + c * 16;   // rows past the segment re-read its last
+  }
+  if (threadIdx.x < TM) {
+    const int r = threadIdx.x;
+    const int src = r < tc.h ? sorted_src[tc.p0 + r] : -1;
+    ri.src[r] = src;
+    ri.scale[r] = src >= 0 ? q_scale[tc.p0 + r] : 0.f;
+    ri.weight[r] = src >= 0 ? topk_weights[src] : 0.f;
+  }
+  const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(w2 + (size_t)tc.e * H * I), (short)0, H * I, kWeightRsrcFlags);
+  const __amdgpu_buffer_rsrc_t qrsrc = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(q + (size_t)tc.p0 * I), (short)0, tc.h * I, kWeightRsrcFlags);
+  auto band = [&](int n, int b) __attribute__((always_inline)) -> int {
+    // bands past H (the last N tile when H % 256 == 128) read the last band
+    return min(kTN * (nt0 + n) + 32 * WM * wn + 16 * b, H - 16);
+  };
+  const float* sexp = w2_scale + (size_t)tc.e * H;
+  auto epi = [&](int n, i32x4 (&acc)[TS][B]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int c = kTN * (nt0 + n) + 32 * WM * wn + 16 * b + 4 * g;
+      if (c >= H) continue;
+      const v4f ws = *reinterpret_cast<const v4f*>(sexp + c);
+#pragma unroll
+      for (int ts = 0; ts < TS; ++ts) {
+        const int r = 16 * (wm * TS + ts) + l16;
+        const int src = ri.src[r];
+        if (src < 0) continue;
+        const float qs = ri.scale[r], tw = ri.weight[r];
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = tw * ((float)acc[ts][b][i] * (qs * ws[i]));
+        *reinterpret_cast<uint2*>(Y + (size_t)src * H + c) = uint2{pack2_bf16(y[0], y[1]), pack2_bf16(y[2], y[3])};
+      }
+    }
+  };
+  i32x4 acc[TS][B];
+#pragma unroll
+  for (int ts = 0; ts < TS; ++ts)
+#pragma unroll
+    for (int b = 0; b < B; ++b) acc[ts][b] = i32x4{0, 0, 0, 0};
+  tile_mainloop<TM, WM, PACKED>(tb, qrsrc, a_off, rsrc, I, nn, wave, lane, acc, band, epi);
+}
+
+// one uniform branch per workgroup on its tile height, in steps of 32 rows
+#define FP8MOE_TILE_BODIES(BODY)       \
+  switch ((tc.tm + 31) / 32) {         \
+    case 1: BODY(32, 1); break;        \
+    case 2: BODY(64, 1); break;        \
+    case 3: BODY(96, 2); break;        \
+    case 4: BODY(128, 2); break;       \
+    case 5: BODY(160, 2); break;       \
+    case 6: BODY(192, 2); break;       \
+    case 7: BODY(224, 2); break;       \
+    default: BODY(256, 2); break;      \
+  }
+
+template <bool PACKED>
+__global__ __launch_bounds__(kThreads) void gemm1_tile_int8_kernel(
+    const uint8_t* __restrict__ x, const float* __restrict__ x_scale, const uint8_t* __restrict__ w13,
+    const float* __restrict__ w13_scale, const int32_t* __restrict__ padded, const int32_t* __restrict__ sorted_src,
+    int E, int K, int H, int I, int NB, uint32_t x_bytes, uint16_t* __restrict__ act) {
+  __shared__ __attribute__((aligned(1024))) uint8_t tb0[kTileMaxInt8 * kKB], tb1[kTileMaxInt8 * kKB],
+      tb2[kTileMaxInt8 * kKB], tb3[kTileMaxInt8 * kKB];
+  __shared__ RowInfo ri;
+  const TokenBuffers tb{{tb0, tb1, tb2, tb3}};
+  const int NT = I / 128;
+  TileCoord tc;
+  if (!tile_coord<kTileMaxInt8>(padded, sorted_src, E, (NT + NB - 1) / NB, tc)) return;
+#define FP8MOE_BODY(TM, WM) \
+  tile_gemm1<TM, WM, PACKED>(tb, ri, tc, x, x_scale, w13, w13_scale, sorted_src, K, H, I, NB, x_bytes, act)
+  FP8MOE_TILE_BODIES(FP8MOE_BODY)
+#undef FP8MOE_BODY
+}
+
+template <bool PACKED>
+__global__ __launch_bounds__(kThreads) void gemm2_tile_int8_kernel(
+    const uint8_t* __restrict__ q, const float* __restrict__ q_scale, const uint8_t* __restrict__ w2,
+    const float* __restrict__ w2_scale, const float* __restrict__ topk_weights, const int32_t* __restrict__ padded,
+    const int32_t* __restrict__ sorted_src, int E, int H, int I, int NB, uint16_t* __restrict__ Y) {
+  __shared__ __attribute__((aligned(1024))) uint8_t tb0[kTileMaxInt8 * kKB], tb1[kTileMaxInt8 * kKB],
+      tb2[kTileMaxInt8 * kKB], tb3[kTileMaxInt8 * kKB];
+  __shared__ RowInfo ri;
+  const TokenBuffers tb{{tb0, tb1, tb2, tb3}};
+  const int NT = (H + kTN - 1) / kTN;
+  TileCoord tc;
+  if (!tile_coord<kTileMaxInt8>(padded, sorted_src, E, (NT + NB - 1) / NB, tc)) return;
+#define FP8MOE_BODY(TM, WM) \
+  tile_gemm2<TM, WM, PACKED>(tb, ri, tc, q, q_scale, w2, w2_scale, topk_weights, sorted_src, H, I, NB, Y)
+  FP8MOE_TILE_BODIES(FP8MOE_BODY)
+#undef FP8MOE_BODY
+}
+
+// N tiles of a workgroup's run: as long as the launch keeps about two
+// workgroups per CU.
+static int run_int8(const GroupedRows& g, int NT, int KT) {
+  if (KT % 4) return 1;   // N tiles of a run end on whole rounds of the token buffers
+  const int64_t cu = g.num_cu > 0 ? g.num_cu : 256;
+  const int64_t mt = g.rows / kTileMaxInt8 + (g.E < g.rows ? g.E : g.rows);
+  int64_t nb = mt * NT / (2 * cu);
+  nb = nb < 1 ? 1 : nb > NT ? NT : nb;
+  const int64_t ng = (NT + nb - 1) / nb;
+  return (int)((NT + ng - 1) / ng);   // runs of equal length
+}
+
+hipError_t launch_gemm1_int8_tile(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
+                                  const GroupedRows& g, int H, int I, uint16_t* act, bool packed,
+                                  hipStream_t stream) {
+  if (g.rows / g.K * H >= (int64_t)1 << 32) return hipErrorInvalidValue;   // x: 32-bit offsets of its rows
+  const uint32_t x_bytes = (uint32_t)(g.rows / g.K * H);
+  const int NT = I / 128, NB = run_int8(g, NT, H / kKB), NG = (NT + NB - 1) / NB;
+  const dim3 grid(grid_for(g, kTileMaxInt8, NG)), block(kThreads);
+  if (packed)
+    hipLaunchKernelGGL((gemm1_tile_int8_kernel<true>), grid, block, 0, stream, x, x_scale, w13, w13_scale,
+                       g.padded_indptr, g.sorted_src, g.E, g.K, H, I, NB, x_bytes, act);
+  else
+    hipLaunchKernelGGL((gemm1_tile_int8_kernel<false>), grid, block, 0, stream, x, x_scale, w13, w13_scale,
+                       g.padded_indptr, g.sorted_src, g.E, g.K, H, I, NB, x_bytes, act);
+  return hipGetLastError();
+}
+
+hipError_t launch_gemm2_int8_tile(const uint8_t* q, const float* q_scale, const uint8_t* w2, const float* w2_scale,
+                                  const float* topk_weights, const GroupedRows& g, int H, int I, uint16_t* Y,
+                                  bool packed, hipStream_t stream) {
+  const int NT = (H + kTN - 1) / kTN, NB = run_int8(g, NT, I / kKB), NG = (NT + NB - 1) / NB;
+  const dim3 grid(grid_for(g, kTileMaxInt8, NG)), block(kThreads);
+  if (packed)
+    hipLaunchKernelGGL((gemm2_tile_int8_kernel<true>), grid, block, 0, stream, q, q_scale, w2, w2_scale,
+                       topk_weights, g.padded_indptr, g.sorted_src, g.E, H, I, NB, Y);
+  else
+    hipLaunchKernelGGL((gemm2_tile_int8_kernel<false>), grid, block, 0, stream, q, q_scale, w2, w2_scale,
+                       topk_weights, g.padded_indptr, g.sorted_src, g.E, H, I, NB, Y);
+  return hipGetLastError();
+}
+
+}  // namespace fp8moe

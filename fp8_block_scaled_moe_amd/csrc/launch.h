@@ -89,7 +89,9 @@ hipError_t launch_gemm2_bf16(const uint16_t* q, const uint16_t* w2, const float*
 // Int8 variants: one scale per token row and per weight row.  GEMM1 writes the
 // SwiGLU output as bf16 (act [cap][I]), launch_quant_rows_int8 quantises its
 // rows (those with sorted_src >= 0; every row if NULL), GEMM2 takes the codes
-// and row scales.  tile_m in {16, 32, 64}.
+// and row scales.  tile_m in {16, 32, 64} (streaming kernels) or kTileMaxInt8
+// (tile kernels).
+constexpr int kTileMaxInt8 = 256;
 hipError_t launch_gemm1_int8(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
                              const GroupedRows& g, int H, int I, uint16_t* act, int tile_m, bool packed,
                              hipStream_t stream);
@@ -98,6 +100,13 @@ hipError_t launch_quant_rows_int8(const uint16_t* in, const int32_t* sorted_src,
 hipError_t launch_gemm2_int8(const uint8_t* q, const float* q_scale, const uint8_t* w2, const float* w2_scale,
                              const float* topk_weights, const GroupedRows& g, int H, int I, uint16_t* Y, int tile_m,
                              bool packed, hipStream_t stream);
+
+// The tile kernels; GEMM1's takes x of less than 4 GiB (hipErrorInvalidValue).
+hipError_t launch_gemm1_int8_tile(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
+                                  const GroupedRows& g, int H, int I, uint16_t* act, bool packed, hipStream_t stream);
+hipError_t launch_gemm2_int8_tile(const uint8_t* q, const float* q_scale, const uint8_t* w2, const float* w2_scale,
+                                  const float* topk_weights, const GroupedRows& g, int H, int I, uint16_t* Y,
+                                  bool packed, hipStream_t stream);
 
 // Residual addition + RMS norm + quantisation (format: FP8MOE_NORM_*), and the
 // router's choice of experts (score: FP8MOE_SCORE_*).
