@@ -147,13 +147,13 @@ __device__ __forceinline__ void stream_gemm2(i32x4* red, const TileCoord& tc, co
   const int r = 16 * wave + l16;
   const int src = r < tc.h ? sorted_src[tc.p0 + r] : -1;
   if (src < 0) return;
-  const float qs = q_scale[tc.p0 + r], tw = topk_weights[src];
+  const float s = q_scale[tc.p0 + r] * topk_weights[src];
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     const float* ws = w2_scale + (size_t)tc.e * H + c0 + 16 * b + 4 * g;
     float y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = tw * ((float)acc[0][b][i] * (qs * ws[i]));
+    for (int i = 0; i < 4; ++i) y[i] = (float)acc[0][b][i] * (s * ws[i]);
     *reinterpret_cast<uint2*>(Y + (size_t)src * H + c0 + 16 * b + 4 * g) =
         uint2{pack2_bf16(y[0], y[1]), pack2_bf16(y[2], y[3])};
   }

@@ -1,11 +1,11 @@
 // Tile kernels of the experts' int8 products, for experts of many rows: the
 // same results as the streaming kernels of experts_int8.hip.
 //
-// A workgroup of 8 waves owns an M tile of up to 256 tokens and a run of N
+// A workgroup of 8 waves owns an M tile of up to 288 tokens and a run of N
 // tiles of 256 weight rows (GEMM1: the gate and up rows of 128 columns).
 // The waves form a WM x 8/WM grid: WM token parts, 8/WM weight parts of 32 WM
-// rows.  With WM = 2 each wave holds 64 weight rows x up to 128 tokens of
-// int32 sums (128 VGPRs), so a 128-byte K step reads each token row from LDS
+// rows.  With WM = 2 each wave holds 64 weight rows x up to 144 tokens of
+// int32 sums (144 VGPRs), so a 128-byte K step reads each token row from LDS
 // four times and each weight row from L1 twice, under both pipes' share of
 // the step's MFMA time; tiles of up to 64 tokens use WM = 1, which reads
 // weights once.
@@ -29,6 +29,14 @@ struct TileCfg {
   static_assert(TM % (16 * WM) == 0, "whole sub-tiles");
   __device__ static int block_of(int wave, int i) { return (wave * APW + i) % NBLK; }
 };
+
+// The lane number, computed afresh: the epilogues' copy takes no register in
+// the main loop, whose largest body has none to spare.
+__device__ __forceinline__ int fresh_lane() {
+  int zero = 0;
+  asm volatile("" : "+s"(zero));
+  return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero));
+}
 
 // acc[ts][b] over a run of nn N tiles of KT K steps; band(n, b) is the first
 // weight row of the wave's band b in N tile n, epi(n) takes the sums of N tile
@@ -55,7 +63,7 @@ __device__ __forceinline__ void tile_mainloop(const TokenBuffers& tb, __amdgpu_b
 #pragma unroll
     for (int b = 0; b < B; ++b)
       wr[slot][hf][b] =
-          __builtin_amdgcn_raw_buffer_load_b128(rsrc, voff + hf * kHalf, band(nw, b) * kdim + kw * kStep, 0);
+          __builtin_amdgcn_raw_buffer_load_b128(rsrc, voff, band(nw, b) * kdim + kw * kStep + hf * kHalf, 0);
   };
   // the next step's weights, without a branch; past the run's last step the
   // ring re-reads the last N tile
@@ -77,19 +85,20 @@ __device__ __forceinline__ void tile_mainloop(const TokenBuffers& tb, __amdgpu_b
 
   // Number u = 0 .. 2 TS - 1 of a step is half u / TS, sub-tile u % TS; its
   // fragment is read two ahead.  Slots go by the sub-tile's number within the
-  // round of four steps, 8 TS of them, so all are constants.
-  constexpr int U = 2 * TS;
-  v4i af[4];
+  // round of four steps, 8 TS of them (a multiple of the slots), so all are
+  // constants.
+  constexpr int U = 2 * TS, AF = 4 * U % 3 == 0 ? 3 : 4;
+  v4i af[AF];
   auto step = [&](int s, bool tail) __attribute__((always_inline)) {
     dma_a((s + 3) & 3);                  // last read at the step before this one
     __builtin_amdgcn_sched_barrier(0);   // the publish wait counts on these being the step's oldest
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int v = u + 2;
-      af[(s * U + v) & 3] = v < U ? frag(s, v / TS, v % TS) : frag((s + 1) & 3, (v - U) / TS, (v - U) % TS);
+      af[(s * U + v) % AF] = v < U ? frag(s, v / TS, v % TS) : frag((s + 1) & 3, (v - U) / TS, (v - U) % TS);
 #pragma unroll
       for (int b = 0; b < B; ++b)
-        acc[u % TS][b] = mfma16x16x64_i8(wr[s & 1][u / TS][b], af[(s * U + u) & 3], acc[u % TS][b]);
+        acc[u % TS][b] = mfma16x16x64_i8(wr[s & 1][u / TS][b], af[(s * U + u) % AF], acc[u % TS][b]);
       if (u == TS - 1) load_w(s & 1, 0);
       if (u == U - 1) load_w(s & 1, 1);
       // one fragment read per B MFMAs, in this order: left alone, the
@@ -149,10 +158,30 @@ __device__ __forceinline__ void tile_mainloop(const TokenBuffers& tb, __amdgpu_b
 
 // What the epilogues need of the tile's rows, in LDS.
 struct RowInfo {
-  int src[256];       // source row, -1 for padding
-  float scale[256];   // x_scale of the token, or q_scale of the row
-  float weight[256];  // GEMM2: the slot's top-k weight
+  int src[kTileMaxInt8];       // source row, -1 for padding
+  float scale[kTileMaxInt8];   // x_scale of the token, or q_scale of the row times the slot's top-k weight
 };
+
+// Lane group g (of 4) holds columns 16 b + 4 g .. + 3 of its row in v[b].  For
+// each pair of bands, groups g and g ^ 1 swap halves: an even group keeps band
+// b and takes its partner's columns of it, an odd one keeps band b + 1, so
+// each lane stores 8 consecutive columns with one 16-byte store instead of two
+// of 8 bytes.  row points at the first of the bands' columns.
+template <int NB>
+__device__ __forceinline__ void store_row(const uint2 (&v)[NB], uint16_t* row, int g, bool live) {
+  if constexpr (NB == 1) {
+    if (live) *reinterpret_cast<uint2*>(row + 4 * g) = v[0];
+  } else {
+    const bool odd = g & 1;
+#pragma unroll
+    for (int b = 0; b < NB; b += 2) {
+      const uint32_t r0 = swap_lane16(odd ? v[b].x : v[b + 1].x), r1 = swap_lane16(odd ? v[b].y : v[b + 1].y);
+      if (live)
+        *reinterpret_cast<uint4*>(row + 16 * b + (odd ? 16 + 4 * (g - 1) : 4 * g)) =
+            odd ? uint4{r0, r1, v[b + 1].x, v[b + 1].y} : uint4{v[b].x, v[b].y, r0, r1};
+    }
+  }
+}
 
 template <int TM, int WM, bool PACKED>
 __device__ __forceinline__ void tile_gemm1(const TokenBuffers& tb, RowInfo& ri, const TileCoord& tc,
@@ -163,7 +192,6 @@ __device__ __forceinline__ void tile_gemm1(const TokenBuffers& tb, RowInfo& ri, 
   using C = TileCfg<TM, WM>;
   constexpr int TS = C::TS, B = C::BANDS;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int g = lane >> 4, l16 = lane & 15;
   const int wm = wave / (8 / WM), wn = wave % (8 / WM);
   const int NT = I / 128, nt0 = tc.run * NB, nn = min(NB, NT - nt0);
   uint32_t a_off[C::APW];
@@ -190,22 +218,29 @@ __device__ __forceinline__ void tile_gemm1(const TokenBuffers& tb, RowInfo& ri, 
   };
   const float* sexp = w13_scale + (size_t)tc.e * 2 * I;
   auto epi = [&](int n, i32x4 (&acc)[TS][B]) __attribute__((always_inline)) {
+    const int el = fresh_lane(), g = el >> 4, l16 = el & 15;
+    const int c0 = 128 * (nt0 + n) + 16 * WM * wn;
+    v4f wg[WM], wu[WM];
 #pragma unroll
     for (int b = 0; b < WM; ++b) {
-      const int c = 128 * (nt0 + n) + 16 * WM * wn + 16 * b + 4 * g;
-      const v4f wg = *reinterpret_cast<const v4f*>(sexp + c), wu = *reinterpret_cast<const v4f*>(sexp + I + c);
+      wg[b] = *reinterpret_cast<const v4f*>(sexp + c0 + 16 * b + 4 * g);
+      wu[b] = *reinterpret_cast<const v4f*>(sexp + I + c0 + 16 * b + 4 * g);
+    }
 #pragma unroll
-      for (int ts = 0; ts < TS; ++ts) {
-        const int r = 16 * (wm * TS + ts) + l16;
-        if (ri.src[r] < 0) continue;
-        const float xs = ri.scale[r];
+    for (int ts = 0; ts < TS; ++ts) {
+      const int r = 16 * (wm * TS + ts) + l16;
+      const float xs = ri.scale[r];
+      const bool live = ri.src[r] >= 0;
+      uint2 v[WM];
+#pragma unroll
+      for (int b = 0; b < WM; ++b) {
         float a[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          a[i] = silu_mul((float)acc[ts][b][i] * (xs * wg[i]), (float)acc[ts][b + WM][i] * (xs * wu[i]));
-        *reinterpret_cast<uint2*>(act + (size_t)(tc.p0 + r) * I + c) =
-            uint2{pack2_bf16(a[0], a[1]), pack2_bf16(a[2], a[3])};
+          a[i] = silu_mul((float)acc[ts][b][i] * (xs * wg[b][i]), (float)acc[ts][b + WM][i] * (xs * wu[b][i]));
+        v[b] = uint2{pack2_bf16(a[0], a[1]), pack2_bf16(a[2], a[3])};
       }
+      store_row<WM>(v, act + (size_t)(tc.p0 + r) * I + c0, g, live);
     }
   };
   i32x4 acc[TS][B];
@@ -226,7 +261,6 @@ __device__ __forceinline__ void tile_gemm2(const TokenBuffers& tb, RowInfo& ri, 
   using C = TileCfg<TM, WM>;
   constexpr int TS = C::TS, B = C::BANDS;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int g = lane >> 4, l16 = lane & 15;
   const int wm = wave / (8 / WM), wn = wave % (8 / WM);
   const int NT = (H + kTN - 1) / kTN, nt0 = tc.run * NB, nn = min(NB, NT - nt0);
   uint32_t a_off[C::APW];
@@ -240,8 +274,7 @@ __device__ __forceinline__ void tile_gemm2(const TokenBuffers& tb, RowInfo& ri, 
     const int r = threadIdx.x;
     const int src = r < tc.h ? sorted_src[tc.p0 + r] : -1;
     ri.src[r] = src;
-    ri.scale[r] = src >= 0 ? q_scale[tc.p0 + r] : 0.f;
-    ri.weight[r] = src >= 0 ? topk_weights[src] : 0.f;
+    ri.scale[r] = src >= 0 ? q_scale[tc.p0 + r] * topk_weights[src] : 0.f;
   }
   const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
       (void*)(w2 + (size_t)tc.e * H * I), (short)0, H * I, kWeightRsrcFlags);
@@ -253,22 +286,26 @@ __device__ __forceinline__ void tile_gemm2(const TokenBuffers& tb, RowInfo& ri, 
   };
   const float* sexp = w2_scale + (size_t)tc.e * H;
   auto epi = [&](int n, i32x4 (&acc)[TS][B]) __attribute__((always_inline)) {
+    const int el = fresh_lane(), g = el >> 4, l16 = el & 15;
+    const int c0 = kTN * (nt0 + n) + 32 * WM * wn;
+    if (c0 >= H) return;   // H is a multiple of 128: the wave's columns lie inside or outside as a whole
+    v4f ws[B];
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const int c = kTN * (nt0 + n) + 32 * WM * wn + 16 * b + 4 * g;
-      if (c >= H) continue;
-      const v4f ws = *reinterpret_cast<const v4f*>(sexp + c);
+    for (int b = 0; b < B; ++b) ws[b] = *reinterpret_cast<const v4f*>(sexp + c0 + 16 * b + 4 * g);
 #pragma unroll
-      for (int ts = 0; ts < TS; ++ts) {
-        const int r = 16 * (wm * TS + ts) + l16;
-        const int src = ri.src[r];
-        if (src < 0) continue;
-        const float qs = ri.scale[r], tw = ri.weight[r];
+    for (int ts = 0; ts < TS; ++ts) {
+      const int r = 16 * (wm * TS + ts) + l16;
+      const int src = ri.src[r];
+      const float s = ri.scale[r];
+      uint2 v[B];
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
         float y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = tw * ((float)acc[ts][b][i] * (qs * ws[i]));
-        *reinterpret_cast<uint2*>(Y + (size_t)src * H + c) = uint2{pack2_bf16(y[0], y[1]), pack2_bf16(y[2], y[3])};
+        for (int i = 0; i < 4; ++i) y[i] = (float)acc[ts][b][i] * (s * ws[b][i]);
+        v[b] = uint2{pack2_bf16(y[0], y[1]), pack2_bf16(y[2], y[3])};
       }
+      store_row<B>(v, Y + (size_t)src * H + c0, g, src >= 0);
     }
   };
   i32x4 acc[TS][B];
@@ -289,7 +326,8 @@ __device__ __forceinline__ void tile_gemm2(const TokenBuffers& tb, RowInfo& ri, 
     case 5: BODY(160, 2); break;       \
     case 6: BODY(192, 2); break;       \
     case 7: BODY(224, 2); break;       \
-    default: BODY(256, 2); break;      \
+    case 8: BODY(256, 2); break;       \
+    default: BODY(288, 2); break;      \
   }
 
 template <bool PACKED>
@@ -328,16 +366,16 @@ __global__ __launch_bounds__(kThreads) void gemm2_tile_int8_kernel(
 #undef FP8MOE_BODY
 }
 
-// N tiles of a workgroup's run: as long as the launch keeps about two
-// workgroups per CU.
+// N tiles of a workgroup's run.  Two pay the tile's prologue once for both;
+// longer ones leave the chip's last round of workgroups uneven and let the
+// workgroups that share token rows drift apart in L2 (T=8192, H=7168, I=2048,
+// E=256, top-8: GEMM1 2.31, 2.28, 2.34, 2.36, 2.97 ms with runs of 1, 2, 4, 8,
+// 16, GEMM2 1.48, 1.43, 1.43, 1.56, 1.66 ms).  One where there are few.
 static int run_int8(const GroupedRows& g, int NT, int KT) {
   if (KT % 4) return 1;   // N tiles of a run end on whole rounds of the token buffers
   const int64_t cu = g.num_cu > 0 ? g.num_cu : 256;
   const int64_t mt = g.rows / kTileMaxInt8 + (g.E < g.rows ? g.E : g.rows);
-  int64_t nb = mt * NT / (2 * cu);
-  nb = nb < 1 ? 1 : nb > NT ? NT : nb;
-  const int64_t ng = (NT + nb - 1) / nb;
-  return (int)((NT + ng - 1) / ng);   // runs of equal length
+  return NT >= 2 && mt * NT >= 4 * cu ? 2 : 1;
 }
 
 hipError_t launch_gemm1_int8_tile(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,

@@ -91,7 +91,7 @@ hipError_t launch_gemm2_bf16(const uint16_t* q, const uint16_t* w2, const float*
 // rows (those with sorted_src >= 0; every row if NULL), GEMM2 takes the codes
 // and row scales.  tile_m in {16, 32, 64} (streaming kernels) or kTileMaxInt8
 // (tile kernels).
-constexpr int kTileMaxInt8 = 256;
+constexpr int kTileMaxInt8 = 288;
 hipError_t launch_gemm1_int8(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
                              const GroupedRows& g, int H, int I, uint16_t* act, int tile_m, bool packed,
                              hipStream_t stream);

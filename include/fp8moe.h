@@ -462,7 +462,7 @@ int moe_router_topk(const void* logits, int32_t logits_bf16, const float* bias, 
  * -> q int8 [rows, N], scale fp32 [rows], N a multiple of 8, sorted_src NULL;
  * no overlap (FP8MOE_ERR_SHAPE).
  * x, w13, w2, act, in, q, Y and out are 16-byte aligned (FP8MOE_ERR_ALIGN).
- * tile_m: -1 (auto) or 16, 32, 64, 256: the largest number of token rows per
+ * tile_m: -1 (auto) or 16, 32, 64, 288: the largest number of token rows per
  * tile.
  * With FP8MOE_WEIGHTS_MFMA_TILED the weights are packed by moe_pack_weights.
  * Results do not depend on tile_m or the layout.

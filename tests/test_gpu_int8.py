@@ -17,7 +17,7 @@ from tests.gpu_helpers import assert_rows_close_to_oracle, say
 
 pytestmark = pytest.mark.gpu
 
-TILES = (16, 32, 64, 256)
+TILES = (16, 32, 64, 288)
 
 
 class Problem:
