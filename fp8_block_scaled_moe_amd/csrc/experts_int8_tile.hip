@@ -366,16 +366,21 @@ __global__ __launch_bounds__(kThreads) void gemm2_tile_int8_kernel(
 #undef FP8MOE_BODY
 }
 
-// N tiles of a workgroup's run.  Two pay the tile's prologue once for both;
-// longer ones leave the chip's last round of workgroups uneven and let the
-// workgroups that share token rows drift apart in L2 (T=8192, H=7168, I=2048,
-// E=256, top-8: GEMM1 2.31, 2.28, 2.34, 2.36, 2.97 ms with runs of 1, 2, 4, 8,
-// 16, GEMM2 1.48, 1.43, 1.43, 1.56, 1.66 ms).  One where there are few.
+// N tiles of a workgroup's run: enough that its prologue serves 32 K steps,
+// fewer where the launch would not fill the chip twice.  Longer runs leave the
+// chip's last round of workgroups uneven and let the workgroups that share
+// token rows drift apart in L2.  Measured with runs of 1, 2, 3, 4 (us): GEMM1
+// of 56 steps 2013, 2039, -, 2041 and GEMM2 of 16 steps 1135, 1100, 1107, 1152
+// (T=8192, H=7168, I=2048, E=256, top-8); GEMM1 of 16 steps 215, 190, 186, 228
+// (T=4096, H=2048, I=768, E=128, top-8, Zipf 1.2).
 static int run_int8(const GroupedRows& g, int NT, int KT) {
   if (KT % 4) return 1;   // N tiles of a run end on whole rounds of the token buffers
   const int64_t cu = g.num_cu > 0 ? g.num_cu : 256;
   const int64_t mt = g.rows / kTileMaxInt8 + (g.E < g.rows ? g.E : g.rows);
-  return NT >= 2 && mt * NT >= 4 * cu ? 2 : 1;
+  int nb = (31 + KT) / KT;
+  if (nb > NT) nb = NT;
+  while (nb > 1 && mt * NT < 2 * cu * nb) nb /= 2;
+  return nb;
 }
 
 hipError_t launch_gemm1_int8_tile(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
