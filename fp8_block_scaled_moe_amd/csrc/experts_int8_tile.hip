@@ -59,11 +59,9 @@ __device__ __forceinline__ void tile_mainloop(const TokenBuffers& tb, __amdgpu_b
 
   v4i wr[2][2][B];   // weight ring: slot j % 2 of step j, by half and band
   int nw = 0, kw = 0;
-  auto load_w = [&](int slot, int hf) __attribute__((always_inline)) {
-#pragma unroll
-    for (int b = 0; b < B; ++b)
-      wr[slot][hf][b] =
-          __builtin_amdgcn_raw_buffer_load_b128(rsrc, voff, band(nw, b) * kdim + kw * kStep + hf * kHalf, 0);
+  auto load_w = [&](int slot, int hf, int b) __attribute__((always_inline)) {
+    wr[slot][hf][b] =
+        __builtin_amdgcn_raw_buffer_load_b128(rsrc, voff, band(nw, b) * kdim + kw * kStep + hf * kHalf, 0);
   };
   // the next step's weights, without a branch; past the run's last step the
   // ring re-reads the last N tile
@@ -73,12 +71,12 @@ __device__ __forceinline__ void tile_mainloop(const TokenBuffers& tb, __amdgpu_b
     nw = end && nw + 1 < nn ? nw + 1 : nw;
   };
   int ka = 0;
-  auto dma_a = [&](int buf) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < APW; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          a_rsrc, (__attribute__((address_space(3))) void*)(tb.b[buf] + C::block_of(wave, i) * 1024), 16, a_off[i],
-          ka * kKB, 0, 0);
+  auto dma_a = [&](int buf, int i) __attribute__((always_inline)) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        a_rsrc, (__attribute__((address_space(3))) void*)(tb.b[buf] + C::block_of(wave, i) * 1024), 16, a_off[i],
+        ka * kKB, 0, 0);
+  };
+  auto next_a = [&]() __attribute__((always_inline)) {
     ++ka;
     ka = ka == KT ? 0 : ka;   // past the last step: valid rows that nothing reads
   };
@@ -89,42 +87,61 @@ __device__ __forceinline__ void tile_mainloop(const TokenBuffers& tb, __amdgpu_b
   // constants.
   constexpr int U = 2 * TS, AF = 4 * U % 3 == 0 ? 3 : 4;
   v4i af[AF];
+  // The loads are spread over the sub-tiles: a wave that meets a full load
+  // queue waits with its products behind it.  The first half of step j issues
+  // the token rows of step j + 3 (into the buffer of step j - 1) and the weights
+  // of step j + 1's second half (into the slot that step j - 1 left), the second
+  // half those of step j + 2's first half.
   auto step = [&](int s, bool tail) __attribute__((always_inline)) {
-    dma_a((s + 3) & 3);                  // last read at the step before this one
-    __builtin_amdgcn_sched_barrier(0);   // the publish wait counts on these being the step's oldest
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int v = u + 2;
       af[(s * U + v) % AF] = v < U ? frag(s, v / TS, v % TS) : frag((s + 1) & 3, (v - U) / TS, (v - U) % TS);
+      if (u < TS) {
+#pragma unroll
+        for (int i = 0; i < APW + B; ++i)
+          if (i * TS / (APW + B) == u) {
+            if (i < APW) dma_a((s + 3) & 3, i);
+            else load_w((s + 1) & 1, 1, i - APW);
+          }
+      } else {
+        if (u == TS) next_w();
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+          if (TS + i * TS / B == u) load_w(s & 1, 0, i);
+      }
 #pragma unroll
       for (int b = 0; b < B; ++b)
         acc[u % TS][b] = mfma16x16x64_i8(wr[s & 1][u / TS][b], af[(s * U + u) % AF], acc[u % TS][b]);
-      if (u == TS - 1) load_w(s & 1, 0);
-      if (u == U - 1) load_w(s & 1, 1);
-      // one fragment read per B MFMAs, in this order: left alone, the
-      // scheduler moves the products apart and spills their sums
+      // one fragment read and at most a few loads per B MFMAs, in this order:
+      // left alone, the scheduler moves the products apart and spills their
+      // sums
       __builtin_amdgcn_sched_barrier(0);
     }
-    next_w();
-    // the token loads of the step before this one have landed: younger are
-    // that step's 2 B weight loads and this step's APW + 2 B
-    // (in the tail the compiler drops weight loads that nothing uses)
+    next_a();
+    // the token loads of the step before this one have landed: younger are at
+    // least that step's last B weight loads and this step's APW + 2 B (in the
+    // tail the compiler drops weight loads that nothing uses)
     if (tail) vmcnt_wait<0>();
-    else vmcnt_wait<4 * B + APW>();
+    else vmcnt_wait<3 * B + APW>();
     step_barrier();
   };
 
-  dma_a(0);
-  dma_a(1);
-  dma_a(2);
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+#pragma unroll
+    for (int i = 0; i < APW; ++i) dma_a(s, i);
+    next_a();
+  }
   __builtin_amdgcn_sched_barrier(0);   // the wait below counts on the weight loads being younger
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    load_w(s, 0);
-    load_w(s, 1);
-    next_w();
-  }
-  vmcnt_wait<APW + 4 * B>();   // rows of steps 0 and 1
+  for (int b = 0; b < B; ++b) load_w(0, 0, b);
+#pragma unroll
+  for (int b = 0; b < B; ++b) load_w(0, 1, b);
+  next_w();
+#pragma unroll
+  for (int b = 0; b < B; ++b) load_w(1, 0, b);
+  vmcnt_wait<APW + 3 * B>();   // rows of steps 0 and 1
   __syncthreads();
   af[0] = frag(0, 0, 0);
   af[1] = frag(0, 1 / TS, 1 % TS);
