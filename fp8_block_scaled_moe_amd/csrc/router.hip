@@ -15,19 +15,63 @@
 // -inf, is never chosen; slots that no expert is left for hold id -1 and
 // weight 0, which the layer treats as dropped.
 //
-// One wave64 owns a token: lane l holds experts l, l + 64, ...  Which expert
-// is chosen hangs on the order of close scores, so choices are compared in 64
-// bits.
+// Which expert is chosen hangs on the order of close scores, and is decided as
+// if in 64 bits.  Two paths give the same answer:
+//
+// Exact path (route_exact): one wave64 per token, every score and choice in
+// fp64.  About 100 64-bit operations per 4 experts; it measured 31 us for 8192
+// tokens of 256 experts in groups, 121 us for 65537 tokens of 128.
+//
+// Fast path (route_fast): L = 16 lanes per token (64 beyond 256 experts or 15
+// slots), lane l holds experts l NV .. l NV + NV - 1, choices in fp32.  Each is
+// a 32-bit key: the order-preserving bits of the choice with the lowest
+// IB replaced by the complement of the expert's index, so keys are unique, the
+// largest key is the winner, and it is taken out by comparing.  The row goes
+// to the exact path where fp32 or the cut bits could have decided wrongly:
+//   * bf16 logits without a bias: 16 value bits and the index fit, always exact;
+//   * fp32 logits without a bias: the chosen set is right unless the K-th and
+//     the next key agree in the kept bits; chosen ones are then put in order by
+//     their full values;
+//   * with a bias, and for groups counted by sums: besides that, neighbours
+//     among the chosen and the next one (kept and left groups) lie further
+//     apart than the error of both.
+// On random logits that is about 1 row in some hundreds.
 #include "device_common.h"
 #include "fp8moe.h"
 #include "launch.h"
 
 namespace fp8moe {
 
-constexpr int kRouterWaves = 4;   // tokens a workgroup
+constexpr int kRouterWaves = 4;   // waves a workgroup
+
+struct RouterArgs {
+  const void* logits;
+  const float* bias;
+  int T, E, K, score, n_group, topk_group, group_top, renormalize;
+  int vec;   // fast path: logits and bias are read in 16-byte vectors
+  float scale;
+  int32_t* ids;
+  float* weights;
+};
 
 __device__ __forceinline__ double shfl_xor_f64(double v, int o) {
   return __hiloint2double(__shfl_xor(__double2hiint(v), o), __shfl_xor(__double2loint(v), o));
+}
+
+constexpr float kRouterInf = __builtin_huge_valf();
+
+template <bool BF16>
+__device__ __forceinline__ float router_logit(const void* logits, int64_t i) {
+  if constexpr (BF16) return bf16_to_f32(static_cast<const uint16_t*>(logits)[i]);
+  else return static_cast<const float*>(logits)[i];
+}
+
+// LDS of a wave is read by its own lanes only: the writes ahead of it have to
+// be in order, which the hardware keeps and this asks of the compiler.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // The largest (key, lowest index on ties) over the wave, in every lane.
@@ -43,27 +87,25 @@ __device__ __forceinline__ void wave_argmax(double& key, int& idx) {
   }
 }
 
+// Token t by one wave: expert lane + 64 i in register i; mine: E doubles of LDS.
 template <int NV, bool BF16>
-__global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(
-    const void* __restrict__ logits, const float* __restrict__ bias, int T, int E, int K, int score, int n_group,
-    int topk_group, int group_top, int renormalize, float scale, int32_t* __restrict__ ids,
-    float* __restrict__ weights) {
-  extern __shared__ double keys_lds[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * kRouterWaves + wave;
-  const bool live = t < T;
+__device__ __noinline__ void route_exact(const RouterArgs& a, int64_t t, int lane, double* mine) {
+  const int E = a.E, K = a.K, score = a.score, n_group = a.n_group, topk_group = a.topk_group,
+            group_top = a.group_top, renormalize = a.renormalize;
+  const float scale = a.scale;
+  const float* bias = a.bias;
+  int32_t* ids = a.ids;
+  float* weights = a.weights;
   const double kNone = -__longlong_as_double(0x7ff0000000000000ll);
 
   float l[NV];
-  float m = -__uint_as_float(0x7f800000u);
+  float m = -kRouterInf;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = lane + 64 * i;
-    l[i] = -__uint_as_float(0x7f800000u);
-    if (live && e < E) {
-      float v;
-      if constexpr (BF16) v = bf16_to_f32(static_cast<const uint16_t*>(logits)[t * E + e]);
-      else v = static_cast<const float*>(logits)[t * E + e];
+    l[i] = -kRouterInf;
+    if (e < E) {
+      const float v = router_logit<BF16>(a.logits, t * E + e);
       if (v == v) l[i] = v;
     }
     m = fmaxf(m, l[i]);
@@ -74,7 +116,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(
   double sc[NV], key[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const bool none = l[i] == -__uint_as_float(0x7f800000u);
+    const bool none = l[i] == -kRouterInf;
     if (score == FP8MOE_SCORE_SOFTMAX) sc[i] = none ? 0.0 : l[i] == m ? 1.0 : exp((double)l[i] - (double)m);
     else sc[i] = none ? 0.0 : 1.0 / (1.0 + exp(-(double)l[i]));
     z += sc[i];
@@ -89,21 +131,21 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(
   for (int i = 0; i < NV; ++i) {
     const int e = lane + 64 * i;
     key[i] = kNone;
-    if (e < E && l[i] != -__uint_as_float(0x7f800000u)) {
+    if (e < E && l[i] != -kRouterInf) {
       const double k = bias ? sc[i] + (double)bias[e] : (double)l[i];
       if (k == k) key[i] = k;
     }
   }
 
   if (n_group > 1) {
-    double* mine = keys_lds + wave * E;
+    wave_lds_fence();   // a row before this one has been read
     const bool by_score = bias == nullptr && group_top > 1;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = lane + 64 * i;
       if (e < E) mine[e] = key[i] == kNone ? kNone : by_score ? sc[i] : key[i];
     }
-    __syncthreads();
+    wave_lds_fence();
     const int G = E / n_group;
     double first = kNone, second = kNone;
     if (lane < n_group) {
@@ -117,7 +159,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(
         }
       }
     }
-    const double total = group_top > 1 ? first + second : first;
+    const double total = group_top > 1 ? (second > kNone ? first + second : kNone) : first;
     bool taken = lane >= n_group;
     uint64_t kept = 0;
     for (int j = 0; j < topk_group; ++j) {
@@ -162,7 +204,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(
       my_w = w;
     }
   }
-  if (live && lane < K) {
+  if (lane < K) {
     double w = my_w;
     if (renormalize) w = sum > 0.0 ? w / sum : 0.0;
     ids[t * K + lane] = my_id;
@@ -170,32 +212,316 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(
   }
 }
 
-template <int NV>
-static void router_launch(const void* logits, bool bf16, const float* bias, int T, int E, int K, int score,
-                          int n_group, int topk_group, int group_top, bool renormalize, float scale, int32_t* ids,
-                          float* weights, hipStream_t stream) {
-  const dim3 grid((unsigned)(((int64_t)T + kRouterWaves - 1) / kRouterWaves)), block(64 * kRouterWaves);
-  const size_t lds = n_group > 1 ? sizeof(double) * kRouterWaves * E : 0;   // at most 32 KB
-  if (bf16)
-    hipLaunchKernelGGL((router_topk_kernel<NV, true>), grid, block, lds, stream, logits, bias, T, E, K, score,
-                       n_group, topk_group, group_top, (int)renormalize, scale, ids, weights);
-  else
-    hipLaunchKernelGGL((router_topk_kernel<NV, false>), grid, block, lds, stream, logits, bias, T, E, K, score,
-                       n_group, topk_group, group_top, (int)renormalize, scale, ids, weights);
+// The largest of v over the row's L lanes, in each of them.
+template <int L>
+__device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, false));   // rotate by 8 of 16
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, false));
+  if constexpr (L == 64) {
+    v = max(v, (uint32_t)__shfl_xor((int)v, 16));
+    v = max(v, (uint32_t)__shfl_xor((int)v, 32));
+  }
+  return v;
+}
+
+// Sum and maximum of floats over the row's L lanes.
+template <int L, bool MAX>
+__device__ __forceinline__ float row_reduce_f32(float v) {
+#pragma unroll
+  for (int o = 1; o < L; o <<= 1) {
+    const float w = __shfl_xor(v, o);
+    v = MAX ? fmaxf(v, w) : v + w;
+  }
+  return v;
+}
+
+// Bits of a float that order as unsigned integers.
+__device__ __forceinline__ uint32_t sortable(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
+// exp(x) for x <= 0 (a few ulp plus |x| 2^-24) and the logistic function on
+// the transcendental units.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
+__device__ __forceinline__ float fast_sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + fast_exp(-x)); }
+
+// The tokens of a wave, 64 / L of them; true in the lanes of a row that the
+// exact path has to decide.
+template <int L, int NV, bool BF16>
+__device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int lane) {
+  constexpr int IB = L * NV <= 256 ? 8 : 10;         // index bits of a key
+  constexpr uint32_t kIdx = (1u << IB) - 1;
+  const int E = a.E, K = a.K;
+  const int rl = lane & (L - 1);                      // lane of the row
+  const bool live = t < a.T;
+  const bool biased = a.bias != nullptr, softmax = a.score == FP8MOE_SCORE_SOFTMAX;
+  const bool sums = a.n_group > 1 && a.group_top > 1 && !biased;   // groups by sums of scores
+  const float kNone = -kRouterInf;
+
+  float x[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) x[i] = kNone;
+  if (live) {
+    if (a.vec) {   // E == L NV
+      const char* src = static_cast<const char*>(a.logits) + (t * E + rl * NV) * (BF16 ? 2 : 4);
+      if constexpr (BF16 && NV % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; i += 8) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src + 2 * i);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[i + 2 * k] = __uint_as_float(w[k] << 16);
+            x[i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+          }
+        }
+      } else if constexpr (BF16) {
+#pragma unroll
+        for (int i = 0; i < NV; i += 4) {
+          const uint2 v = *reinterpret_cast<const uint2*>(src + 2 * i);
+          x[i] = __uint_as_float(v.x << 16);
+          x[i + 1] = __uint_as_float(v.x & 0xffff0000u);
+          x[i + 2] = __uint_as_float(v.y << 16);
+          x[i + 3] = __uint_as_float(v.y & 0xffff0000u);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; i += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src + 4 * i);
+          x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (rl * NV + i < E) x[i] = router_logit<BF16>(a.logits, t * E + rl * NV + i);
+    }
+  }
+  float m = kNone;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    x[i] = x[i] == x[i] ? x[i] : kNone;
+    m = fmaxf(m, x[i]);
+  }
+  // softmax: the row's maximum and sum; scores only where choices need them
+  float z = 1.f;
+  const bool scored = biased || sums;
+  if (softmax) {
+    m = row_reduce_f32<L, true>(m);
+    if (scored || !a.renormalize) {
+      z = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (x[i] > kNone) z += x[i] == m ? 1.f : fast_exp(x[i] - m);
+      z = row_reduce_f32<L, false>(z);
+    }
+  }
+  const float zinv = 1.0f / z;
+  auto score_of = [&](float v) __attribute__((always_inline)) -> float {
+    if (v == kNone) return 0.f;
+    return softmax ? (v == m ? 1.f : fast_exp(v - m)) * zinv : fast_sigmoid(v);
+  };
+
+  // choices: x itself without a bias; groups by sums look at the scores
+  bool unsure = false;
+  float c[NV];
+  if (biased) {
+#pragma unroll
+    for (int i = 0; i < NV; i += 4) {
+      float b[4];
+      if (a.vec) {
+        const float4 v = *reinterpret_cast<const float4*>(a.bias + rl * NV + i);
+        b[0] = v.x; b[1] = v.y; b[2] = v.z; b[3] = v.w;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) b[k] = rl * NV + i + k < E ? a.bias[rl * NV + i + k] : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float v = score_of(x[i + k]) + b[k];
+        c[i + k] = x[i + k] > kNone && v == v ? v : kNone;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) c[i] = x[i];
+  }
+  // Error of a choice, with margin: fp32 scores are within 2^-19 of the exact
+  // ones (a softmax's sum is 16 terms a lane and 6 levels of lanes, 1 + 2 + 22 +
+  // a few roundings of 2^-24; the logistic function is within 2^-22), and the
+  // bias adds half a step.
+  auto choice_tol = [&](float v) __attribute__((always_inline)) -> float { return 0x1p-18f + fabsf(v) * 0x1p-21f; };
+
+  if (a.n_group > 1) {
+    // a group is a whole number (a power of two) of the row's lanes
+    const int gl = E / a.n_group / NV;
+    float first = kNone, second = kNone;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float v = sums ? (c[i] > kNone ? score_of(c[i]) : kNone) : c[i];
+      second = fmaxf(second, fminf(first, v));
+      first = fmaxf(first, v);
+    }
+    for (int o = 1; o < gl; o <<= 1) {
+      const float f2 = __shfl_xor(first, o), s2 = __shfl_xor(second, o);
+      second = fmaxf(fmaxf(second, s2), fminf(first, f2));
+      first = fmaxf(first, f2);
+    }
+    const float total = a.group_top > 1 ? (second > kNone ? first + second : kNone) : first;
+    // rank of the lane's group, and the distance of kept and left groups
+    const int g = rl / gl;
+    int rank = 0;
+    for (int h = 0; h < a.n_group; ++h) {
+      const float other = __shfl(total, (lane & ~(L - 1)) + h * gl);
+      rank += other > total || (other == total && h < g);
+    }
+    const bool keep = rank < a.topk_group;
+    if (biased || sums) {
+      const float worst = -row_reduce_f32<L, true>(keep && rl < a.n_group * gl ? -total : kNone);
+      const float best = row_reduce_f32<L, true>(keep || rl >= a.n_group * gl ? kNone : total);
+      const float tol = biased ? 2.f * choice_tol(fmaxf(fabsf(worst), fabsf(best))) : 0x1p-15f * fabsf(worst);
+      // (sums of scores next to fp32's smallest have no relative bound)
+      if (a.topk_group < a.n_group && best > kNone) unsure = !(worst - best > tol) || (sums && worst < 0x1p-100f);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (!keep) c[i] = kNone;
+  }
+
+  uint32_t key[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)   // + 0: zeros of both signs are equal
+    key[i] = c[i] > kNone ? (sortable(c[i] + 0.f) & ~kIdx) | (kIdx - (uint32_t)(rl * NV + i)) : 0u;
+  const bool cut = !BF16 || biased;   // keys hold a part of the choice: the one behind the last slot is looked at too
+  uint32_t mine = 0;
+  const int rounds = K + (cut ? 1 : 0);
+  for (int j = 0; j < rounds; ++j) {
+    uint32_t w = key[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) w = max(w, key[i]);
+    w = row_max_u32<L>(w);
+    if (rl == j) mine = w;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) key[i] = key[i] == w ? 0u : key[i];
+  }
+  int e = mine ? (int)(kIdx - (mine & kIdx)) : -1;
+  float v = e >= 0 ? router_logit<BF16>(a.logits, t * E + e) : kNone;
+
+  if (cut) {
+    auto right = [&](uint32_t w) __attribute__((always_inline)) -> uint32_t { return (uint32_t)__shfl((int)w, lane + 1); };
+    const uint32_t k2 = right(mine);
+    // the set is right unless the last slot and the next one agree in the kept bits
+    if (rl == K - 1 && k2 && (k2 & ~kIdx) == (mine & ~kIdx)) unsure = true;
+    // slots out of order (equal kept bits): odd-even exchanges until none is
+    float ch = biased ? (e >= 0 ? score_of(v) + a.bias[e] : kNone) : v;
+    for (int pass = 0; pass < K; ++pass) {
+      const float ch2 = __uint_as_float(right(__float_as_uint(ch)));
+      const int e2 = (int)right((uint32_t)e);
+      const bool wrong = rl + 1 < K && e2 >= 0 && (ch2 > ch || (ch2 == ch && e2 < e));
+      if (!__ballot(wrong)) break;
+#pragma unroll
+      for (int odd = 0; odd < 2; ++odd) {
+        const bool left = ((rl ^ odd) & 1) == 0;
+        const int p = left ? lane + 1 : lane - 1, pr = left ? rl + 1 : rl - 1;
+        const float pch = __shfl(ch, p), pv = __shfl(v, p);
+        const int pe = __shfl(e, p);
+        if (pr >= 0 && pr < K && rl < K && pe >= 0 && e >= 0) {
+          const bool partner_first = pch > ch || (pch == ch && pe < e);
+          if (left ? partner_first : !partner_first) {
+            ch = pch;
+            v = pv;
+            e = pe;
+          }
+        }
+      }
+    }
+    if (biased) {
+      // neighbours lie apart by more than both errors; behind the last slot
+      // counts the largest choice that the next key's kept bits allow
+      const uint32_t top = k2 | kIdx;
+      const float bound = __uint_as_float(top ^ (((int32_t)top < 0) ? 0x80000000u : 0xffffffffu));
+      const float ch2 = __uint_as_float(right(__float_as_uint(ch)));
+      const int e2 = (int)right((uint32_t)e);
+      if (rl + 1 < K && e2 >= 0) unsure = unsure || !(ch - ch2 > 2.f * choice_tol(ch));
+      if (rl == K - 1 && k2) unsure = unsure || !(ch - bound > 2.f * choice_tol(ch));
+    }
+  }
+
+  float w = rl < K && e >= 0 ? (softmax ? (v == m ? 1.f : expf(v - m)) * zinv : 1.0f / (1.0f + expf(-v))) : 0.f;
+  if (a.renormalize) {
+    const float sum = row_reduce_f32<L, false>(w);
+    w = sum > 0.f ? w / sum : 0.f;
+  }
+  // one lane's doubt is the row's
+  unsure = row_max_u32<L>(unsure ? 1u : 0u) != 0;
+  if (live && rl < K && !unsure) {
+    a.ids[t * K + rl] = e;
+    a.weights[t * K + rl] = w * a.scale;
+  }
+  return live && unsure;
+}
+
+// FAST: the fast path, then the exact one for the rows it leaves; else the
+// exact path alone.
+template <int L, int NV, bool BF16, bool FAST>
+__global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(RouterArgs a) {
+  extern __shared__ double keys_lds[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  double* mine = keys_lds + wave * a.E;
+  constexpr int ENV = (L * NV + 63) / 64;   // experts of a lane on the exact path
+  const int64_t t0 = ((int64_t)blockIdx.x * kRouterWaves + wave) * (FAST ? 64 / L : 1);
+  if constexpr (FAST) {
+    const uint64_t left = __ballot(route_fast<L, NV, BF16>(a, t0 + lane / L, lane));
+    if (left == 0) return;
+    for (int r = 0; r < 64 / L; ++r)
+      if (left >> (r * L) & 1) route_exact<ENV, BF16>(a, t0 + r, lane, mine);
+  } else {
+    if (t0 < a.T) route_exact<ENV, BF16>(a, t0, lane, mine);
+  }
+}
+
+template <int L, int NV, bool FAST>
+static void router_launch(const RouterArgs& a, bool bf16, hipStream_t stream) {
+  constexpr int rows = kRouterWaves * (FAST ? 64 / L : 1);
+  const dim3 grid((unsigned)(((int64_t)a.T + rows - 1) / rows)), block(64 * kRouterWaves);
+  const size_t lds = a.n_group > 1 ? sizeof(double) * kRouterWaves * a.E : 0;   // at most 32 KB
+  if (bf16) hipLaunchKernelGGL((router_topk_kernel<L, NV, true, FAST>), grid, block, lds, stream, a);
+  else hipLaunchKernelGGL((router_topk_kernel<L, NV, false, FAST>), grid, block, lds, stream, a);
 }
 
 hipError_t launch_router_topk(const void* logits, bool bf16, const float* bias, int T, int E, int K, int score,
                               int n_group, int topk_group, int group_top, bool renormalize, float scale,
                               int32_t* ids, float* weights, hipStream_t stream) {
-#define FP8MOE_ROUTER(NV)                                                                                         \
-  router_launch<NV>(logits, bf16, bias, T, E, K, score, n_group, topk_group, group_top, renormalize, scale, ids, \
-                    weights, stream)
-  if (E <= 64) FP8MOE_ROUTER(1);
-  else if (E <= 128) FP8MOE_ROUTER(2);
-  else if (E <= 256) FP8MOE_ROUTER(4);
-  else if (E <= 512) FP8MOE_ROUTER(8);
-  else FP8MOE_ROUTER(16);
-#undef FP8MOE_ROUTER
+  // The fast path's rows: 16 lanes up to 256 experts and 15 slots (one more
+  // lane holds the expert behind the last slot), else 64.  Groups have to be
+  // whole lanes, a power of two of them.
+  const int L = E <= 256 && K < 16 ? 16 : 64;
+  const int NV = L == 16 ? (E <= 64 ? 4 : E <= 128 ? 8 : 16) : E <= 512 ? 8 : 16;
+  const int per = E / n_group, gl = per / NV;
+  const bool whole = n_group == 1 || (per % NV == 0 && (gl & (gl - 1)) == 0);
+  const bool fast = K < L && whole;
+  const bool vec = E == L * NV && (uintptr_t)logits % 16 == 0 && (uintptr_t)bias % 16 == 0;
+  const RouterArgs a{logits, bias, T, E, K, score, n_group, topk_group, group_top, (int)renormalize, (int)vec,
+                     scale, ids, weights};
+  if (fast) {
+    if (L == 16) {
+      if (NV == 4) router_launch<16, 4, true>(a, bf16, stream);
+      else if (NV == 8) router_launch<16, 8, true>(a, bf16, stream);
+      else router_launch<16, 16, true>(a, bf16, stream);
+    } else {
+      if (NV == 8) router_launch<64, 8, true>(a, bf16, stream);
+      else router_launch<64, 16, true>(a, bf16, stream);
+    }
+  } else {
+    if (E <= 64) router_launch<16, 4, false>(a, bf16, stream);
+    else if (E <= 128) router_launch<16, 8, false>(a, bf16, stream);
+    else if (E <= 256) router_launch<16, 16, false>(a, bf16, stream);
+    else if (E <= 512) router_launch<64, 8, false>(a, bf16, stream);
+    else router_launch<64, 16, false>(a, bf16, stream);
+  }
   return hipGetLastError();
 }
 

@@ -30,7 +30,9 @@ def router_reference(logits, K, score, bias=None, n_group=1, topk_group=1, group
         choice[~able] = -np.inf
         if n_group > 1:
             inside = choice if bias is not None or group_top == 1 else np.where(able, sc, -np.inf)
-            best = -np.sort(-inside.reshape(n_group, -1), axis=1)[:, :group_top].sum(axis=1)
+            best = -np.sort(-inside.reshape(n_group, -1), axis=1)[:, :group_top]
+            # a group of fewer experts than group_top counts as -inf
+            best = np.where((best == -np.inf).any(axis=1), -np.inf, np.where(best == -np.inf, 0, best).sum(axis=1))
             kept = np.lexsort((np.arange(n_group), -best))[:topk_group]
             out = ~np.isin(np.arange(E) // (E // n_group), kept)
             able &= ~out

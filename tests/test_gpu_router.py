@@ -77,6 +77,7 @@ def test_ties_go_to_the_lowest_index(score, dtype):
     logits[1] = torch.arange(200) % 3
     logits[2] = -(torch.arange(200) // 50).to(dtype)
     logits[3, 150:] = 1
+    logits[0, ::3] = -0.0
     ids, _ = check(logits, 8, score)
     assert ids[0].tolist() == list(range(8))
     check(logits, 8, score, torch.zeros(200))
@@ -142,10 +143,32 @@ def test_softmax_of_far_logits_underflows_to_zero():
     assert ids[0].tolist() == [0, 1, 2, 3] and w[0].tolist() == [0, 0, 0, 0]
 
 
-def test_many_tokens():
-    logits, bias = make(5000, 256, 77)
-    check(logits, 8, "sigmoid", bias, n_group=8, topk_group=4, group_top=2)
-    check(logits.bfloat16(), 8, "softmax")
+@pytest.mark.parametrize("T,E,K,groups", [(5000, 256, 8, (8, 4, 2)), (5000, 256, 8, (8, 3, 1)), (5003, 128, 6, (1, 1, 1)),
+                                          (3001, 64, 7, (4, 2, 2)), (2000, 512, 15, (8, 4, 2)),
+                                          (1501, 192, 15, (6, 2, 2)), (1200, 1000, 20, (1, 1, 1))])
+def test_many_tokens(T, E, K, groups):
+    """Enough rows that close scores occur among them."""
+    say("router many", T, E, K, groups)
+    kw = dict(zip(("n_group", "topk_group", "group_top"), groups))
+    logits, bias = make(T, E, 77)
+    check(logits, K, "sigmoid", bias, **kw)
+    check(logits, K, "softmax", bias, **kw)
+    check(logits, K, "softmax", **kw)
+    check(logits.bfloat16(), K, "softmax", renormalize=False, **kw)
+    check(logits.bfloat16(), K, "sigmoid", bias, **kw)
+    check(logits * 2.0 ** -12, K, "sigmoid", **kw)
+    check(logits * 2.0 ** -12, K, "sigmoid", bias * 2.0 ** -12, **kw)
+
+
+def test_unaligned_views():
+    """Rows that no 16-byte vector can read."""
+    flat = make(40, 256, 3)[0].reshape(-1)
+    for off in (1, 2, 3):
+        logits = flat[off:off + 39 * 256].view(39, 256)
+        dev = flat.cuda()[off:off + 39 * 256].view(39, 256)
+        ids, w = fm.moe_router_topk(dev, 8)
+        rid, _ = router_reference(logits.double().numpy(), 8, "softmax")
+        assert np.array_equal(ids.cpu().numpy(), rid)
 
 
 def test_given_outputs_stream_and_graph():
