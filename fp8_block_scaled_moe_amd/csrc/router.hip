@@ -19,8 +19,8 @@
 // if in 64 bits.  Two paths give the same answer:
 //
 // Exact path (route_exact): one wave64 per token, every score and choice in
-// fp64.  About 100 64-bit operations per 4 experts; it measured 31 us for 8192
-// tokens of 256 experts in groups, 121 us for 65537 tokens of 128.
+// fp64.  As the only path it measured 31 us for 8192 tokens of 256 experts in
+// groups, 121 us for 65537 tokens of 128.
 //
 // Fast path (route_fast): L = 16 lanes per token (64 beyond 256 experts or 15
 // slots), lane l holds experts l NV .. l NV + NV - 1, choices in fp32.  Each is
@@ -74,17 +74,37 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// The largest (key, lowest index on ties) over the wave, in every lane.
-__device__ __forceinline__ void wave_argmax(double& key, int& idx) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) {
-    const double k2 = shfl_xor_f64(key, o);
-    const int i2 = __shfl_xor(idx, o);
-    if (k2 > key || (k2 == key && i2 < idx)) {
-      key = k2;
-      idx = i2;
-    }
+// The largest of v over the row's L lanes, in each of them: rotations inside
+// 16 lanes, then row and half swaps.
+template <int L>
+__device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, false));   // rotate by 8 of 16
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, false));
+  if constexpr (L == 64) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(r[0], r[1]);
+    const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max(h[0], h[1]);
   }
+  return v;
+}
+
+// Bits of a double that order as unsigned integers; 0 for "never chosen",
+// which -inf stands for.  + 0: zeros of both signs are equal.
+__device__ __forceinline__ uint64_t sortable64(double v) {
+  if (!(v > -__longlong_as_double(0x7ff0000000000000ll))) return 0;
+  const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
+  return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+}
+
+// The lowest index among the lanes with the largest key; -1 where none has one.
+__device__ __forceinline__ int wave_argmax(uint64_t key, int idx) {
+  const uint32_t hi = row_max_u32<64>((uint32_t)(key >> 32));
+  const uint32_t lo = row_max_u32<64>((uint32_t)(key >> 32) == hi ? (uint32_t)key : 0u);
+  const bool best = key != 0 && key == ((uint64_t)hi << 32 | lo);
+  return (int)(0xffffffffu - row_max_u32<64>(best ? 0xffffffffu - (uint32_t)idx : 0u));
 }
 
 // Token t by one wave: expert lane + 64 i in register i; mine: E doubles of LDS.
@@ -149,25 +169,26 @@ __device__ __noinline__ void route_exact(const RouterArgs& a, int64_t t, int lan
     const int G = E / n_group;
     double first = kNone, second = kNone;
     if (lane < n_group) {
-      for (int i = 0; i < G; ++i) {
-        const double v = mine[lane * G + i];
-        if (v > first) {
-          second = first;
-          first = v;
-        } else if (v > second) {
-          second = v;
+      for (int i = 0; i < G; i += 8) {
+        double v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = mine[min(lane * G + i + k, E - 1)];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const double u = i + k < G ? v[k] : kNone;
+          second = fmax(second, fmin(first, u));
+          first = fmax(first, u);
         }
       }
     }
     const double total = group_top > 1 ? (second > kNone ? first + second : kNone) : first;
-    bool taken = lane >= n_group;
+    // groups of no choice come last, in ascending order, by a key below all others
+    uint64_t gkey = lane < n_group ? (sortable64(total) ? sortable64(total) : 1) : 0;
     uint64_t kept = 0;
     for (int j = 0; j < topk_group; ++j) {
-      double k = taken ? kNone : total;
-      int g = taken ? 64 + lane : lane;
-      wave_argmax(k, g);
-      kept |= 1ull << (g & 63);
-      if (lane == g) taken = true;
+      const int g = wave_argmax(gkey, lane);
+      kept |= 1ull << g;
+      if (lane == g) gkey = 0;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -177,27 +198,31 @@ __device__ __noinline__ void route_exact(const RouterArgs& a, int64_t t, int lan
   }
 
   // slot j's expert and weight end in lane j
+  uint64_t left[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) left[i] = sortable64(key[i]);
   int my_id = -1;
   double my_w = 0.0, sum = 0.0;
   for (int j = 0; j < K; ++j) {
-    double k = kNone;
-    int e = E + lane;
+    uint64_t k = left[0];
+    int e = lane;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (key[i] > k) {
-        k = key[i];
+    for (int i = 1; i < NV; ++i)
+      if (left[i] > k) {
+        k = left[i];
         e = lane + 64 * i;
       }
-    wave_argmax(k, e);
-    if (e >= E) break;   // nothing left
+    e = wave_argmax(k, e);
+    if (e < 0) break;   // nothing left
     double w = 0.0;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (e == lane + 64 * i) {
-        key[i] = kNone;
+        left[i] = 0;
         w = sc[i];
       }
-    w = __hiloint2double(__shfl(__double2hiint(w), e & 63), __shfl(__double2loint(w), e & 63));
+    w = __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(w), e & 63),
+                         __builtin_amdgcn_readlane(__double2loint(w), e & 63));
     sum += w;
     if (lane == j) {
       my_id = e;
@@ -210,20 +235,6 @@ __device__ __noinline__ void route_exact(const RouterArgs& a, int64_t t, int lan
     ids[t * K + lane] = my_id;
     weights[t * K + lane] = (float)(w * (double)scale);
   }
-}
-
-// The largest of v over the row's L lanes, in each of them.
-template <int L>
-__device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, false));   // rotate by 8 of 16
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, false));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, false));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, false));
-  if constexpr (L == 64) {
-    v = max(v, (uint32_t)__shfl_xor((int)v, 16));
-    v = max(v, (uint32_t)__shfl_xor((int)v, 32));
-  }
-  return v;
 }
 
 // Sum and maximum of floats over the row's L lanes.
