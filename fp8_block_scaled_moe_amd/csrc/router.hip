@@ -109,7 +109,7 @@ __device__ __forceinline__ int wave_argmax(uint64_t key, int idx) {
 
 // Token t by one wave: expert lane + 64 i in register i; mine: E doubles of LDS.
 template <int NV, bool BF16>
-__device__ __noinline__ void route_exact(const RouterArgs& a, int64_t t, int lane, double* mine) {
+__device__ __forceinline__ void route_exact(const RouterArgs& a, int64_t t, int lane, double* mine) {
   const int E = a.E, K = a.K, score = a.score, n_group = a.n_group, topk_group = a.topk_group,
             group_top = a.group_top, renormalize = a.renormalize;
   const float scale = a.scale;
