@@ -272,6 +272,11 @@ static hipError_t norm_launch(const uint16_t* x, const void* residual, bool resi
   return hipGetLastError();
 }
 
+// Up to this many rows a row is spread over as many threads as it has vectors:
+// the call is then bound by latency, which the fewest elements per thread make
+// shortest.
+constexpr int kNormFewRows = 512;
+
 template <int FMT>
 static hipError_t norm_format(const uint16_t* x, const void* residual, bool residual_f32, const void* weight,
                               bool weight_f32, float eps, int64_t T, int H, void* residual_out, uint16_t* norm_out,
@@ -280,6 +285,11 @@ static hipError_t norm_format(const uint16_t* x, const void* residual, bool resi
   return norm_launch<TPR, V, FMT>(x, residual, residual_f32, weight, weight_f32, eps, T, H, residual_out, norm_out, \
                                   q, scale, stream)
   if (H <= 512) FP8MOE_NORM(64, 1);
+  if (T <= kNormFewRows) {
+    if (H <= 2048) FP8MOE_NORM(256, 1);
+    if (H <= 8192) FP8MOE_NORM(1024, 1);
+    FP8MOE_NORM(1024, 2);
+  }
   if (H <= 2048) FP8MOE_NORM(64, 4);
   if (H <= 8192) FP8MOE_NORM(256, 4);
   FP8MOE_NORM(256, 8);

@@ -26,16 +26,15 @@
 // slots), lane l holds experts l NV .. l NV + NV - 1, choices in fp32.  Each is
 // a 32-bit key: the order-preserving bits of the choice with the lowest
 // IB replaced by the complement of the expert's index, so keys are unique, the
-// largest key is the winner, and it is taken out by comparing.  The row goes
-// to the exact path where fp32 or the cut bits could have decided wrongly:
+// largest key is the winner, and it is taken out by comparing.
 //   * bf16 logits without a bias: 16 value bits and the index fit, always exact;
-//   * fp32 logits without a bias: the chosen set is right unless the K-th and
-//     the next key agree in the kept bits; chosen ones are then put in order by
-//     their full values;
-//   * with a bias, and for groups counted by sums: besides that, neighbours
-//     among the chosen and the next one (kept and left groups) lie further
-//     apart than the error of both.
-// On random logits that is about 1 row in some hundreds.
+//   * else further keys are taken until the next cannot reach the last slot's,
+//     and the candidates are put in order by their full choices: the logits
+//     themselves, or, where neighbours lie closer than fp32's error, the
+//     biased logistic function in fp64;
+//   * what is left for the exact path: more close candidates than lanes, close
+//     choices of a biased softmax, and groups counted by sums of which a kept
+//     and a left one are closer than the error of both.
 #include "device_common.h"
 #include "fp8moe.h"
 #include "launch.h"
@@ -254,6 +253,15 @@ __device__ __forceinline__ uint32_t sortable(float v) {
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
+__device__ __forceinline__ float key_value(uint32_t s) {
+  return __uint_as_float(s ^ ((int32_t)s < 0 ? 0x80000000u : 0xffffffffu));
+}
+
+__device__ __forceinline__ float shfl_any(float v, int l) { return __shfl(v, l); }
+__device__ __forceinline__ double shfl_any(double v, int l) {
+  return __hiloint2double(__shfl(__double2hiint(v), l), __shfl(__double2loint(v), l));
+}
+
 // exp(x) for x <= 0 (a few ulp plus |x| 2^-24) and the logistic function on
 // the transcendental units.
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
@@ -360,11 +368,13 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
 #pragma unroll
     for (int i = 0; i < NV; ++i) c[i] = x[i];
   }
-  // Error of a choice, with margin: fp32 scores are within 2^-19 of the exact
-  // ones (a softmax's sum is 16 terms a lane and 6 levels of lanes, 1 + 2 + 22 +
-  // a few roundings of 2^-24; the logistic function is within 2^-22), and the
-  // bias adds half a step.
-  auto choice_tol = [&](float v) __attribute__((always_inline)) -> float { return 0x1p-18f + fabsf(v) * 0x1p-21f; };
+  // Error of a choice c of score s, with margin: the logistic function is
+  // within 2^-22, a softmax's score within 2^-19 of itself (the exponential's
+  // argument, and a sum of 16 terms a lane and 6 levels of lanes), and the bias
+  // adds half a step of c.
+  auto choice_tol = [&](float s, float c) __attribute__((always_inline)) -> float {
+    return (softmax ? s * 0x1p-18f : 0x1p-21f) + fabsf(c) * 0x1p-22f;
+  };
 
   if (a.n_group > 1) {
     // a group is a whole number (a power of two) of the row's lanes
@@ -393,7 +403,16 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
     if (biased || sums) {
       const float worst = -row_reduce_f32<L, true>(keep && rl < a.n_group * gl ? -total : kNone);
       const float best = row_reduce_f32<L, true>(keep || rl >= a.n_group * gl ? kNone : total);
-      const float tol = biased ? 2.f * choice_tol(fmaxf(fabsf(worst), fabsf(best))) : 0x1p-15f * fabsf(worst);
+      // two choices each (the tolerance has a margin of two); scores without a
+      // bias carry their argument's rounding relative to themselves
+      float tol = 2.f * choice_tol(1.f, fmaxf(fabsf(worst), fabsf(best)));
+      if (sums) {
+        float far = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (fabsf(x[i]) < kRouterInf) far = fmaxf(far, fabsf(x[i]));
+        tol = (2.f * row_reduce_f32<L, true>(far) + 32.f) * 0x1p-23f * fabsf(worst);
+      }
       // (sums of scores next to fp32's smallest have no relative bound)
       if (a.topk_group < a.n_group && best > kNone) unsure = !(worst - best > tol) || (sums && worst < 0x1p-100f);
     }
@@ -406,58 +425,79 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
 #pragma unroll
   for (int i = 0; i < NV; ++i)   // + 0: zeros of both signs are equal
     key[i] = c[i] > kNone ? (sortable(c[i] + 0.f) & ~kIdx) | (kIdx - (uint32_t)(rl * NV + i)) : 0u;
-  const bool cut = !BF16 || biased;   // keys hold a part of the choice: the one behind the last slot is looked at too
-  uint32_t mine = 0;
-  const int rounds = K + (cut ? 1 : 0);
-  for (int j = 0; j < rounds; ++j) {
+  const bool cut = !BF16 || biased;   // keys hold a part of the choice
+  uint32_t mine = 0, last = 0;
+  auto take = [&](int j) __attribute__((always_inline)) {
     uint32_t w = key[0];
 #pragma unroll
     for (int i = 1; i < NV; ++i) w = max(w, key[i]);
     w = row_max_u32<L>(w);
     if (rl == j) mine = w;
+    last = w;
 #pragma unroll
     for (int i = 0; i < NV; ++i) key[i] = key[i] == w ? 0u : key[i];
+  };
+  for (int j = 0; j < K; ++j) take(j);
+  int taken = K;
+  if (cut) {
+    // Further candidates, until the last one's largest possible choice lies
+    // below the smallest of slot K - 1's by more than both errors: the K best
+    // are then among them.
+    const uint32_t kth = last;
+    const float kmin = key_value(kth & ~kIdx);
+    const float margin = biased ? 2.f * choice_tol(1.f, kmin) : 0.f;
+    bool open = kth != 0;
+    while (taken < L - 1 && __ballot(open)) {
+      take(taken++);
+      open = open && last != 0 && !(key_value(last | kIdx) < kmin - margin);
+    }
+    unsure = unsure || open;
   }
   int e = mine ? (int)(kIdx - (mine & kIdx)) : -1;
   float v = e >= 0 ? router_logit<BF16>(a.logits, t * E + e) : kNone;
 
   if (cut) {
-    auto right = [&](uint32_t w) __attribute__((always_inline)) -> uint32_t { return (uint32_t)__shfl((int)w, lane + 1); };
-    const uint32_t k2 = right(mine);
-    // the set is right unless the last slot and the next one agree in the kept bits
-    if (rl == K - 1 && k2 && (k2 & ~kIdx) == (mine & ~kIdx)) unsure = true;
-    // slots out of order (equal kept bits): odd-even exchanges until none is
-    float ch = biased ? (e >= 0 ? score_of(v) + a.bias[e] : kNone) : v;
-    for (int pass = 0; pass < K; ++pass) {
-      const float ch2 = __uint_as_float(right(__float_as_uint(ch)));
-      const int e2 = (int)right((uint32_t)e);
-      const bool wrong = rl + 1 < K && e2 >= 0 && (ch2 > ch || (ch2 == ch && e2 < e));
-      if (!__ballot(wrong)) break;
+    // candidates in the order of their choices (nearly so already): odd-even
+    // exchanges until no neighbours are out of order
+    auto sort = [&](auto ch) __attribute__((always_inline)) {
+      for (int pass = 0; pass < L; ++pass) {
+        const auto ch2 = shfl_any(ch, lane + 1);
+        const int e2 = __shfl(e, lane + 1);
+        const bool wrong = rl + 1 < taken && e2 >= 0 && (ch2 > ch || (ch2 == ch && e2 < e));
+        if (!__ballot(wrong)) break;
 #pragma unroll
-      for (int odd = 0; odd < 2; ++odd) {
-        const bool left = ((rl ^ odd) & 1) == 0;
-        const int p = left ? lane + 1 : lane - 1, pr = left ? rl + 1 : rl - 1;
-        const float pch = __shfl(ch, p), pv = __shfl(v, p);
-        const int pe = __shfl(e, p);
-        if (pr >= 0 && pr < K && rl < K && pe >= 0 && e >= 0) {
-          const bool partner_first = pch > ch || (pch == ch && pe < e);
-          if (left ? partner_first : !partner_first) {
-            ch = pch;
-            v = pv;
-            e = pe;
+        for (int odd = 0; odd < 2; ++odd) {
+          const bool left = ((rl ^ odd) & 1) == 0;
+          const int p = left ? lane + 1 : lane - 1, pr = left ? rl + 1 : rl - 1;
+          const auto pch = shfl_any(ch, p);
+          const float pv = __shfl(v, p);
+          const int pe = __shfl(e, p);
+          if (pr >= 0 && pr < taken && rl < taken && pe >= 0 && e >= 0) {
+            const bool partner_first = pch > ch || (pch == ch && pe < e);
+            if (left ? partner_first : !partner_first) {
+              ch = pch;
+              v = pv;
+              e = pe;
+            }
           }
         }
       }
-    }
-    if (biased) {
-      // neighbours lie apart by more than both errors; behind the last slot
-      // counts the largest choice that the next key's kept bits allow
-      const uint32_t top = k2 | kIdx;
-      const float bound = __uint_as_float(top ^ (((int32_t)top < 0) ? 0x80000000u : 0xffffffffu));
-      const float ch2 = __uint_as_float(right(__float_as_uint(ch)));
-      const int e2 = (int)right((uint32_t)e);
-      if (rl + 1 < K && e2 >= 0) unsure = unsure || !(ch - ch2 > 2.f * choice_tol(ch));
-      if (rl == K - 1 && k2) unsure = unsure || !(ch - bound > 2.f * choice_tol(ch));
+      return ch;
+    };
+    if (!biased) {
+      sort(v);
+    } else {
+      const float ch = sort(e >= 0 ? score_of(v) + a.bias[e] : kNone);
+      const float tol = e >= 0 ? choice_tol(score_of(v), ch) : 0.f;
+      const float ch2 = __shfl(ch, lane + 1), tol2 = __shfl(tol, lane + 1);
+      const int e2 = __shfl(e, lane + 1);
+      const bool close = rl < K && rl + 1 < taken && e2 >= 0 && !(ch - ch2 > tol + tol2);
+      if (__ballot(close)) {
+        // neighbours too close for fp32: the logistic function's choices in
+        // fp64; a softmax's need its sum in fp64 and go the exact way
+        if (softmax) unsure = unsure || close;
+        else sort(e >= 0 ? 1.0 / (1.0 + exp(-(double)v)) + (double)a.bias[e] : -(double)kRouterInf);
+      }
     }
   }
 

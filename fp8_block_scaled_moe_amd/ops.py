@@ -5,7 +5,6 @@ check dtypes/shapes/devices, allocate outputs with torch, pass raw pointers
 and the current HIP stream, and raise Fp8MoeError on a non-zero status.
 """
 
-import contextlib
 import ctypes
 
 import torch
@@ -13,6 +12,9 @@ import torch
 from ._lib import lib, check, Fp8MoeError  # noqa: F401
 
 ALIGNS = (16, 32, 64, 128)
+
+# the hipStream_t of a device's current stream as an integer, without building a Stream object
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _p(t):
@@ -50,14 +52,17 @@ def _same_device(dev, **tensors):
             raise ValueError(f"{name} is on {t.device}, not on {dev}")
 
 
-@contextlib.contextmanager
-def _on(dev):
-    """The launches of a call go to its tensors' device, whichever is current."""
-    if torch.cuda.current_device() == dev.index:
-        yield
-    else:
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(dev, fn, *args):
+    """fn(*args, stream): the call goes to its tensors' device, whichever is current, on that device's
+    current stream."""
+    if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
-            yield
+            return check(fn(*args, _current_raw_stream(dev.index)))
+    return check(fn(*args, _current_raw_stream(dev.index)))
 
 
 def _out(t, shape, dtype, name, dev):
@@ -640,10 +645,9 @@ def moe_fused_int8(x, x_scale, w13, w13_scale, w2, w2_scale, topk_ids, topk_weig
         workspace = alloc_workspace_int8(T, H, I, E, K, dev)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    with _on(dev):
-        check(lib().moe_fused_int8(_p(x), _p(x_scale), _p(w13), _p(w13_scale), _p(w2), _p(w2_scale), _p(topk_ids),
-                                   _p(topk_weights), T, H, I, E, K, _p(out), _p(workspace), workspace.nbytes, tile_m,
-                                   weight_layout, _stream(dev)))
+    _launch(dev, lib().moe_fused_int8, _ptr(x), _ptr(x_scale), _ptr(w13), _ptr(w13_scale), _ptr(w2),
+            _ptr(w2_scale), _ptr(topk_ids), _ptr(topk_weights), T, H, I, E, K, _ptr(out), _ptr(workspace),
+            workspace.nbytes, tile_m, weight_layout)
     return out
 
 
@@ -664,10 +668,9 @@ def gemm1_swiglu_int8(x, x_scale, w13, w13_scale, route, T, K, align, tile_m=-1,
     _same_device(dev, x_scale=x_scale, w13=w13, w13_scale=w13_scale, route=route["sorted_src"])
     act = torch.zeros((cap, I), dtype=torch.bfloat16, device=dev) if act is None else act
     act = _out(act, (cap, I), torch.bfloat16, "act", dev)
-    with _on(dev):
-        check(lib().moe_gemm1_swiglu_int8(_p(x), _p(x_scale), _p(w13), _p(w13_scale), _p(route["padded_indptr"]),
-                                          _p(route["sorted_src"]), T, H, I, E, K, align, _p(act), cap, tile_m,
-                                          weight_layout, _stream(dev)))
+    _launch(dev, lib().moe_gemm1_swiglu_int8, _ptr(x), _ptr(x_scale), _ptr(w13), _ptr(w13_scale),
+            _ptr(route["padded_indptr"]), _ptr(route["sorted_src"]), T, H, I, E, K, align, _ptr(act), cap,
+            tile_m, weight_layout)
     return act
 
 
@@ -686,8 +689,7 @@ def quant_rows_int8(x, q=None, scale=None, route=None):
         scale = torch.zeros(rows, dtype=torch.float32, device=dev) if scale is None else scale
     q = _out(q, (rows, N), torch.int8, "q", dev)
     scale = _out(scale, (rows,), torch.float32, "scale", dev)
-    with _on(dev):
-        check(lib().moe_quant_rows_int8(_p(x), _p(src), rows, N, _p(q), _p(scale), _stream(dev)))
+    _launch(dev, lib().moe_quant_rows_int8, _ptr(x), _ptr(src), rows, N, _ptr(q), _ptr(scale))
     return q, scale
 
 
@@ -709,10 +711,9 @@ def gemm2_weighted_int8(q, q_scale, w2, w2_scale, route, topk_weights, T, K, ali
                  topk_weights=topk_weights)
     Y = torch.zeros((T * K, H), dtype=torch.bfloat16, device=dev) if Y is None else Y
     Y = _out(Y, (T * K, H), torch.bfloat16, "Y", dev)
-    with _on(dev):
-        check(lib().moe_gemm2_weighted_int8(_p(q), _p(q_scale), _p(w2), _p(w2_scale), _p(route["padded_indptr"]),
-                                            _p(route["sorted_src"]), _p(topk_weights), T, H, I, E, K, align, _p(Y),
-                                            cap, tile_m, weight_layout, _stream(dev)))
+    _launch(dev, lib().moe_gemm2_weighted_int8, _ptr(q), _ptr(q_scale), _ptr(w2), _ptr(w2_scale),
+            _ptr(route["padded_indptr"]), _ptr(route["sorted_src"]), _ptr(topk_weights), T, H, I, E, K, align,
+            _ptr(Y), cap, tile_m, weight_layout)
     return Y
 
 
@@ -781,11 +782,10 @@ def add_rmsnorm_quant(x, weight, eps, format, residual=None, want_norm=False, q=
         scale = _out(scale, (T,), torch.float32, "scale", dev)
     elif q is not None or scale is not None:
         raise ValueError("NORM_BF16 has no codes")
-    with _on(dev):
-        check(lib().add_rmsnorm_quant(_p(x), _p(residual), int(residual is not None and
-                                                               residual.dtype == torch.float32),
-                                      _p(weight), int(weight.dtype == torch.float32), eps, T, H, format,
-                                      _p(residual_out), _p(norm_out), _p(q), _p(scale), _stream(dev)))
+    residual_f32 = int(residual is not None and residual.dtype == torch.float32)
+    _launch(dev, lib().add_rmsnorm_quant, _ptr(x), _ptr(residual), residual_f32, _ptr(weight),
+            int(weight.dtype == torch.float32), eps, T, H, format, _ptr(residual_out), _ptr(norm_out), _ptr(q),
+            _ptr(scale))
     return q, scale, norm_out, residual_out
 
 
@@ -810,10 +810,8 @@ def moe_router_topk(logits, K, score=SCORE_SOFTMAX, bias=None, n_group=1, topk_g
         _same_device(dev, bias=bias)
     ids = _out(ids, (T, max(K, 0)), torch.int32, "ids", dev)
     weights = _out(weights, (T, max(K, 0)), torch.float32, "weights", dev)
-    with _on(dev):
-        check(lib().moe_router_topk(_p(logits), int(logits.dtype == torch.bfloat16), _p(bias), T, E, K, score,
-                                    n_group, topk_group, group_top, int(bool(renormalize)), scale, _p(ids),
-                                    _p(weights), _stream(dev)))
+    _launch(dev, lib().moe_router_topk, _ptr(logits), int(logits.dtype == torch.bfloat16), _ptr(bias), T, E, K,
+            score, n_group, topk_group, group_top, int(bool(renormalize)), scale, _ptr(ids), _ptr(weights))
     return ids, weights
 
 
