@@ -849,12 +849,22 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 
 bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
-// Tile height of the int8 products: the smallest that holds an even share of
-// the routed rows over the experts they can reach.
-int int8_tile_m(int requested, int64_t R, int E) {
+// Tile height of one of the int8 products, of NT N tiles of 256 weight rows:
+// the tile kernels from 8 rows an expert on, if their workgroups fill half the
+// chip, else the streaming kernel of the smallest height that holds an even
+// share of the routed rows over the experts they can reach.  Layer times with
+// streaming heights 16, 32, 64 and with tiles (us):
+//   H=2048, I=768, E=128, top-8:  T=128: 134, 144, 166 | 140; T=256: 164, 172,
+//     192 | 142; T=512: 227, 234, 235 | 156; Zipf 1.2: T=128: 96, 106, 146 | 87;
+//     T=512: 225, 221, 265 | 174
+//   H=7168, I=2048, E=256, top-8: T=256: 1857, 1848, 1926 | 1901; T=512: 2232,
+//     2114, 2116 | 2000; T=2048: 5167, 4397, 4218 | 2292
+//   H=7168, I=2048, E=1, top-1 (16 and 28 N tiles):  T=64: 35, 33, 40 | 50
+int int8_tile_m(int requested, int64_t R, int E, int64_t NT) {
   if (requested != -1) return requested;
   const int64_t active = R < E ? R : E, rows = active > 0 ? (R + active - 1) / active : 0;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kTileMaxInt8;
+  if (rows > 8 && (R / kTileMaxInt8 + active) * NT >= device_num_cu() / 2) return kTileMaxInt8;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
 int check_int8_stage(int64_t T, int32_t H, int32_t I, int32_t E, int32_t K, int32_t align, int64_t cap,
@@ -961,18 +971,18 @@ int moe_fused_int8(const void* x, const float* x_scale, const void* w13, const f
   if (T == 0) return ok();
   if (!aligned16(x) || !aligned16(w13) || !aligned16(w2) || !aligned16(out))
     return fail(FP8MOE_ERR_ALIGN, "tensors must be 16-byte aligned");
-  const int tm = int8_tile_m(tile_m, P.R, E);
+  const int tm1 = int8_tile_m(tile_m, P.R, E, I / 128), tm2 = int8_tile_m(tile_m, P.R, E, (H + 255) / 256);
   hipStream_t s = (hipStream_t)stream;
   hipError_t err = launch_route_permute(topk_ids, (int)P.R, E, P.align, (int)P.cap, P.counts, P.m_indptr, P.padded,
                                         P.sorted_src, P.src_to_sorted, s);
   if (err != hipSuccess) return hip_fail(err, "route_permute launch");
   GroupedRows g{P.padded, P.sorted_src, P.cap, E, K, P.R, device_num_cu()};
   err = launch_gemm1_int8(static_cast<const uint8_t*>(x), x_scale, static_cast<const uint8_t*>(w13), w13_scale, g, H,
-                          I, P.act, tm, P.packed, s);
+                          I, P.act, tm1, P.packed, s);
   if (err != hipSuccess) return hip_fail(err, "gemm1 launch");
   err = launch_quant_rows_int8(P.act, P.sorted_src, P.cap, I, P.q, P.q_scale, s);
   if (err != hipSuccess) return hip_fail(err, "quant_rows launch");
-  err = launch_gemm2_int8(P.q, P.q_scale, static_cast<const uint8_t*>(w2), w2_scale, topk_weights, g, H, I, P.Y, tm,
+  err = launch_gemm2_int8(P.q, P.q_scale, static_cast<const uint8_t*>(w2), w2_scale, topk_weights, g, H, I, P.Y, tm2,
                           P.packed, s);
   if (err != hipSuccess) return hip_fail(err, "gemm2 launch");
   err = launch_combine(P.Y, topk_ids, (int)T, H, E, K, static_cast<uint16_t*>(out), s);
@@ -993,7 +1003,8 @@ int moe_gemm1_swiglu_int8(const void* x, const float* x_scale, const void* w13, 
     return fail(FP8MOE_ERR_ALIGN, "tensors must be 16-byte aligned");
   GroupedRows g{padded_indptr, sorted_src, cap, E, K, T * K, device_num_cu()};
   hipError_t err = launch_gemm1_int8(static_cast<const uint8_t*>(x), x_scale, static_cast<const uint8_t*>(w13),
-                                     w13_scale, g, H, I, static_cast<uint16_t*>(act), int8_tile_m(tile_m, T * K, E),
+                                     w13_scale, g, H, I, static_cast<uint16_t*>(act),
+                                     int8_tile_m(tile_m, T * K, E, I / 128),
                                      weight_layout == FP8MOE_WEIGHTS_MFMA_TILED, (hipStream_t)stream);
   if (err != hipSuccess) return hip_fail(err, "gemm1 launch");
   return ok();
@@ -1029,7 +1040,8 @@ int moe_gemm2_weighted_int8(const void* q, const float* q_scale, const void* w2,
   GroupedRows g{padded_indptr, sorted_src, cap, E, K, T * K, device_num_cu()};
   hipError_t err = launch_gemm2_int8(static_cast<const uint8_t*>(q), q_scale, static_cast<const uint8_t*>(w2),
                                      w2_scale, topk_weights, g, H, I, static_cast<uint16_t*>(Y),
-                                     int8_tile_m(tile_m, T * K, E), weight_layout == FP8MOE_WEIGHTS_MFMA_TILED,
+                                     int8_tile_m(tile_m, T * K, E, (H + 255) / 256),
+                                     weight_layout == FP8MOE_WEIGHTS_MFMA_TILED,
                                      (hipStream_t)stream);
   if (err != hipSuccess) return hip_fail(err, "gemm2 launch");
   return ok();
