@@ -973,6 +973,15 @@ int moe_fused_int8(const void* x, const float* x_scale, const void* w13, const f
     return fail(FP8MOE_ERR_ALIGN, "tensors must be 16-byte aligned");
   const int tm1 = int8_tile_m(tile_m, P.R, E, I / 128), tm2 = int8_tile_m(tile_m, P.R, E, (H + 255) / 256);
   hipStream_t s = (hipStream_t)stream;
+  // a handful of rows, most of them of experts of their own: no routing
+  if (tile_m == -1 && P.R <= kDirectMaxRows && K <= kDirectMaxSlots && 8 * P.R <= E) {
+    const hipError_t err = launch_moe_direct_int8(
+        static_cast<const uint8_t*>(x), x_scale, static_cast<const uint8_t*>(w13), w13_scale,
+        static_cast<const uint8_t*>(w2), w2_scale, topk_ids, topk_weights, (int)T, H, I, E, K, P.act,
+        static_cast<uint16_t*>(out), P.packed, s);
+    if (err != hipSuccess) return hip_fail(err, "int8 layer launch");
+    return ok();
+  }
   hipError_t err = launch_route_permute(topk_ids, (int)P.R, E, P.align, (int)P.cap, P.counts, P.m_indptr, P.padded,
                                         P.sorted_src, P.src_to_sorted, s);
   if (err != hipSuccess) return hip_fail(err, "route_permute launch");

@@ -102,6 +102,20 @@ __device__ __forceinline__ void stream_gemm1(i32x4* red, const TileCoord& tc, co
   }
   const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
       (void*)(w13 + (size_t)tc.e * 2 * I * H), (short)0, 2 * I * H, kWeightRsrcFlags);
+  // the epilogue's scales: loaded ahead of the products where there are
+  // registers for them
+  const int r = 16 * wave + l16;
+  int src = -1;
+  float xs = 0.f;
+  v4f wg = {}, wu = {};
+  auto scales = [&]() __attribute__((always_inline)) {
+    src = r < tc.h ? sorted_src[tc.p0 + r] : -1;
+    xs = x_scale[src >= 0 ? src / K : 0];
+    const float* ws = w13_scale + (size_t)tc.e * 2 * I + c0 + 4 * g;
+    wg = *reinterpret_cast<const v4f*>(ws);
+    wu = *reinterpret_cast<const v4f*>(ws + I);
+  };
+  if constexpr (TS == 1) scales();
   i32x4 acc[TS][2];
 #pragma unroll
   for (int ts = 0; ts < TS; ++ts) acc[ts][0] = acc[ts][1] = i32x4{0, 0, 0, 0};
@@ -109,15 +123,12 @@ __device__ __forceinline__ void stream_gemm1(i32x4* red, const TileCoord& tc, co
   stream_steps<TS, PACKED>(rsrc, band, tok, H, wave, lane, acc);
   stream_join<TS>(red, wave, lane, acc);
   if (wave >= TS) return;
-  const int r = 16 * wave + l16;
-  const int src = r < tc.h ? sorted_src[tc.p0 + r] : -1;
+  if constexpr (TS > 1) scales();
   if (src < 0) return;
-  const float xs = x_scale[src / K];
-  const float* ws = w13_scale + (size_t)tc.e * 2 * I + c0 + 4 * g;
   float a[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    a[i] = silu_mul((float)acc[0][0][i] * (xs * ws[i]), (float)acc[0][1][i] * (xs * ws[I + i]));
+    a[i] = silu_mul((float)acc[0][0][i] * (xs * wg[i]), (float)acc[0][1][i] * (xs * wu[i]));
   *reinterpret_cast<uint2*>(act + (size_t)(tc.p0 + r) * I + c0 + 4 * g) =
       uint2{pack2_bf16(a[0], a[1]), pack2_bf16(a[2], a[3])};
 }
@@ -156,6 +167,161 @@ __device__ __forceinline__ void stream_gemm2(i32x4* red, const TileCoord& tc, co
     for (int i = 0; i < 4; ++i) y[i] = (float)acc[0][b][i] * (s * ws[i]);
     *reinterpret_cast<uint2*>(Y + (size_t)src * H + c0 + 16 * b + 4 * g) =
         uint2{pack2_bf16(y[0], y[1]), pack2_bf16(y[2], y[3])};
+  }
+}
+
+// GEMM2's sums straight from the bf16 activation, quantised on the way: the
+// lane's row (act_row points at its value 16 g) against one weight band.  The
+// first U K steps stay in registers between the row's maximum and the
+// products, with their weights in flight meanwhile; a longer row is read
+// twice.  Returns the row's scale.
+// (Done so in the routed launches too, beside each 32 weight rows, it cost what
+// the quantisation's own launch costs: T=33 58.8 and 58.4 us, T=64 1566 and
+// 1546 us.)
+template <int U, bool PACKED>
+__device__ __forceinline__ float act_steps(__amdgpu_buffer_rsrc_t rsrc, int band, const uint16_t* act_row, int I,
+                                           int lane, i32x4& acc) {
+  constexpr int kHalf = PACKED ? 1024 : 64, kStep = PACKED ? 2048 : 128;
+  const int KT = I / kKB;
+  const int voff = weight_lane_offset<PACKED>(lane, I);
+  v4i w[U][2];
+  uint4 a[U][2][2];
+  auto load_a = [&](int k0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + u < KT) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint4* p = reinterpret_cast<const uint4*>(act_row + (k0 + u) * kKB + hf * 64);
+          a[u][hf][0] = p[0];
+          a[u][hf][1] = p[1];
+        }
+      }
+  };
+  auto load_w = [&](int k0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + u < KT) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+          w[u][hf] =
+              __builtin_amdgcn_raw_buffer_load_b128(rsrc, voff, band * I + (k0 + u) * kStep + hf * kHalf, 0);
+      }
+  };
+  uint32_t m = 0;
+  auto maximum = [&](int k0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + u < KT) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) m = amax8_bits(a[u][hf][1], amax8_bits(a[u][hf][0], m));
+      }
+  };
+  load_a(0);
+  load_w(0);
+  maximum(0);
+  for (int k0 = U; k0 < KT; k0 += U) {
+    load_a(k0);
+    maximum(k0);
+  }
+  if (U < KT) load_a(0);
+  m = max(m, (uint32_t)__shfl_xor((int)m, 16));   // the lane groups of one row
+  m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+  const RowScaleInt8 s(m);
+  for (int k0 = 0; k0 < KT; k0 += U) {
+    if (k0 != 0) {
+      load_w(k0);
+      load_a(k0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + u < KT) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint2 lo = s.codes8(a[u][hf][0]), hi = s.codes8(a[u][hf][1]);
+          const v4i t = {(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
+          acc = mfma16x16x64_i8(w[u][hf], t, acc);
+        }
+      }
+  }
+  return s.scale;
+}
+
+// ------------------------------------------------------------------------------------------
+// A handful of routed rows (a decoded token or two): two launches without
+// routing, each row by itself, which reads a weight row once more only where
+// two of the rows share an expert.  The same arithmetic, and so the same bits,
+// as the launches above.  The operand's other 15 token columns are idle copies.
+//
+// GEMM1: workgroup (columns 16 x, row y); act holds row y at row y.
+template <bool PACKED>
+__global__ __launch_bounds__(64 * kStreamWaves) void gemm1_direct_int8_kernel(
+    const uint8_t* __restrict__ x, const float* __restrict__ x_scale, const uint8_t* __restrict__ w13,
+    const float* __restrict__ w13_scale, const int32_t* __restrict__ topk_ids, int E, int K, int H, int I,
+    uint16_t* __restrict__ act) {
+  __shared__ i32x4 red[kStreamWaves * 2 * 64];
+  const int row = blockIdx.y, e = topk_ids[row];
+  if ((unsigned)e >= (unsigned)E) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, c0 = 16 * blockIdx.x;
+  const uint8_t* const tok[1] = {x + (size_t)(row / K) * H + 16 * g};
+  const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(w13 + (size_t)e * 2 * I * H), (short)0, 2 * I * H, kWeightRsrcFlags);
+  const float xs = x_scale[row / K];
+  const float* ws = w13_scale + (size_t)e * 2 * I + c0 + 4 * g;
+  const v4f wg = *reinterpret_cast<const v4f*>(ws), wu = *reinterpret_cast<const v4f*>(ws + I);
+  i32x4 acc[1][2] = {{{0, 0, 0, 0}, {0, 0, 0, 0}}};
+  const int band[2] = {c0, I + c0};
+  stream_steps<1, PACKED>(rsrc, band, tok, H, wave, lane, acc);
+  stream_join<1>(red, wave, lane, acc);
+  if (wave != 0 || (lane & 15) != 0) return;
+  float a[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    a[i] = silu_mul((float)acc[0][0][i] * (xs * wg[i]), (float)acc[0][1][i] * (xs * wu[i]));
+  *reinterpret_cast<uint2*>(act + (size_t)row * I + c0 + 4 * g) =
+      uint2{pack2_bf16(a[0], a[1]), pack2_bf16(a[2], a[3])};
+}
+
+// GEMM2, row quantisation and combine: workgroup (columns 16 x, token y), one
+// wave per slot; each slot's value is rounded to bf16 before the sum over the
+// slots, as where it passes through memory.
+template <bool PACKED>
+__global__ __launch_bounds__(64 * kDirectMaxSlots) void gemm2_direct_int8_kernel(
+    const uint16_t* __restrict__ act, const uint8_t* __restrict__ w2, const float* __restrict__ w2_scale,
+    const int32_t* __restrict__ topk_ids, const float* __restrict__ topk_weights, int E, int K, int H, int I,
+    uint16_t* __restrict__ out) {
+  __shared__ float ys[kDirectMaxSlots][16];
+  const int t = blockIdx.y, lane = threadIdx.x & 63;
+  const int slot = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, c0 = 16 * blockIdx.x, row = t * K + slot;
+  const int e = topk_ids[row];
+  if ((unsigned)e < (unsigned)E) {
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(w2 + (size_t)e * H * I), (short)0, H * I, kWeightRsrcFlags);
+    const v4f ws = *reinterpret_cast<const v4f*>(w2_scale + (size_t)e * H + c0 + 4 * g);
+    const float tw = topk_weights[row];
+    i32x4 acc = {0, 0, 0, 0};
+    const float s = act_steps<6, PACKED>(rsrc, c0, act + (size_t)row * I + 16 * g, I, lane, acc) * tw;
+    if ((lane & 15) == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const uint32_t y = pack2_bf16((float)acc[i] * (s * ws[i]), (float)acc[i + 1] * (s * ws[i + 1]));
+        ys[slot][4 * g + i] = __uint_as_float(y << 16);
+        ys[slot][4 * g + i + 1] = __uint_as_float(y & 0xffff0000u);
+      }
+    }
+  } else if (lane < 16) {
+    ys[slot][lane] = 0.f;
+  }
+  __syncthreads();
+  if (threadIdx.x < 8) {
+    float a = 0.f, b = 0.f;
+    for (int j = 0; j < K; ++j) {
+      a += ys[j][2 * threadIdx.x];
+      b += ys[j][2 * threadIdx.x + 1];
+    }
+    reinterpret_cast<uint32_t*>(out + (size_t)t * H + c0)[threadIdx.x] = pack2_bf16(a, b);
   }
 }
 
@@ -241,81 +407,97 @@ hipError_t launch_gemm2_int8(const uint8_t* q, const float* q_scale, const uint8
 #undef FP8MOE_LAUNCH
 }
 
-// ------------------------------------------------------------------------------------------
-// Row quantisation: bf16 [rows][N] -> int8 codes and one scale per row.  One
-// wave per row; rows whose sorted_src is negative (padding) are left alone.
-// A row up to 64 * 8 * kQuantV values stays in registers; a longer one is read
-// twice (the second time from L2).
-constexpr int kQuantV = 8;
-
-__device__ __forceinline__ float amax8(const uint4& v, float m) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float a = fabsf(bf16_to_f32((uint16_t)(w[k] >> (16 * h))));
-      m = fmaxf(m, a <= 3.4028234e38f ? a : __uint_as_float(0x7f800000u));   // NaN counts as infinite
-    }
-  return m;
-}
-
-__device__ __forceinline__ uint2 quant8(const uint4& v, float s, float inv) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t o[2] = {0u, 0u};
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float n = bf16_to_f32((uint16_t)(w[k >> 1] >> (16 * (k & 1))));
-    // the correctly rounded quotient (see the 1x128 requantisation)
-    const float q0 = n * inv;
-    const float qv = s < 0x1p-100f ? n / s : fmaf(fmaf(-s, q0, n), inv, q0);
-    o[k >> 2] |= ((uint32_t)(int)rintf(fminf(fmaxf(qv, -127.f), 127.f)) & 0xffu) << (8 * (k & 3));
+hipError_t launch_moe_direct_int8(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
+                                  const uint8_t* w2, const float* w2_scale, const int32_t* topk_ids,
+                                  const float* topk_weights, int T, int H, int I, int E, int K, uint16_t* act,
+                                  uint16_t* out, bool packed, hipStream_t stream) {
+  if (K > kDirectMaxSlots || T * K > kDirectMaxRows) return hipErrorInvalidValue;
+  const dim3 grid1(I / 16, T * K), grid2(H / 16, T);
+#define FP8MOE_DIRECT(P)                                                                                        \
+  hipLaunchKernelGGL((gemm1_direct_int8_kernel<P>), grid1, dim3(64 * kStreamWaves), 0, stream, x, x_scale, w13, \
+                     w13_scale, topk_ids, E, K, H, I, act);                                                     \
+  hipLaunchKernelGGL((gemm2_direct_int8_kernel<P>), grid2, dim3(64 * K), 0, stream, act, w2, w2_scale, topk_ids, \
+                     topk_weights, E, K, H, I, out)
+  if (packed) {
+    FP8MOE_DIRECT(true);
+  } else {
+    FP8MOE_DIRECT(false);
   }
-  return uint2{o[0], o[1]};
+#undef FP8MOE_DIRECT
+  return hipGetLastError();
 }
 
+// ------------------------------------------------------------------------------------------
+// Row quantisation: bf16 [rows][N] -> int8 codes and one scale per row; rows
+// whose sorted_src is negative (padding) are left alone.  A wave takes R rows
+// at a time, V 16-byte vectors a lane and row, all loads of them in flight
+// together, since one row is far less than what hides a load's latency.  Rows
+// longer than 512 V values are read twice (the second time from L2).
+template <int V, int R>
 __global__ __launch_bounds__(256) void quant_rows_int8_kernel(const uint16_t* __restrict__ in,
                                                               const int32_t* __restrict__ sorted_src, int64_t rows,
                                                               int N, uint8_t* __restrict__ q,
                                                               float* __restrict__ scale) {
   const int lane = threadIdx.x & 63;
   const int NV = N / 8;
-  for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < rows; row += (int64_t)gridDim.x * 4) {
-    if (sorted_src && sorted_src[row] < 0) continue;
-    const uint4* src = reinterpret_cast<const uint4*>(in + row * N);
-    uint2* dst = reinterpret_cast<uint2*>(q + row * N);
-    uint4 v[kQuantV];
-    float m = 0.f;
-  #pragma unroll
-    for (int j = 0; j < kQuantV; ++j) {
-      const int c = lane + 64 * j;
-      v[j] = c < NV ? src[c] : uint4{0, 0, 0, 0};
+  const int64_t step = (int64_t)gridDim.x * 4 * R;
+  for (int64_t row0 = ((int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * R; row0 < rows;
+       row0 += step) {
+    bool live[R];
+    uint4 v[R][V];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      live[r] = row0 + r < rows && !(sorted_src && sorted_src[row0 + r] < 0);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (!live[r]) continue;
+      const uint4* src = reinterpret_cast<const uint4*>(in + (row0 + r) * N);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c = lane + 64 * j;
+        v[r][j] = c < NV ? src[c] : uint4{0, 0, 0, 0};
+      }
     }
-  #pragma unroll
-    for (int j = 0; j < kQuantV; ++j) m = amax8(v[j], m);
-    for (int c = lane + 64 * kQuantV; c < NV; c += 64) m = amax8(src[c], m);
-  #pragma unroll
-    for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-    const bool bad = !(m <= 3.4028234e38f);   // a row that holds no numbers: NaN scale, zero codes
-    float s = m / 127.f;
-    if (!(s > 0.f)) s = 1.f;
-    const float inv = 1.0f / s;
-  #pragma unroll
-    for (int j = 0; j < kQuantV; ++j) {
-      const int c = lane + 64 * j;
-      if (c < NV) dst[c] = bad ? uint2{0, 0} : quant8(v[j], s, inv);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (!live[r]) continue;
+      const uint4* src = reinterpret_cast<const uint4*>(in + (row0 + r) * N);
+      uint2* dst = reinterpret_cast<uint2*>(q + (row0 + r) * N);
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) m = amax8_bits(v[r][j], m);
+      for (int c = lane + 64 * V; c < NV; c += 64) m = amax8_bits(src[c], m);
+#pragma unroll
+      for (int o = 32; o; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
+      const RowScaleInt8 s(m);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c = lane + 64 * j;
+        if (c < NV) dst[c] = s.codes8(v[r][j]);
+      }
+      for (int c = lane + 64 * V; c < NV; c += 64) dst[c] = s.codes8(src[c]);
+      if (lane == 0) scale[row0 + r] = s.scale;
     }
-    for (int c = lane + 64 * kQuantV; c < NV; c += 64) dst[c] = bad ? uint2{0, 0} : quant8(src[c], s, inv);
-    if (lane == 0) scale[row] = bad ? __uint_as_float(0x7fc00000u) : s;
   }
 }
 
 hipError_t launch_quant_rows_int8(const uint16_t* in, const int32_t* sorted_src, int64_t rows, int N, uint8_t* q,
                                   float* scale, hipStream_t stream) {
-  const int64_t blocks = (rows + 3) / 4;
   constexpr int64_t kMaxBlocks = 1 << 20;   // beyond that, the grid-stride loop covers the rest
-  hipLaunchKernelGGL(quant_rows_int8_kernel, dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), dim3(256), 0, stream, in, sorted_src,
-                     rows, N, q, scale);
+#define FP8MOE_QUANT(V, R)                                                                                          \
+  const int64_t blocks = (rows + 4 * R - 1) / (4 * R);                                                              \
+  hipLaunchKernelGGL((quant_rows_int8_kernel<V, R>), dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), \
+                     dim3(256), 0, stream, in, sorted_src, rows, N, q, scale)
+  if (N <= 512) {
+    FP8MOE_QUANT(1, 4);
+  } else if (N <= 1024) {
+    FP8MOE_QUANT(2, 4);
+  } else if (N <= 2048) {
+    FP8MOE_QUANT(4, 2);
+  } else {
+    FP8MOE_QUANT(8, 1);
+  }
+#undef FP8MOE_QUANT
   return hipGetLastError();
 }
 

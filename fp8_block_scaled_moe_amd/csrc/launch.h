@@ -101,6 +101,13 @@ hipError_t launch_gemm2_int8(const uint8_t* q, const float* q_scale, const uint8
                              const float* topk_weights, const GroupedRows& g, int H, int I, uint16_t* Y, int tile_m,
                              bool packed, hipStream_t stream);
 
+// The whole layer without routing for at most kDirectMaxRows routed rows of at
+// most kDirectMaxSlots slots; act [T*K][I].
+constexpr int kDirectMaxRows = 16, kDirectMaxSlots = 8;
+hipError_t launch_moe_direct_int8(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
+                                  const uint8_t* w2, const float* w2_scale, const int32_t* topk_ids,
+                                  const float* topk_weights, int T, int H, int I, int E, int K, uint16_t* act,
+                                  uint16_t* out, bool packed, hipStream_t stream);
 // The tile kernels; GEMM1's takes x of less than 4 GiB (hipErrorInvalidValue).
 hipError_t launch_gemm1_int8_tile(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
                                   const GroupedRows& g, int H, int I, uint16_t* act, bool packed, hipStream_t stream);

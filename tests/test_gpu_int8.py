@@ -60,7 +60,11 @@ class Problem:
 LAYERS = [dict(T=16, H=256, I=128, E=4, K=2), dict(T=1, H=128, I=128, E=1, K=1), dict(T=1, H=2048, I=768, E=16, K=8),
           dict(T=33, H=640, I=384, E=8, K=3, skew=1.2), dict(T=257, H=384, I=256, E=3, K=2, skew=1.2),
           dict(T=700, H=256, I=640, E=5, K=2, skew=1.2, drop=0.3), dict(T=65, H=896, I=128, E=300, K=2),
-          dict(T=1300, H=512, I=256, E=2, K=1), dict(T=300, H=1152, I=896, E=1, K=1)]
+          dict(T=1300, H=512, I=256, E=2, K=1),
+          # a handful of rows: without routing, the largest of them, with dropped slots and beyond
+          dict(T=1, H=384, I=1408, E=64, K=8), dict(T=2, H=512, I=768, E=128, K=8, skew=1.2),
+          dict(T=5, H=128, I=2048, E=128, K=3, drop=0.4), dict(T=16, H=256, I=128, E=128, K=1),
+          dict(T=17, H=256, I=4224, E=136, K=1), dict(T=1, H=256, I=128, E=128, K=9), dict(T=300, H=1152, I=896, E=1, K=1)]
 
 
 @pytest.mark.parametrize("case", LAYERS, ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
@@ -141,28 +145,31 @@ def test_largest_sums_are_exact(H, low):
 
 
 def test_all_slots_dropped_and_no_tokens():
-    p = Problem(9, 256, 128, 4, 2)
-    p.d["ids"].fill_(-1)
-    for packed in (False, True):
-        assert not p.run(packed=packed).any()
+    for E in (4, 256):      # routed, and a handful of rows
+        p = Problem(8, 256, 128, E, 2)
+        p.d["ids"].fill_(-1)
+        for packed in (False, True):
+            assert not p.run(packed=packed).any()
     d = p.d
     out = fm.moe_fused_int8(d["x"][:0], d["xs"][:0], d["w13"], d["w13s"], d["w2"], d["w2s"], d["ids"][:0],
                             d["tw"][:0])
     assert out.shape == (0, 256)
 
 
-def test_scales_without_numbers_stay_in_their_rows():
-    p = Problem(40, 256, 128, 4, 2, seed=2)
-    clean = p.run()
+@pytest.mark.parametrize("T,E,tile_m", [(40, 4, 16), (40, 4, 64), (40, 4, 288), (13, 128, -1)])
+def test_scales_without_numbers_stay_in_their_rows(T, E, tile_m):
+    K = 2 if E == 4 else 1
+    p = Problem(T, 256, 128, E, K, seed=2)
+    clean = p.run(tile_m)
     p.d["xs"][7] = float("nan")
     p.d["xs"][11] = float("inf")
-    out = p.run()
+    out = p.run(tile_m)
     assert torch.isnan(out[[7, 11]]).all()
-    keep = [t for t in range(40) if t not in (7, 11)]
+    keep = [t for t in range(T) if t not in (7, 11)]
     assert torch.equal(out[keep], clean[keep])
 
 
-@pytest.mark.parametrize("N", [8, 72, 256, 2048, 4096, 4104, 16384])
+@pytest.mark.parametrize("N", [8, 72, 256, 520, 1024, 1032, 2048, 4096, 4104, 16384])
 def test_quant_rows(N):
     say("quant rows", N)
     g = torch.Generator().manual_seed(N)
@@ -170,12 +177,13 @@ def test_quant_rows(N):
     x[3] = 0
     x[4, N // 2] = float("nan")
     x[5, N - 1] = float("-inf")
-    x[6] = (x[6].float() * 2.0 ** -130).bfloat16()      # subnormal scales
+    x[6] = (torch.randn(N, generator=g) * 2.0 ** -130).bfloat16()      # below the smallest scale
+    x[7] = (torch.randn(N, generator=g).clamp(-4, 4) * 2.0 ** -112).bfloat16()
     q, s = fm.quant_rows_int8(x.cuda())
     torch.cuda.synchronize()
     q, s = q.cpu().double().numpy(), s.cpu().double().numpy()
-    assert np.isnan(s[[4, 5]]).all() and not q[[4, 5]].any() and s[3] == 1 and not q[3].any()
-    ok = [r for r in range(37) if r not in (3, 4, 5)]
+    assert np.isnan(s[[4, 5]]).all() and not q[[4, 5]].any() and (s[[3, 6]] == 1).all() and not q[[3, 6]].any()
+    ok = [r for r in range(37) if r not in (3, 4, 5, 6)]
     v = x[ok].double().numpy()
     _, want = O8.quantize_rows_int8(v)
     assert np.all(np.abs(s[ok] - want) <= want * 2.0 ** -23 + 2.0 ** -149)
@@ -184,8 +192,8 @@ def test_quant_rows(N):
 
 
 def test_more_rows_than_one_pass_of_the_grid():
-    """Beyond 2^20 workgroups of four rows the quantiser strides."""
-    rows = (1 << 22) + 5
+    """Beyond 2^20 workgroups of 16 rows the quantiser strides."""
+    rows = (1 << 24) + 5
     x = torch.zeros(rows, 8, dtype=torch.bfloat16, device="cuda")
     x[:, 3] = (torch.arange(rows, device="cuda") % 128).bfloat16()
     q, s = fm.quant_rows_int8(x)
