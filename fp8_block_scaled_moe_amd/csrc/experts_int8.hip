@@ -11,8 +11,13 @@
 //
 // The intermediate is rounded to bf16 before it is quantised: its row maximum
 // needs every column, so it passes through memory between the products, and
-// bf16 halves those bytes.  The rounding (2^-9 relative) is at most a quarter
-// of an int8 step.
+// bf16 halves those bytes.  The rounding (half a step, 2^-8 relative) is at
+// most half an int8 step.
+//
+// GEMM2's rows Y are fp32 where they are few beside the weights, and bf16 where
+// they are many: then their bytes, written and read once more by the combine,
+// are a tenth of the layer's time, and one more rounding (2^-8 of each slot's
+// value, the size of the output's own) buys half of them back.
 //
 // Streaming kernel: a workgroup owns 32 weight rows (GEMM1: 16 columns' gate
 // and up rows, so SwiGLU is lane-local) and an M tile of up to 64 tokens; its
@@ -133,13 +138,13 @@ __device__ __forceinline__ void stream_gemm1(i32x4* red, const TileCoord& tc, co
       uint2{pack2_bf16(a[0], a[1]), pack2_bf16(a[2], a[3])};
 }
 
-template <int TS, bool PACKED>
+template <int TS, bool PACKED, typename YT>
 __device__ __forceinline__ void stream_gemm2(i32x4* red, const TileCoord& tc, const uint8_t* __restrict__ q,
                                              const float* __restrict__ q_scale, const uint8_t* __restrict__ w2,
                                              const float* __restrict__ w2_scale,
                                              const float* __restrict__ topk_weights,
                                              const int32_t* __restrict__ sorted_src, int H, int I,
-                                             uint16_t* __restrict__ Y) {
+                                             YT* __restrict__ Y) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, l16 = lane & 15, c0 = 32 * tc.run;
   const uint8_t* tok[TS];
@@ -165,8 +170,7 @@ __device__ __forceinline__ void stream_gemm2(i32x4* red, const TileCoord& tc, co
     float y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = (float)acc[0][b][i] * (s * ws[i]);
-    *reinterpret_cast<uint2*>(Y + (size_t)src * H + c0 + 16 * b + 4 * g) =
-        uint2{pack2_bf16(y[0], y[1]), pack2_bf16(y[2], y[3])};
+    store_y4(Y + (size_t)src * H + c0 + 16 * b + 4 * g, y);
   }
 }
 
@@ -284,8 +288,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void gemm1_direct_int8_kernel(
 }
 
 // GEMM2, row quantisation and combine: workgroup (columns 16 x, token y), one
-// wave per slot; each slot's value is rounded to bf16 before the sum over the
-// slots, as where it passes through memory.
+// wave per slot, the slots summed in ascending order.
 template <bool PACKED>
 __global__ __launch_bounds__(64 * kDirectMaxSlots) void gemm2_direct_int8_kernel(
     const uint16_t* __restrict__ act, const uint8_t* __restrict__ w2, const float* __restrict__ w2_scale,
@@ -305,11 +308,7 @@ __global__ __launch_bounds__(64 * kDirectMaxSlots) void gemm2_direct_int8_kernel
     const float s = act_steps<6, PACKED>(rsrc, c0, act + (size_t)row * I + 16 * g, I, lane, acc) * tw;
     if ((lane & 15) == 0) {
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const uint32_t y = pack2_bf16((float)acc[i] * (s * ws[i]), (float)acc[i + 1] * (s * ws[i + 1]));
-        ys[slot][4 * g + i] = __uint_as_float(y << 16);
-        ys[slot][4 * g + i + 1] = __uint_as_float(y & 0xffff0000u);
-      }
+      for (int i = 0; i < 4; ++i) ys[slot][4 * g + i] = (float)acc[i] * (s * ws[i]);
     }
   } else if (lane < 16) {
     ys[slot][lane] = 0.f;
@@ -347,16 +346,16 @@ __global__ __launch_bounds__(64 * kStreamWaves) void gemm1_stream_int8_kernel(
 #undef FP8MOE_BODY
 }
 
-template <int TMAX, bool PACKED>
+template <int TMAX, bool PACKED, typename YT>
 __global__ __launch_bounds__(64 * kStreamWaves) void gemm2_stream_int8_kernel(
     const uint8_t* __restrict__ q, const float* __restrict__ q_scale, const uint8_t* __restrict__ w2,
     const float* __restrict__ w2_scale, const float* __restrict__ topk_weights, const int32_t* __restrict__ padded,
-    const int32_t* __restrict__ sorted_src, int E, int H, int I, uint16_t* __restrict__ Y) {
+    const int32_t* __restrict__ sorted_src, int E, int H, int I, YT* __restrict__ Y) {
   __shared__ i32x4 red[kStreamWaves * (TMAX / 16) * 2 * 64];
   TileCoord tc;
   if (!tile_coord<TMAX>(padded, sorted_src, E, H / 32, tc)) return;
 #define FP8MOE_BODY(TS) \
-  stream_gemm2<TS, PACKED>(red, tc, q, q_scale, w2, w2_scale, topk_weights, sorted_src, H, I, Y)
+  stream_gemm2<TS, PACKED, YT>(red, tc, q, q_scale, w2, w2_scale, topk_weights, sorted_src, H, I, Y)
   FP8MOE_STREAM_BODIES(FP8MOE_BODY)
 #undef FP8MOE_BODY
 }
@@ -390,22 +389,27 @@ hipError_t launch_gemm1_int8(const uint8_t* x, const float* x_scale, const uint8
 #undef FP8MOE_LAUNCH
 }
 
+template <typename YT>
 hipError_t launch_gemm2_int8(const uint8_t* q, const float* q_scale, const uint8_t* w2, const float* w2_scale,
-                             const float* topk_weights, const GroupedRows& g, int H, int I, uint16_t* Y, int tile_m,
+                             const float* topk_weights, const GroupedRows& g, int H, int I, YT* Y, int tile_m,
                              bool packed, hipStream_t stream) {
   if (tile_m == kTileMaxInt8)
     return launch_gemm2_int8_tile(q, q_scale, w2, w2_scale, topk_weights, g, H, I, Y, packed, stream);
   const dim3 grid(grid_for(g, tile_m, H / 32)), block(64 * kStreamWaves);
-#define FP8MOE_LAUNCH(TM)                                                                                          \
-  if (packed)                                                                                                      \
-    hipLaunchKernelGGL((gemm2_stream_int8_kernel<TM, true>), grid, block, 0, stream, q, q_scale, w2, w2_scale,     \
-                       topk_weights, g.padded_indptr, g.sorted_src, g.E, H, I, Y);                                 \
-  else                                                                                                             \
-    hipLaunchKernelGGL((gemm2_stream_int8_kernel<TM, false>), grid, block, 0, stream, q, q_scale, w2, w2_scale,    \
-                       topk_weights, g.padded_indptr, g.sorted_src, g.E, H, I, Y)
+#define FP8MOE_LAUNCH(TM)                                                                                         \
+  if (packed)                                                                                                     \
+    hipLaunchKernelGGL((gemm2_stream_int8_kernel<TM, true, YT>), grid, block, 0, stream, q, q_scale, w2, w2_scale, \
+                       topk_weights, g.padded_indptr, g.sorted_src, g.E, H, I, Y);                                \
+  else                                                                                                            \
+    hipLaunchKernelGGL((gemm2_stream_int8_kernel<TM, false, YT>), grid, block, 0, stream, q, q_scale, w2,         \
+                       w2_scale, topk_weights, g.padded_indptr, g.sorted_src, g.E, H, I, Y)
   FP8MOE_STREAM_TILES(FP8MOE_LAUNCH);
 #undef FP8MOE_LAUNCH
 }
+template hipError_t launch_gemm2_int8(const uint8_t*, const float*, const uint8_t*, const float*, const float*,
+                                      const GroupedRows&, int, int, uint16_t*, int, bool, hipStream_t);
+template hipError_t launch_gemm2_int8(const uint8_t*, const float*, const uint8_t*, const float*, const float*,
+                                      const GroupedRows&, int, int, float*, int, bool, hipStream_t);
 
 hipError_t launch_moe_direct_int8(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
                                   const uint8_t* w2, const float* w2_scale, const int32_t* topk_ids,

@@ -15,6 +15,8 @@
 // LDS buffers, filled by direct-to-LDS loads three K steps ahead; one barrier
 // per K step hands a buffer over.  The fragment reads of a step's first two
 // sub-tiles are issued before the barrier that ends the step ahead of it.
+#include <type_traits>
+
 #include "gemm_kernels.h"
 #include "int8_common.h"
 
@@ -268,13 +270,13 @@ __device__ __forceinline__ void tile_gemm1(const TokenBuffers& tb, RowInfo& ri, 
   tile_mainloop<TM, WM, PACKED>(tb, xrsrc, a_off, rsrc, H, nn, wave, lane, acc, band, epi);
 }
 
-template <int TM, int WM, bool PACKED>
+template <int TM, int WM, bool PACKED, typename YT>
 __device__ __forceinline__ void tile_gemm2(const TokenBuffers& tb, RowInfo& ri, const TileCoord& tc,
                                            const uint8_t* __restrict__ q, const float* __restrict__ q_scale,
                                            const uint8_t* __restrict__ w2, const float* __restrict__ w2_scale,
                                            const float* __restrict__ topk_weights,
                                            const int32_t* __restrict__ sorted_src, int H, int I, int NB,
-                                           uint16_t* __restrict__ Y) {
+                                           YT* __restrict__ Y) {
   using C = TileCfg<TM, WM>;
   constexpr int TS = C::TS, B = C::BANDS;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -314,15 +316,20 @@ __device__ __forceinline__ void tile_gemm2(const TokenBuffers& tb, RowInfo& ri, 
       const int r = 16 * (wm * TS + ts) + l16;
       const int src = ri.src[r];
       const float s = ri.scale[r];
+      YT* row = Y + (size_t)src * H + c0;
       uint2 v[B];
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         float y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = (float)acc[ts][b][i] * (s * ws[b][i]);
-        v[b] = uint2{pack2_bf16(y[0], y[1]), pack2_bf16(y[2], y[3])};
+        if constexpr (std::is_same_v<YT, float>) {
+          if (src >= 0) store_y4(row + 16 * b + 4 * g, y);
+        } else {
+          v[b] = uint2{pack2_bf16(y[0], y[1]), pack2_bf16(y[2], y[3])};
+        }
       }
-      store_row<B>(v, Y + (size_t)src * H + c0, g, src >= 0);
+      if constexpr (!std::is_same_v<YT, float>) store_row<B>(v, row, g, src >= 0);
     }
   };
   i32x4 acc[TS][B];
@@ -365,11 +372,11 @@ __global__ __launch_bounds__(kThreads) void gemm1_tile_int8_kernel(
 #undef FP8MOE_BODY
 }
 
-template <bool PACKED>
+template <bool PACKED, typename YT>
 __global__ __launch_bounds__(kThreads) void gemm2_tile_int8_kernel(
     const uint8_t* __restrict__ q, const float* __restrict__ q_scale, const uint8_t* __restrict__ w2,
     const float* __restrict__ w2_scale, const float* __restrict__ topk_weights, const int32_t* __restrict__ padded,
-    const int32_t* __restrict__ sorted_src, int E, int H, int I, int NB, uint16_t* __restrict__ Y) {
+    const int32_t* __restrict__ sorted_src, int E, int H, int I, int NB, YT* __restrict__ Y) {
   __shared__ __attribute__((aligned(1024))) uint8_t tb0[kTileMaxInt8 * kKB], tb1[kTileMaxInt8 * kKB],
       tb2[kTileMaxInt8 * kKB], tb3[kTileMaxInt8 * kKB];
   __shared__ RowInfo ri;
@@ -378,7 +385,7 @@ __global__ __launch_bounds__(kThreads) void gemm2_tile_int8_kernel(
   TileCoord tc;
   if (!tile_coord<kTileMaxInt8>(padded, sorted_src, E, (NT + NB - 1) / NB, tc)) return;
 #define FP8MOE_BODY(TM, WM) \
-  tile_gemm2<TM, WM, PACKED>(tb, ri, tc, q, q_scale, w2, w2_scale, topk_weights, sorted_src, H, I, NB, Y)
+  tile_gemm2<TM, WM, PACKED, YT>(tb, ri, tc, q, q_scale, w2, w2_scale, topk_weights, sorted_src, H, I, NB, Y)
   FP8MOE_TILE_BODIES(FP8MOE_BODY)
 #undef FP8MOE_BODY
 }
@@ -416,18 +423,24 @@ hipError_t launch_gemm1_int8_tile(const uint8_t* x, const float* x_scale, const 
   return hipGetLastError();
 }
 
+template <typename YT>
 hipError_t launch_gemm2_int8_tile(const uint8_t* q, const float* q_scale, const uint8_t* w2, const float* w2_scale,
-                                  const float* topk_weights, const GroupedRows& g, int H, int I, uint16_t* Y,
+                                  const float* topk_weights, const GroupedRows& g, int H, int I, YT* Y,
                                   bool packed, hipStream_t stream) {
   const int NT = (H + kTN - 1) / kTN, NB = run_int8(g, NT, I / kKB), NG = (NT + NB - 1) / NB;
   const dim3 grid(grid_for(g, kTileMaxInt8, NG)), block(kThreads);
   if (packed)
-    hipLaunchKernelGGL((gemm2_tile_int8_kernel<true>), grid, block, 0, stream, q, q_scale, w2, w2_scale,
+    hipLaunchKernelGGL((gemm2_tile_int8_kernel<true, YT>), grid, block, 0, stream, q, q_scale, w2, w2_scale,
                        topk_weights, g.padded_indptr, g.sorted_src, g.E, H, I, NB, Y);
   else
-    hipLaunchKernelGGL((gemm2_tile_int8_kernel<false>), grid, block, 0, stream, q, q_scale, w2, w2_scale,
+    hipLaunchKernelGGL((gemm2_tile_int8_kernel<false, YT>), grid, block, 0, stream, q, q_scale, w2, w2_scale,
                        topk_weights, g.padded_indptr, g.sorted_src, g.E, H, I, NB, Y);
   return hipGetLastError();
 }
+
+template hipError_t launch_gemm2_int8_tile(const uint8_t*, const float*, const uint8_t*, const float*, const float*,
+                                           const GroupedRows&, int, int, uint16_t*, bool, hipStream_t);
+template hipError_t launch_gemm2_int8_tile(const uint8_t*, const float*, const uint8_t*, const float*, const float*,
+                                           const GroupedRows&, int, int, float*, bool, hipStream_t);
 
 }  // namespace fp8moe

@@ -14,6 +14,14 @@ __device__ __forceinline__ i32x4 mfma16x16x64_i8(const v4i& a, const v4i& b, con
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
+// Four consecutive values of a Y row, as bf16 or as they are.
+__device__ __forceinline__ void store_y4(uint16_t* p, const float (&y)[4]) {
+  *reinterpret_cast<uint2*>(p) = uint2{pack2_bf16(y[0], y[1]), pack2_bf16(y[2], y[3])};
+}
+__device__ __forceinline__ void store_y4(float* p, const float (&y)[4]) {
+  *reinterpret_cast<v4f*>(p) = v4f{y[0], y[1], y[2], y[3]};
+}
+
 // Largest magnitude of eight bf16 values and of m, as bf16 bits (sign
 // cleared): they order as integers, infinity and NaN last.
 __device__ __forceinline__ uint32_t amax8_bits(const uint4& v, uint32_t m) {

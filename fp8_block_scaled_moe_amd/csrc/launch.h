@@ -97,8 +97,10 @@ hipError_t launch_gemm1_int8(const uint8_t* x, const float* x_scale, const uint8
                              hipStream_t stream);
 hipError_t launch_quant_rows_int8(const uint16_t* in, const int32_t* sorted_src, int64_t rows, int N, uint8_t* q,
                                   float* scale, hipStream_t stream);
+// YT: uint16_t (bf16 rows) or float
+template <typename YT>
 hipError_t launch_gemm2_int8(const uint8_t* q, const float* q_scale, const uint8_t* w2, const float* w2_scale,
-                             const float* topk_weights, const GroupedRows& g, int H, int I, uint16_t* Y, int tile_m,
+                             const float* topk_weights, const GroupedRows& g, int H, int I, YT* Y, int tile_m,
                              bool packed, hipStream_t stream);
 
 // The whole layer without routing for at most kDirectMaxRows routed rows of at
@@ -111,8 +113,9 @@ hipError_t launch_moe_direct_int8(const uint8_t* x, const float* x_scale, const 
 // The tile kernels; GEMM1's takes x of less than 4 GiB (hipErrorInvalidValue).
 hipError_t launch_gemm1_int8_tile(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
                                   const GroupedRows& g, int H, int I, uint16_t* act, bool packed, hipStream_t stream);
+template <typename YT>
 hipError_t launch_gemm2_int8_tile(const uint8_t* q, const float* q_scale, const uint8_t* w2, const float* w2_scale,
-                                  const float* topk_weights, const GroupedRows& g, int H, int I, uint16_t* Y,
+                                  const float* topk_weights, const GroupedRows& g, int H, int I, YT* Y,
                                   bool packed, hipStream_t stream);
 
 // Residual addition + RMS norm + quantisation (format: FP8MOE_NORM_*), and the
@@ -145,6 +148,9 @@ hipError_t launch_pack_mx_scales(const uint8_t* in, int64_t E, int N, int K, int
 
 hipError_t launch_combine(const uint16_t* Y, const int32_t* topk_ids, int T, int H, int E, int K,
                           uint16_t* out, hipStream_t stream);
+// The same over fp32 rows.
+hipError_t launch_combine_f32(const float* Y, const int32_t* topk_ids, int T, int H, int E, int K, uint16_t* out,
+                              hipStream_t stream);
 
 // The FP8 layer for small T in one cooperative persistent launch (after the
 // routing launch, which zeroes ctr_err[0..1]): GEMM1 + SwiGLU + requant over

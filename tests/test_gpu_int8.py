@@ -96,7 +96,8 @@ def test_stages(align, tile_m):
     Y = fm.gemm2_weighted_int8(q, qs, d["w2"], d["w2s"], r, d["tw"], T, K, align, tile_m=tile_m)
     out = fm.combine(Y, d["ids"], E)
     torch.cuda.synchronize()
-    assert torch.equal(out, p.run())
+    fused = p.run().cpu().double().numpy()
+    total, size = np.zeros((T, H)), np.zeros((T, H))
     src = r["sorted_src"].cpu().numpy()
     pos = np.flatnonzero(src >= 0)
     s = src[pos]
@@ -120,6 +121,12 @@ def test_stages(align, tile_m):
         y = O8.int8_product(qn[rows], qsn[rows], p.w2.numpy()[x], p.w2s.numpy()[x])
         y *= p.tw.numpy().astype(np.float64).reshape(-1)[src[rows]][:, None]
         assert np.all(np.abs(Yn[src[rows]] - y) <= np.abs(y) * (2.0 ** -8 + 6 * 2.0 ** -24) + 1e-38)
+        np.add.at(total, tok, y)
+        np.add.at(size, tok, np.abs(y))
+    # the layer keeps these few rows in fp32: its output is one bf16 rounding of their sum (K fp32 roundings of it)
+    assert np.all(np.abs(fused - total) <= np.abs(total) * 2.0 ** -8 + size * (6 + K) * 2.0 ** -23)
+    # the stages' Y is bf16: one rounding more per slot
+    assert np.all(np.abs(out.cpu().double().numpy() - total) <= np.abs(total) * 2.0 ** -8 + size * 2.0 ** -8 * 1.01)
     # rows of padding and of dropped slots are left alone
     pad = np.flatnonzero(src < 0)
     assert not a[pad].any() and not qn[pad].any() and not qsn[pad].any()
@@ -229,6 +236,17 @@ def test_streams_graph_and_poisoned_workspace():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, p.run(packed=True))
+
+
+@pytest.mark.parametrize("T", [1024, 1025])
+def test_rows_kept_in_fp32_and_in_bf16(T):
+    """T * K * H at the border between the two: the same output to a bf16 step of each slot."""
+    p = Problem(T, 1024, 128, 16, 4, seed=4)
+    ref = p.oracle()
+    first = p.run()
+    assert_rows_close_to_oracle(first, ref, f"int8 Y T={T}")
+    for tm in TILES:
+        assert torch.equal(p.run(tm), first)
 
 
 def test_offsets_beyond_32_bits():
