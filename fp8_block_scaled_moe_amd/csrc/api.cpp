@@ -988,7 +988,7 @@ int moe_fused_int8(const void* x, const float* x_scale, const void* w13, const f
     return ok();
   }
   hipError_t err = launch_route_permute(topk_ids, (int)P.R, E, P.align, (int)P.cap, P.counts, P.m_indptr, P.padded,
-                                        P.sorted_src, P.src_to_sorted, s);
+                                        P.sorted_src, P.src_to_sorted, s, nullptr, false);
   if (err != hipSuccess) return hip_fail(err, "route_permute launch");
   GroupedRows g{P.padded, P.sorted_src, P.cap, E, K, P.R, device_num_cu()};
   err = launch_gemm1_int8(static_cast<const uint8_t*>(x), x_scale, static_cast<const uint8_t*>(w13), w13_scale, g, H,

@@ -340,6 +340,137 @@ __device__ __forceinline__ void tile_gemm2(const TokenBuffers& tb, RowInfo& ri, 
   tile_mainloop<TM, WM, PACKED>(tb, qrsrc, a_off, rsrc, I, nn, wave, lane, acc, band, epi);
 }
 
+// Work item `slot` of XCD x (workgroup b runs on XCD b % 8).  Experts of one M
+// tile go to the XCD of their index modulo 8 with all their N runs, which share
+// the token rows through its L2; the tiles of experts with more are dealt out
+// evenly, a contiguous range of (expert, run, M tile) to each XCD, so that M
+// tiles that share weights meet in one L2.  Equal counts of one list of all
+// tiles, as the other formats' kernels deal them, give one XCD the tall tiles
+// of popular experts and another the short ones: Zipf 1.2 routing (H=2048,
+// I=768, E=128, top-8) took 171 us at T=512 and 398 at T=4096 that way.
+// The range's tiles come first, being the tall ones.
+template <int TMAX>
+struct TileChunk {   // experts c + 4 lane .. + 3: their rows and tile counts (0 past E)
+  int start[5], nt[4];
+  __device__ __forceinline__ void load(const int32_t* __restrict__ padded, int E, int c, int lane) {
+    const int e0 = c + 4 * lane;
+#pragma unroll
+    for (int k = 0; k < 5; ++k) start[k] = padded[min(e0 + k, E)];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) nt[k] = e0 + k < E ? tiles_of<TMAX>(start[k + 1] - start[k]) : 0;
+  }
+  // inclusive prefix over the lanes of the tiles of experts with more than one
+  __device__ __forceinline__ int many(int lane) const {
+    int sum = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum += nt[k] > 1 ? nt[k] : 0;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(sum, o);
+      if (lane >= o) sum += v;
+    }
+    return sum;
+  }
+  // lanes that hold an expert of one tile and of residue x = 4 (lane % 2) + k
+  __device__ __forceinline__ uint64_t single(int x) const {
+    uint64_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t b = __ballot(nt[k] == 1);
+      if ((x & 3) == k) m = b;
+    }
+    return m & (x & 4 ? 0xaaaaaaaaaaaaaaaaull : 0x5555555555555555ull);
+  }
+  // expert k of lane `own` -> its first and last row and tile count, uniform
+  __device__ __forceinline__ void expert(int own, int k, int& s0, int& s1, int& n) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (k == i) {
+        s0 = __builtin_amdgcn_readlane(start[i], own);
+        s1 = __builtin_amdgcn_readlane(start[i + 1], own);
+        n = __builtin_amdgcn_readlane(nt[i], own);
+      }
+  }
+};
+
+template <int TMAX>
+__device__ __forceinline__ bool tile_item(const int32_t* __restrict__ padded,
+                                              const int32_t* __restrict__ sorted_src, int E, int NG, int x, int slot,
+                                              TileCoord& tc) {
+  const int lane = threadIdx.x & 63;
+  TileChunk<TMAX> ch;
+  int many = 0;
+  for (int c = 0; c < E; c += 256) {
+    ch.load(padded, E, c, lane);
+    many += __builtin_amdgcn_readlane(ch.many(lane), 63);
+  }
+  const int share = (many * NG + kNumXcd - 1) / kNumXcd;
+  const int a0 = min(x * share, many * NG), a1 = min(a0 + share, many * NG);
+  int c = 0, own = 0, k = 0, mt = 0, s0 = 0, s1 = 0, nm = 1;
+  if (slot < a1 - a0) {
+    const int t = (a0 + slot) / NG;   // its tile among those of experts with more than one
+    int base = 0, incl;
+    for (;; c += 256) {
+      ch.load(padded, E, c, lane);
+      incl = ch.many(lane);
+      const int total = __builtin_amdgcn_readlane(incl, 63);
+      if (base + total > t) break;   // t < many, so this stops at a chunk of the experts
+      base += total;
+    }
+    own = __builtin_amdgcn_readfirstlane(__popcll(__ballot(base + incl <= t)));
+    int first = base + (own ? __builtin_amdgcn_readlane(incl, own - 1) : 0);
+    int o_nt[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = __builtin_amdgcn_readlane(ch.nt[i], own);
+      o_nt[i] = n > 1 ? n : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i)   // skip the lane's experts whose tiles all precede t
+      if (k == i && first + o_nt[i] <= t) {
+        first += o_nt[i];
+        k = i + 1;
+      }
+    ch.expert(own, k, s0, s1, nm);
+    const int j = a0 + slot - NG * first;
+    tc.run = j / nm;
+    mt = j - tc.run * nm;
+  } else {
+    const int rest = slot - (a1 - a0);
+    int ord = rest / NG;   // its expert among the XCD's of one tile
+    tc.run = rest - ord * NG;
+    uint64_t m = 0;
+    for (;; c += 256) {
+      if (c >= E) return false;
+      ch.load(padded, E, c, lane);
+      m = ch.single(x);
+      const int n = __popcll(m);
+      if (ord < n) break;
+      ord -= n;
+    }
+    const bool mine = (m >> lane & 1) && __popcll(m & ((1ull << lane) - 1)) == ord;
+    own = __builtin_amdgcn_readfirstlane(__ffsll((long long)__ballot(mine)) - 1);
+    k = x & 3;
+    ch.expert(own, k, s0, s1, nm);
+  }
+  const int len = s1 - s0;
+  tc.mt = mt;
+  tc.tm = ((len + nm - 1) / nm + 15) / 16 * 16;
+  tc.p0 = s0 + mt * tc.tm;
+  tc.h = min(tc.tm, len - mt * tc.tm);
+  tc.e = c + 4 * own + k;
+  return sorted_src[tc.p0] >= 0;   // false: segment padding only, nothing to compute
+}
+
+// Workgroups for every possible item; those past the actual ones (known on the
+// device only) exit at once.  An expert of more than one tile has more than
+// TMAX padded rows, so their tiles are at most twice the padded rows / TMAX.
+static unsigned tile_grid(const GroupedRows& g, int NG) {
+  const int64_t singles = (g.E < g.rows ? (g.E + kNumXcd - 1) / kNumXcd : g.rows) * NG;
+  const int64_t many = (2 * g.cap / kTileMaxInt8 * NG + kNumXcd - 1) / kNumXcd;
+  return (unsigned)(kNumXcd * (singles + many));
+}
+
 // one uniform branch per workgroup on its tile height, in steps of 32 rows
 #define FP8MOE_TILE_BODIES(BODY)       \
   switch ((tc.tm + 31) / 32) {         \
@@ -365,7 +496,9 @@ __global__ __launch_bounds__(kThreads) void gemm1_tile_int8_kernel(
   const TokenBuffers tb{{tb0, tb1, tb2, tb3}};
   const int NT = I / 128;
   TileCoord tc;
-  if (!tile_coord<kTileMaxInt8>(padded, sorted_src, E, (NT + NB - 1) / NB, tc)) return;
+  if (!tile_item<kTileMaxInt8>(padded, sorted_src, E, (NT + NB - 1) / NB, blockIdx.x % kNumXcd, blockIdx.x / kNumXcd,
+                               tc))
+    return;
 #define FP8MOE_BODY(TM, WM) \
   tile_gemm1<TM, WM, PACKED>(tb, ri, tc, x, x_scale, w13, w13_scale, sorted_src, K, H, I, NB, x_bytes, act)
   FP8MOE_TILE_BODIES(FP8MOE_BODY)
@@ -383,7 +516,9 @@ __global__ __launch_bounds__(kThreads) void gemm2_tile_int8_kernel(
   const TokenBuffers tb{{tb0, tb1, tb2, tb3}};
   const int NT = (H + kTN - 1) / kTN;
   TileCoord tc;
-  if (!tile_coord<kTileMaxInt8>(padded, sorted_src, E, (NT + NB - 1) / NB, tc)) return;
+  if (!tile_item<kTileMaxInt8>(padded, sorted_src, E, (NT + NB - 1) / NB, blockIdx.x % kNumXcd, blockIdx.x / kNumXcd,
+                               tc))
+    return;
 #define FP8MOE_BODY(TM, WM) \
   tile_gemm2<TM, WM, PACKED, YT>(tb, ri, tc, q, q_scale, w2, w2_scale, topk_weights, sorted_src, H, I, NB, Y)
   FP8MOE_TILE_BODIES(FP8MOE_BODY)
@@ -413,7 +548,7 @@ hipError_t launch_gemm1_int8_tile(const uint8_t* x, const float* x_scale, const 
   if (g.rows / g.K * H >= (int64_t)1 << 32) return hipErrorInvalidValue;   // x: 32-bit offsets of its rows
   const uint32_t x_bytes = (uint32_t)(g.rows / g.K * H);
   const int NT = I / 128, NB = run_int8(g, NT, H / kKB), NG = (NT + NB - 1) / NB;
-  const dim3 grid(grid_for(g, kTileMaxInt8, NG)), block(kThreads);
+  const dim3 grid(tile_grid(g, NG)), block(kThreads);
   if (packed)
     hipLaunchKernelGGL((gemm1_tile_int8_kernel<true>), grid, block, 0, stream, x, x_scale, w13, w13_scale,
                        g.padded_indptr, g.sorted_src, g.E, g.K, H, I, NB, x_bytes, act);
@@ -428,7 +563,7 @@ hipError_t launch_gemm2_int8_tile(const uint8_t* q, const float* q_scale, const 
                                   const float* topk_weights, const GroupedRows& g, int H, int I, YT* Y,
                                   bool packed, hipStream_t stream) {
   const int NT = (H + kTN - 1) / kTN, NB = run_int8(g, NT, I / kKB), NG = (NT + NB - 1) / NB;
-  const dim3 grid(grid_for(g, kTileMaxInt8, NG)), block(kThreads);
+  const dim3 grid(tile_grid(g, NG)), block(kThreads);
   if (packed)
     hipLaunchKernelGGL((gemm2_tile_int8_kernel<true, YT>), grid, block, 0, stream, q, q_scale, w2, w2_scale,
                        topk_weights, g.padded_indptr, g.sorted_src, g.E, H, I, NB, Y);

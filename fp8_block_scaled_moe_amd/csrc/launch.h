@@ -25,12 +25,14 @@ size_t route_lds_bytes(int E);
 // zero2 (nullable): kSmallBarrierWords words the one-workgroup path
 // (R <= 4096) sets to zero in the same launch (the small-T layer's barrier
 // counters and error flag); hipErrorInvalidValue if given with more rows.
+// inverse false: the caller does not read src_to_sorted, which then holds
+// anything where there are many rows (its launch is left out).
 constexpr int kRouteOneBlockRows = 4096;
 constexpr int kSmallBarrierWords = 16;   // 8 group counters, the top counter, the error flag, spare
 hipError_t launch_route_permute(const int32_t* ids, int R, int E, int align, int cap,
                                 int32_t* counts, int32_t* m_indptr, int32_t* padded_indptr,
                                 int32_t* sorted_src, int32_t* src_to_sorted, hipStream_t stream,
-                                uint32_t* zero2 = nullptr);
+                                uint32_t* zero2 = nullptr, bool inverse = true);
 
 // Largest tile heights.  GEMM2's body fits 256 VGPRs up to 160 rows.  GEMM1's
 // body (with its SwiGLU/requant epilogue) reaches the VGPR limit at 144 rows

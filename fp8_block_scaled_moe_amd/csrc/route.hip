@@ -253,7 +253,7 @@ __global__ __launch_bounds__(256) void route_inverse_kernel(const int32_t* __res
 hipError_t launch_route_permute(const int32_t* ids, int R, int E, int align, int cap,
                                 int32_t* counts, int32_t* m_indptr, int32_t* padded_indptr,
                                 int32_t* sorted_src, int32_t* src_to_sorted, hipStream_t stream,
-                                uint32_t* zero2) {
+                                uint32_t* zero2, bool inverse) {
   const size_t lds = route_lds_bytes(E);
   // raise the dynamic-LDS limit once (thread-safe static initialisation)
   static const hipError_t attr = hipFuncSetAttribute((const void*)route_permute_kernel,
@@ -284,6 +284,7 @@ hipError_t launch_route_permute(const int32_t* ids, int R, int E, int align, int
                      m_indptr, padded_indptr);
   hipLaunchKernelGGL(route_place_kernel, dim3(C), dim3(kRouteThreads), (2 + kRouteWaves) * e_bytes, stream, ids,
                      R, E, cap, cc, counts, padded_indptr, sorted_src);
+  if (!inverse) return hipGetLastError();
   const int inv_blocks = (R + 255) / 256 < 2048 ? (R + 255) / 256 : 2048;
   hipLaunchKernelGGL(route_inverse_kernel, dim3(inv_blocks), dim3(256), 0, stream, ids, R, E, padded_indptr,
                      sorted_src, src_to_sorted);
