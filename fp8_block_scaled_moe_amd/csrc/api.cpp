@@ -931,8 +931,8 @@ int moe_router_topk(const void* logits, int32_t logits_bf16, const float* bias, 
                     int32_t score, int32_t n_group, int32_t topk_group, int32_t group_top, int32_t renormalize,
                     float scale, int32_t* topk_ids, float* topk_weights, void* stream) {
   if (T < 0 || E < 1) return fail(FP8MOE_ERR_SHAPE, "invalid T=%lld E=%d", (long long)T, E);
-  if (E > FP8MOE_MAX_EXPERTS || T >= ((int64_t)1 << 26))
-    return fail(FP8MOE_ERR_LIMIT, "E=%d must be at most %d and T=%lld below 2^26", E, FP8MOE_MAX_EXPERTS,
+  if (E > FP8MOE_MAX_EXPERTS || T >= ((int64_t)1 << 25))
+    return fail(FP8MOE_ERR_LIMIT, "E=%d must be at most %d and T=%lld below 2^25", E, FP8MOE_MAX_EXPERTS,
                 (long long)T);
   if (score != FP8MOE_SCORE_SOFTMAX && score != FP8MOE_SCORE_SIGMOID)
     return fail(FP8MOE_ERR_ARG, "score %d not 0 or 1", score);
@@ -949,6 +949,11 @@ int moe_router_topk(const void* logits, int32_t logits_bf16, const float* bias, 
                 FP8MOE_MAX_ROUTER_TOPK, E / n_group * topk_group);
   if (T == 0) return ok();
   if (!logits || !topk_ids || !topk_weights) return fail(FP8MOE_ERR_NULL, "null tensor argument");
+  const int64_t nl = T * E * (logits_bf16 ? 2 : 4), nb = (int64_t)E * 4, no = T * K * 4;
+  if (overlap(topk_ids, no, logits, nl) || overlap(topk_weights, no, logits, nl) ||
+      overlap(topk_ids, no, bias, nb) || overlap(topk_weights, no, bias, nb) ||
+      overlap(topk_ids, no, topk_weights, no))
+    return fail(FP8MOE_ERR_SHAPE, "an output overlaps an input or the other output");
   hipError_t err = launch_router_topk(logits, logits_bf16 != 0, bias, (int)T, E, K, score, n_group, topk_group,
                                       group_top, renormalize != 0, scale, topk_ids, topk_weights,
                                       (hipStream_t)stream);
@@ -974,7 +979,8 @@ int moe_fused_int8(const void* x, const float* x_scale, const void* w13, const f
   if (st) return st;
   if ((st = check_int8_stage(T, H, I, E, K, kFusedAlign, 0, tile_m, weight_layout))) return st;
   if (T == 0) return ok();
-  if (!aligned16(x) || !aligned16(w13) || !aligned16(w2) || !aligned16(out))
+  if (!aligned16(x) || !aligned16(w13) || !aligned16(w2) || !aligned16(out) || !aligned16(w13_scale) ||
+      !aligned16(w2_scale))
     return fail(FP8MOE_ERR_ALIGN, "tensors must be 16-byte aligned");
   const int tm1 = int8_tile_m(tile_m, P.R, E, I / 128), tm2 = int8_tile_m(tile_m, P.R, E, (H + 255) / 256);
   hipStream_t s = (hipStream_t)stream;
@@ -1021,7 +1027,7 @@ int moe_gemm1_swiglu_int8(const void* x, const float* x_scale, const void* w13, 
   if (T == 0 || cap == 0) return ok();
   if (!x || !x_scale || !w13 || !w13_scale || !padded_indptr || !sorted_src || !act)
     return fail(FP8MOE_ERR_NULL, "null tensor argument");
-  if (!aligned16(x) || !aligned16(w13) || !aligned16(act))
+  if (!aligned16(x) || !aligned16(w13) || !aligned16(w13_scale) || !aligned16(act))
     return fail(FP8MOE_ERR_ALIGN, "tensors must be 16-byte aligned");
   GroupedRows g{padded_indptr, sorted_src, cap, E, K, T * K, device_num_cu()};
   hipError_t err = launch_gemm1_int8(static_cast<const uint8_t*>(x), x_scale, static_cast<const uint8_t*>(w13),
@@ -1057,7 +1063,7 @@ int moe_gemm2_weighted_int8(const void* q, const float* q_scale, const void* w2,
   if (T == 0 || cap == 0) return ok();
   if (!q || !q_scale || !w2 || !w2_scale || !padded_indptr || !sorted_src || !topk_weights || !Y)
     return fail(FP8MOE_ERR_NULL, "null tensor argument");
-  if (!aligned16(q) || !aligned16(w2) || !aligned16(Y))
+  if (!aligned16(q) || !aligned16(w2) || !aligned16(w2_scale) || !aligned16(Y))
     return fail(FP8MOE_ERR_ALIGN, "tensors must be 16-byte aligned");
   GroupedRows g{padded_indptr, sorted_src, cap, E, K, T * K, device_num_cu()};
   hipError_t err = launch_gemm2_int8(static_cast<const uint8_t*>(q), q_scale, static_cast<const uint8_t*>(w2),

@@ -22,7 +22,7 @@
 // fp64.  As the only path it measured 31 us for 8192 tokens of 256 experts in
 // groups, 121 us for 65537 tokens of 128.
 //
-// Fast path (route_fast): L = 16 lanes per token (64 beyond 256 experts or 15
+// Fast path (route_fast): L = 16 lanes per token (64 beyond 256 experts or 14
 // slots), lane l holds experts l NV .. l NV + NV - 1, choices in fp32.  Each is
 // a 32-bit key: the order-preserving bits of the choice with the lowest
 // IB replaced by the complement of the expert's index, so keys are unique, the
@@ -546,14 +546,14 @@ static void router_launch(const RouterArgs& a, bool bf16, hipStream_t stream) {
 hipError_t launch_router_topk(const void* logits, bool bf16, const float* bias, int T, int E, int K, int score,
                               int n_group, int topk_group, int group_top, bool renormalize, float scale,
                               int32_t* ids, float* weights, hipStream_t stream) {
-  // The fast path's rows: 16 lanes up to 256 experts and 15 slots (one more
-  // lane holds the expert behind the last slot), else 64.  Groups have to be
-  // whole lanes, a power of two of them.
-  const int L = E <= 256 && K < 16 ? 16 : 64;
+  // The fast path's rows: 16 lanes up to 256 experts and 14 slots, else 64 (at
+  // least one further candidate has a lane).  Groups have to be whole lanes, a
+  // power of two of them.
+  const int L = E <= 256 && K < 15 ? 16 : 64;
   const int NV = L == 16 ? (E <= 64 ? 4 : E <= 128 ? 8 : 16) : E <= 512 ? 8 : 16;
   const int per = E / n_group, gl = per / NV;
   const bool whole = n_group == 1 || (per % NV == 0 && (gl & (gl - 1)) == 0);
-  const bool fast = K < L && whole;
+  const bool fast = K < L - 1 && whole;
   const bool vec = E == L * NV && (uintptr_t)logits % 16 == 0 && (uintptr_t)bias % 16 == 0;
   const RouterArgs a{logits, bias, T, E, K, score, n_group, topk_group, group_top, (int)renormalize, (int)vec,
                      scale, ids, weights};

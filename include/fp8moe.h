@@ -46,7 +46,8 @@ extern "C" {
 #define FP8MOE_ERR_SHAPE       -2  /* a size is negative, zero where it must not be,
                                       or overflows the int32 row index space         */
 #define FP8MOE_ERR_ALIGN       -3  /* H or I not a multiple of 128; N not of 32;
-                                      align not in {16,32,64,128}                     */
+                                      align not in {16,32,64,128}; a pointer of the
+                                      norm or the int8 layer not 16-byte aligned      */
 #define FP8MOE_ERR_TOPK        -4  /* top-k K outside [1, E]                          */
 #define FP8MOE_ERR_TILE        -5  /* tile_m / tile_n / variant not supported         */
 #define FP8MOE_ERR_WORKSPACE   -6  /* workspace NULL, too small or not 256-B aligned  */
@@ -418,8 +419,8 @@ int add_rmsnorm_quant(const void* x, const void* residual, int32_t residual_f32,
  *                equal ones in ascending index
  *   topk_weights score_e (without the bias), divided by the chosen ones' sum if
  *                renormalize != 0 (0 where that sum is 0), times scale
- * Which experts are chosen is decided as if in 64 bits; weights are rounded to
- * fp32 once.
+ * Which experts are chosen is decided as if in 64 bits; weights are computed in
+ * fp32.
  *
  *   logits  fp32 or bf16 (logits_bf16 != 0) [T, E]
  *   bias    fp32 [E] or NULL
@@ -431,8 +432,9 @@ int add_rmsnorm_quant(const void* x, const void* residual, int32_t residual_f32,
  * Limits: 1 <= E <= FP8MOE_MAX_EXPERTS; 1 <= K <= min(FP8MOE_MAX_ROUTER_TOPK,
  * topk_group * E / n_group) (FP8MOE_ERR_TOPK); n_group divides E and is at most
  * FP8MOE_MAX_ROUTER_GROUPS, 1 <= topk_group <= n_group, group_top at most
- * E / n_group (FP8MOE_ERR_ARG); T < 2^26 (FP8MOE_ERR_LIMIT); scale finite.  With
- * n_group == 1, topk_group is 1 and group_top is 1 or 2 and not used.
+ * E / n_group (FP8MOE_ERR_ARG); T < 2^25 (FP8MOE_ERR_LIMIT); scale finite.  With
+ * n_group == 1, topk_group is 1 and group_top is 1 or 2 and not used.  No
+ * output overlaps an input or the other output (FP8MOE_ERR_SHAPE).
  */
 #define FP8MOE_SCORE_SOFTMAX 0
 #define FP8MOE_SCORE_SIGMOID 1
@@ -462,7 +464,8 @@ int moe_router_topk(const void* logits, int32_t logits_bf16, const float* bias, 
  * moe_quant_rows_int8 also serves rows of any bf16 matrix: `in` bf16 [rows, N]
  * -> q int8 [rows, N], scale fp32 [rows], N a multiple of 8, sorted_src NULL;
  * no overlap (FP8MOE_ERR_SHAPE).
- * x, w13, w2, act, in, q, Y and out are 16-byte aligned (FP8MOE_ERR_ALIGN).
+ * x, w13, w2, their weight scales, act, in, q, Y and out are 16-byte aligned
+ * (FP8MOE_ERR_ALIGN).
  * tile_m: -1 (auto) or 16, 32, 64, 288: the largest number of token rows per
  * tile.
  * With FP8MOE_WEIGHTS_MFMA_TILED the weights are packed by moe_pack_weights.

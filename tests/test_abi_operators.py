@@ -58,7 +58,7 @@ def router(logits=P(0), bf16=0, bias=P(1), T=4, E=64, K=4, score=0, n_group=1, t
 
 def test_router_validation():
     assert router(T=-1) == E_SHAPE and router(E=0) == E_SHAPE
-    assert router(E=1025) == E_LIMIT and router(T=1 << 26) == E_LIMIT
+    assert router(E=1025) == E_LIMIT and router(T=1 << 25) == E_LIMIT
     assert router(K=0) == E_TOPK and router(K=65) == E_TOPK and router(K=5, E=4) == E_TOPK
     assert router(K=17, n_group=4, topk_group=1) == E_TOPK
     assert router(score=2) == E_ARG and router(score=-1) == E_ARG
@@ -69,6 +69,8 @@ def test_router_validation():
     assert router(scale=float("nan")) == E_ARG and router(scale=float("inf")) == E_ARG
     for k in ("logits", "ids", "w"):
         assert router(**{k: NULL}) == E_NULL
+    assert router(ids=P(0)) == E_SHAPE and router(w=P(1)) == E_SHAPE and router(w=P(2)) == E_SHAPE
+    assert router(w=ctypes.c_void_p((3 << 34) + 4 * 4 * 4 - 4)) == E_SHAPE
     assert router(T=0, logits=NULL, bias=NULL, ids=NULL, w=NULL) == OK
 
 
@@ -87,6 +89,10 @@ def test_int8_validation():
     assert fused(ptr=ctypes.c_void_p((1 << 34) + 8)) == E_ALIGN
     assert fused(ws=NULL) == E_WS and fused(wsb=1024) == E_WS and fused(ws=ctypes.c_void_p(0x1010)) == E_WS
     assert fused(T=0, ptr=NULL, ws=NULL, out=NULL) == OK
+    p, odd = P(0), ctypes.c_void_p((1 << 34) + 4)
+    for scales in ((odd, p), (p, odd)):
+        assert lib().moe_fused_int8(p, p, p, scales[0], p, scales[1], p, p, 16, 256, 128, 4, 2, P(2), P(1), 1 << 40, -1,
+                                    0, NULL) == E_ALIGN
     n = fm.fused_int8_workspace_size(16, 256, 128, 4, 2)
     cap, R = 32 + 4 * 15, 32
     assert n >= cap * 128 * 3 + cap * 8 + R * 256 * 2

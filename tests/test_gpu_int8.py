@@ -61,6 +61,8 @@ LAYERS = [dict(T=16, H=256, I=128, E=4, K=2), dict(T=1, H=128, I=128, E=1, K=1),
           dict(T=33, H=640, I=384, E=8, K=3, skew=1.2), dict(T=257, H=384, I=256, E=3, K=2, skew=1.2),
           dict(T=700, H=256, I=640, E=5, K=2, skew=1.2, drop=0.3), dict(T=65, H=896, I=128, E=300, K=2),
           dict(T=1300, H=512, I=256, E=2, K=1),
+          # more experts than one round of the tile kernels' search, some of more than one tile
+          dict(T=1700, H=128, I=128, E=600, K=2, skew=1.2), dict(T=2100, H=128, I=128, E=1024, K=1, skew=1.5),
           # a handful of rows: without routing, the largest of them, with dropped slots and beyond
           dict(T=1, H=384, I=1408, E=64, K=8), dict(T=2, H=512, I=768, E=128, K=8, skew=1.2),
           dict(T=5, H=128, I=2048, E=128, K=3, drop=0.4), dict(T=16, H=256, I=128, E=128, K=1),
@@ -149,6 +151,21 @@ def test_largest_sums_are_exact(H, low):
     want = h / (1 + np.exp(-h)) * h
     live = r["sorted_src"].cpu() >= 0
     assert np.all(np.abs(act.cpu()[live].double().numpy() - want) <= want * (2.0 ** -8 + 40 * 2.0 ** -24))
+
+
+@pytest.mark.parametrize("T,E", [(4, 64), (90, 4)])
+def test_repeated_and_foreign_experts(T, E):
+    """The same expert in several slots of a token, and ids on both sides of [0, E)."""
+    p = Problem(T, 256, 128, E, 4, seed=6)
+    p.ids[:, 1] = p.ids[:, 0]
+    p.ids[1] = 3
+    p.ids[2, 2:] = torch.tensor([-7, E], dtype=torch.int32)
+    p.d["ids"].copy_(p.ids)
+    ref = p.oracle()
+    first = p.run()
+    assert_rows_close_to_oracle(first, ref, f"int8 repeated ids T={T}")
+    for tm in TILES:
+        assert torch.equal(p.run(tm, packed=True), first)
 
 
 def test_all_slots_dropped_and_no_tokens():
