@@ -46,34 +46,35 @@ def _u8(t):
     return t
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+def _check(t, dtype, shape, index, name):
+    """t is a contiguous tensor of this dtype and shape on device `index`; one expression, as small calls
+    are bound by the host."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == index and t.shape == shape
+            and t.is_contiguous()):
+        _need(t, dtype, name, len(shape))
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        raise ValueError(f"{name} is on {t.device}, not on device {index}")
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _launch(dev, fn, *args):
+def _launch(index, fn, *args):
     """fn(*args, stream): the call goes to its tensors' device, whichever is current, on that device's
     current stream."""
-    if torch.cuda.current_device() != dev.index:
-        with torch.cuda.device(dev):
-            return check(fn(*args, _current_raw_stream(dev.index)))
-    return check(fn(*args, _current_raw_stream(dev.index)))
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return check(fn(*args, _current_raw_stream(index)))
+    return check(fn(*args, _current_raw_stream(index)))
 
 
-def _out(t, shape, dtype, name, dev):
-    """The caller's output tensor, checked, or a new one."""
+def _out(t, dtype, shape, x, name):
+    """The caller's output tensor, checked, or a new one beside x."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need(t, dtype, name)
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+        return torch.empty(shape, dtype=dtype, device=x.device)
+    _check(t, dtype, shape, x.get_device(), name)
     return t
 
 
@@ -620,35 +621,37 @@ def moe_fused_int8(x, x_scale, w13, w13_scale, w2, w2_scale, topk_ids, topk_weig
     [E, 2I], w2 int8 [E, H, I] with w2_scale [E, H], scales fp32.  Returns bf16 [T, H].
     weight_layout 1: w13 and w2 packed by pack_weights."""
     _need(x, torch.int8, "x", 2)
-    _need(x_scale, torch.float32, "x_scale", 1)
     _need(w13, torch.int8, "w13", 3)
-    _need(w13_scale, torch.float32, "w13_scale", 2)
-    _need(w2, torch.int8, "w2", 3)
-    _need(w2_scale, torch.float32, "w2_scale", 2)
     _need(topk_ids, torch.int32, "topk_ids", 2)
-    _need(topk_weights, torch.float32, "topk_weights", 2)
     T, H = x.shape
-    E, I2, H2 = w13.shape
+    E, I2, _ = w13.shape
     I = I2 // 2
     K = topk_ids.shape[1]
-    if H2 != H or w2.shape != (E, H, I) or I2 != 2 * I:
-        raise ValueError("inconsistent x / w13 / w2 shapes")
-    if x_scale.shape != (T,) or w13_scale.shape != (E, I2) or w2_scale.shape != (E, H):
-        raise ValueError("inconsistent scale shapes")
-    if topk_ids.shape != (T, K) or topk_weights.shape != (T, K):
-        raise ValueError("topk_ids / topk_weights must be [T, K]")
-    dev = x.device
-    _same_device(dev, x_scale=x_scale, w13=w13, w13_scale=w13_scale, w2=w2, w2_scale=w2_scale, topk_ids=topk_ids,
-                 topk_weights=topk_weights, workspace=workspace)
-    out = _out(out, (T, H), torch.bfloat16, "out", dev)
+    index = x.get_device()
+    _check(w13, torch.int8, (E, 2 * I, H), index, "w13")
+    _check(w2, torch.int8, (E, H, I), index, "w2")
+    _check(x_scale, torch.float32, (T,), index, "x_scale")
+    _check(w13_scale, torch.float32, (E, I2), index, "w13_scale")
+    _check(w2_scale, torch.float32, (E, H), index, "w2_scale")
+    _check(topk_ids, torch.int32, (T, K), index, "topk_ids")
+    _check(topk_weights, torch.float32, (T, K), index, "topk_weights")
+    out = _out(out, torch.bfloat16, (T, H), x, "out")
     if workspace is None:
-        workspace = alloc_workspace_int8(T, H, I, E, K, dev)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _launch(dev, lib().moe_fused_int8, _ptr(x), _ptr(x_scale), _ptr(w13), _ptr(w13_scale), _ptr(w2),
-            _ptr(w2_scale), _ptr(topk_ids), _ptr(topk_weights), T, H, I, E, K, _ptr(out), _ptr(workspace),
-            workspace.nbytes, tile_m, weight_layout)
+        workspace = alloc_workspace_int8(T, H, I, E, K, x.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the tensors' device")
+    _launch(index, lib().moe_fused_int8, x.data_ptr(), x_scale.data_ptr(), w13.data_ptr(), w13_scale.data_ptr(),
+            w2.data_ptr(), w2_scale.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), T, H, I, E, K,
+            out.data_ptr(), workspace.data_ptr(), workspace.nbytes, tile_m, weight_layout)
     return out
+
+
+def _route_on(route, index, E=None):
+    """A routing result's arrays, checked (of E experts, if given); returns (padded_indptr, sorted_src, cap)."""
+    padded, src = route["padded_indptr"], route["sorted_src"]
+    _check(padded, torch.int32, (padded.numel() if E is None else E + 1,), index, "padded_indptr")
+    _check(src, torch.int32, (src.numel(),), index, "sorted_src")
+    return padded, src, src.numel()
 
 
 def gemm1_swiglu_int8(x, x_scale, w13, w13_scale, route, T, K, align, tile_m=-1, weight_layout=WEIGHTS_ROW_MAJOR,
@@ -656,21 +659,19 @@ def gemm1_swiglu_int8(x, x_scale, w13, w13_scale, route, T, K, align, tile_m=-1,
     """Int8 GEMM1 + SwiGLU stage.  Returns act bf16 [cap, I]; rows of padding are not written (zero
     when act is allocated here)."""
     _need(x, torch.int8, "x", 2)
-    _need(x_scale, torch.float32, "x_scale", 1)
     _need(w13, torch.int8, "w13", 3)
-    _need(w13_scale, torch.float32, "w13_scale", 2)
     E, I2, H = w13.shape
     I = I2 // 2
-    cap = route["sorted_src"].numel()
-    dev = x.device
-    if x.shape != (T, H) or x_scale.shape != (T,) or w13_scale.shape != (E, I2) or I2 != 2 * I:
-        raise ValueError("inconsistent x / w13 / scale shapes")
-    _same_device(dev, x_scale=x_scale, w13=w13, w13_scale=w13_scale, route=route["sorted_src"])
-    act = torch.zeros((cap, I), dtype=torch.bfloat16, device=dev) if act is None else act
-    act = _out(act, (cap, I), torch.bfloat16, "act", dev)
-    _launch(dev, lib().moe_gemm1_swiglu_int8, _ptr(x), _ptr(x_scale), _ptr(w13), _ptr(w13_scale),
-            _ptr(route["padded_indptr"]), _ptr(route["sorted_src"]), T, H, I, E, K, align, _ptr(act), cap,
-            tile_m, weight_layout)
+    index = x.get_device()
+    _check(x, torch.int8, (T, H), index, "x")
+    _check(w13, torch.int8, (E, 2 * I, H), index, "w13")
+    _check(x_scale, torch.float32, (T,), index, "x_scale")
+    _check(w13_scale, torch.float32, (E, I2), index, "w13_scale")
+    padded, src, cap = _route_on(route, index, E)
+    act = torch.zeros((cap, I), dtype=torch.bfloat16, device=x.device) if act is None else act
+    _check(act, torch.bfloat16, (cap, I), index, "act")
+    _launch(index, lib().moe_gemm1_swiglu_int8, _ptr(x), _ptr(x_scale), _ptr(w13), _ptr(w13_scale), _ptr(padded),
+            _ptr(src), T, H, I, E, K, align, _ptr(act), cap, tile_m, weight_layout)
     return act
 
 
@@ -679,17 +680,17 @@ def quant_rows_int8(x, q=None, scale=None, route=None):
     rows of padding are not written."""
     _need(x, torch.bfloat16, "x", 2)
     rows, N = x.shape
-    dev = x.device
-    src = None if route is None else route["sorted_src"]
-    if src is not None and src.numel() != rows:
-        raise ValueError("route and x disagree on the rows")
-    _same_device(dev, route=src)
-    if route is not None:      # the rows that are not written
-        q = torch.zeros((rows, N), dtype=torch.int8, device=dev) if q is None else q
-        scale = torch.zeros(rows, dtype=torch.float32, device=dev) if scale is None else scale
-    q = _out(q, (rows, N), torch.int8, "q", dev)
-    scale = _out(scale, (rows,), torch.float32, "scale", dev)
-    _launch(dev, lib().moe_quant_rows_int8, _ptr(x), _ptr(src), rows, N, _ptr(q), _ptr(scale))
+    index = x.get_device()
+    src = None
+    if route is not None:      # its rows of padding are not written
+        _, src, cap = _route_on(route, index)
+        if cap != rows:
+            raise ValueError("route and x disagree on the rows")
+        q = torch.zeros((rows, N), dtype=torch.int8, device=x.device) if q is None else q
+        scale = torch.zeros(rows, dtype=torch.float32, device=x.device) if scale is None else scale
+    q = _out(q, torch.int8, (rows, N), x, "q")
+    scale = _out(scale, torch.float32, (rows,), x, "scale")
+    _launch(index, lib().moe_quant_rows_int8, _ptr(x), _ptr(src), rows, N, _ptr(q), _ptr(scale))
     return q, scale
 
 
@@ -698,22 +699,19 @@ def gemm2_weighted_int8(q, q_scale, w2, w2_scale, route, topk_weights, T, K, ali
     """Int8 GEMM2 + routing-weight stage.  Returns Y bf16 [T*K, H]; rows of dropped slots are not
     written (zero when Y is allocated here)."""
     _need(q, torch.int8, "q", 2)
-    _need(q_scale, torch.float32, "q_scale", 1)
     _need(w2, torch.int8, "w2", 3)
-    _need(w2_scale, torch.float32, "w2_scale", 2)
-    _need(topk_weights, torch.float32, "topk_weights", 2)
     E, H, I = w2.shape
-    cap = route["sorted_src"].numel()
-    dev = q.device
-    if q.shape != (cap, I) or q_scale.shape != (cap,) or w2_scale.shape != (E, H) or topk_weights.shape != (T, K):
-        raise ValueError("inconsistent q / w2 / scale / topk_weights shapes")
-    _same_device(dev, q_scale=q_scale, w2=w2, w2_scale=w2_scale, route=route["sorted_src"],
-                 topk_weights=topk_weights)
-    Y = torch.zeros((T * K, H), dtype=torch.bfloat16, device=dev) if Y is None else Y
-    Y = _out(Y, (T * K, H), torch.bfloat16, "Y", dev)
-    _launch(dev, lib().moe_gemm2_weighted_int8, _ptr(q), _ptr(q_scale), _ptr(w2), _ptr(w2_scale),
-            _ptr(route["padded_indptr"]), _ptr(route["sorted_src"]), _ptr(topk_weights), T, H, I, E, K, align,
-            _ptr(Y), cap, tile_m, weight_layout)
+    index = q.get_device()
+    padded, src, cap = _route_on(route, index, E)
+    _check(q, torch.int8, (cap, I), index, "q")
+    _check(w2, torch.int8, (E, H, I), index, "w2")
+    _check(q_scale, torch.float32, (cap,), index, "q_scale")
+    _check(w2_scale, torch.float32, (E, H), index, "w2_scale")
+    _check(topk_weights, torch.float32, (T, K), index, "topk_weights")
+    Y = torch.zeros((T * K, H), dtype=torch.bfloat16, device=q.device) if Y is None else Y
+    _check(Y, torch.bfloat16, (T * K, H), index, "Y")
+    _launch(index, lib().moe_gemm2_weighted_int8, _ptr(q), _ptr(q_scale), _ptr(w2), _ptr(w2_scale), _ptr(padded),
+            _ptr(src), _ptr(topk_weights), T, H, I, E, K, align, _ptr(Y), cap, tile_m, weight_layout)
     return Y
 
 
@@ -756,36 +754,32 @@ def add_rmsnorm_quant(x, weight, eps, format, residual=None, want_norm=False, q=
     NORM_BF16, v the new residual stream if a residual is given; None where there is none.
     residual_out may be `residual`."""
     _need(x, torch.bfloat16, "x", 2)
-    T, H = x.shape
-    dev = x.device
-    _need(weight, torch.float32 if weight.dtype == torch.float32 else torch.bfloat16, "weight", 1)
-    if weight.shape != (H,):
-        raise ValueError("weight must be [H]")
-    _same_device(dev, weight=weight, residual=residual)
+    T, H = shape = x.shape
+    index = x.get_device()
+    weight_f32 = weight.dtype == torch.float32
+    _check(weight, torch.float32 if weight_f32 else torch.bfloat16, (H,), index, "weight")
+    residual_f32 = False
     if residual is not None:
-        _need(residual, torch.float32 if residual.dtype == torch.float32 else torch.bfloat16, "residual", 2)
-        if residual.shape != (T, H):
-            raise ValueError("residual must be [T, H]")
-        residual_out = _out(residual_out, (T, H), residual.dtype, "residual_out", dev)
+        residual_f32 = residual.dtype == torch.float32
+        _check(residual, torch.float32 if residual_f32 else torch.bfloat16, shape, index, "residual")
+        residual_out = _out(residual_out, residual.dtype, shape, x, "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if want_norm or norm_out is not None or format == NORM_BF16:
-        norm_out = _out(norm_out, (T, H), torch.bfloat16, "norm_out", dev)
+        norm_out = _out(norm_out, torch.bfloat16, shape, x, "norm_out")
     if format == NORM_FP8:
-        q = _out(q, (T, H), torch.uint8, "q", dev)
-        scale = _out(scale, (T, H // 128), torch.float32, "scale", dev)
+        q = _out(q, torch.uint8, shape, x, "q")
+        scale = _out(scale, torch.float32, (T, H // 128), x, "scale")
     elif format == NORM_MXFP8:
-        q = _out(q, (T, H), torch.uint8, "q", dev)
-        scale = _out(scale, (T, H // 32), torch.uint8, "scale", dev)
+        q = _out(q, torch.uint8, shape, x, "q")
+        scale = _out(scale, torch.uint8, (T, H // 32), x, "scale")
     elif format == NORM_INT8:
-        q = _out(q, (T, H), torch.int8, "q", dev)
-        scale = _out(scale, (T,), torch.float32, "scale", dev)
+        q = _out(q, torch.int8, shape, x, "q")
+        scale = _out(scale, torch.float32, (T,), x, "scale")
     elif q is not None or scale is not None:
         raise ValueError("NORM_BF16 has no codes")
-    residual_f32 = int(residual is not None and residual.dtype == torch.float32)
-    _launch(dev, lib().add_rmsnorm_quant, _ptr(x), _ptr(residual), residual_f32, _ptr(weight),
-            int(weight.dtype == torch.float32), eps, T, H, format, _ptr(residual_out), _ptr(norm_out), _ptr(q),
-            _ptr(scale))
+    _launch(index, lib().add_rmsnorm_quant, x.data_ptr(), _ptr(residual), residual_f32, weight.data_ptr(), weight_f32,
+            eps, T, H, format, _ptr(residual_out), _ptr(norm_out), _ptr(q), _ptr(scale))
     return q, scale, norm_out, residual_out
 
 
@@ -800,18 +794,17 @@ def moe_router_topk(logits, K, score=SCORE_SOFTMAX, bias=None, n_group=1, topk_g
     softmax or sigmoid, chosen by score + bias (fp32 [E]) among the topk_group best of n_group expert
     groups, ties to the lower index; weights are the scores, renormalised and scaled (see
     moe_router_topk in include/fp8moe.h).  Returns (ids int32 [T, K], weights fp32 [T, K])."""
-    _need(logits, torch.bfloat16 if logits.dtype == torch.bfloat16 else torch.float32, "logits", 2)
+    bf16 = logits.dtype == torch.bfloat16
+    _need(logits, torch.bfloat16 if bf16 else torch.float32, "logits", 2)
     T, E = logits.shape
-    dev = logits.device
+    index = logits.get_device()
     if bias is not None:
-        _need(bias, torch.float32, "bias", 1)
-        if bias.shape != (E,):
-            raise ValueError("bias must be [E]")
-        _same_device(dev, bias=bias)
-    ids = _out(ids, (T, max(K, 0)), torch.int32, "ids", dev)
-    weights = _out(weights, (T, max(K, 0)), torch.float32, "weights", dev)
-    _launch(dev, lib().moe_router_topk, _ptr(logits), int(logits.dtype == torch.bfloat16), _ptr(bias), T, E, K,
-            score, n_group, topk_group, group_top, int(bool(renormalize)), scale, _ptr(ids), _ptr(weights))
+        _check(bias, torch.float32, (E,), index, "bias")
+    shape = (T, max(K, 0))
+    ids = _out(ids, torch.int32, shape, logits, "ids")
+    weights = _out(weights, torch.float32, shape, logits, "weights")
+    _launch(index, lib().moe_router_topk, logits.data_ptr(), bf16, _ptr(bias), T, E, K, score, n_group, topk_group,
+            group_top, bool(renormalize), scale, ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 

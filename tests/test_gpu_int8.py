@@ -320,3 +320,12 @@ def test_refusals():
     flat = torch.zeros(8 * 256 + 16, dtype=torch.int8, device="cuda")
     with pytest.raises(fm.Fp8MoeError, match="aligned"):
         f(x=flat[1:1 + 8 * 256].view(8, 256))
+    r = fm.route_permute(d["ids"], 4, 16)      # a routing of 4 experts is no routing of 3
+    with pytest.raises(ValueError, match="padded_indptr"):
+        fm.gemm1_swiglu_int8(d["x"], d["xs"], d["w13"][:3], d["w13s"][:3], r, 8, 2, 16)
+    act = fm.gemm1_swiglu_int8(d["x"], d["xs"], d["w13"], d["w13s"], r, 8, 2, 16)
+    q, qs = fm.quant_rows_int8(act, route=r)
+    with pytest.raises(ValueError, match="padded_indptr"):
+        fm.gemm2_weighted_int8(q, qs, d["w2"][:3], d["w2s"][:3], r, d["tw"], 8, 2, 16)
+    with pytest.raises(ValueError, match="rows"):
+        fm.quant_rows_int8(act[:-1], route=r)
