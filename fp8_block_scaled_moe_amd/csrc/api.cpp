@@ -854,22 +854,35 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 
 bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
-// Tile height of one of the int8 products, of NT N tiles of 256 weight rows:
-// the tile kernels from 8 rows an expert on, if their workgroups fill half the
-// chip, else the streaming kernel of the smallest height that holds an even
-// share of the routed rows over the experts they can reach.  Layer times with
-// streaming heights 16, 32, 64 and with tiles (us):
-//   H=2048, I=768, E=128, top-8:  T=128: 134, 144, 166 | 140; T=256: 164, 172,
-//     192 | 142; T=512: 227, 234, 235 | 156; Zipf 1.2: T=128: 96, 106, 146 | 87;
-//     T=512: 225, 221, 265 | 174
-//   H=7168, I=2048, E=256, top-8: T=256: 1857, 1848, 1926 | 1901; T=512: 2232,
-//     2114, 2116 | 2000; T=2048: 5167, 4397, 4218 | 2292
-//   H=7168, I=2048, E=1, top-1 (16 and 28 N tiles):  T=64: 35, 33, 40 | 50
+// Tile height of one of the int8 products, of NT N tiles of 256 weight rows.
+//
+// Beyond an even share of 8 rows an expert, the tile kernels, if their
+// workgroups W fill 3/8 of the chip, or 3/16 of it and the streaming kernel
+// would have more than 16 rows x N tiles for each CU: a K step of that one
+// takes as long as it has rows, a tile's about the same however few there are.
+// Else the streaming kernel: 16 rows to a share, 32 (whose waves hold more
+// weights in flight) up to 64 rows, 64 beyond, where weights read once for 64
+// rows win.  Packed weights, us for heights 16, 32, 64 | tiles:
+//   layer, E=128, top-8, H=2048, I=768:  T=128: 136, 143, 168 | 144; T=256: 163,
+//     171, 194 | 152; T=512: 227, 233, 238 | 161; T=4096: 1175, 1066, 1047 | 307
+//     (Zipf 1.2: T=128: 96, 107, 146 | 89; T=512: 225, 220, 265 | 123)
+//   layer, E=256, top-8, H=7168, I=2048: T=256: 1888, 1907, 1951 | 1934; T=512:
+//     2233, 2114, 2100 | 1979; T=2048: 5174, 4374, 4212 | 2261
+//   layer, one expert, H=7168, I=2048:   T=64: 33, 32, 39 | 60; T=384: 113, 100,
+//     96 | 94; T=512: 141, 124, 115 | 114; T=1024: 266, 228, 210 | 116
+//   GEMM1, H=2048, I=768, by rows x experts (W, rows x N tiles):
+//     1024x1 (24, 6144): 24, 20, 20 | 27; 2048x1 (48, 12288): 45, 40, 37 | 27;
+//     64x8 (54, 3072): 15, 15, 20 | 15; 128x8 (66, 6144): 25, 23, 24 | 19;
+//     64x12 (84, 4608): 21, 21, 24 | 18; 32x16 (96, 3072): 17, 18, 18 | 13
+//   GEMM1, H=7168, I=2048: 64x2 (32, 2048): 28, 28, 31 | 43; 32x4 (64, 2048): 30,
+//     29, 26 | 36; 64x4 (64, 4096): 46, 43, 47 | 47; 32x8 (128, 4096): 57, 54,
+//     44 | 36
 int int8_tile_m(int requested, int64_t R, int E, int64_t NT) {
   if (requested != -1) return requested;
   const int64_t active = R < E ? R : E, rows = active > 0 ? (R + active - 1) / active : 0;
-  if (rows > 8 && (R / kTileMaxInt8 + active) * NT >= device_num_cu() / 2) return kTileMaxInt8;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  const int64_t W = (R / kTileMaxInt8 + active) * NT, cus = device_num_cu();
+  if (rows > 8 && (8 * W >= 3 * cus || (16 * W >= 3 * cus && R * NT > 16 * cus))) return kTileMaxInt8;
+  return rows <= 16 ? 16 : rows <= 64 ? 32 : 64;
 }
 
 int check_int8_stage(int64_t T, int32_t H, int32_t I, int32_t E, int32_t K, int32_t align, int64_t cap,
