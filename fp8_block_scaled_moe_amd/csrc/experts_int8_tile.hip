@@ -15,6 +15,21 @@
 // LDS buffers, filled by direct-to-LDS loads three K steps ahead; one barrier
 // per K step hands a buffer over.  The fragment reads of a step's first two
 // sub-tiles are issued before the barrier that ends the step ahead of it.
+//
+// Measured, packed weights: H=7168, I=2048, E=256, top-8, T=8192 (256 rows an
+// expert): GEMM1 2.02-2.09 ms, 1840-1910 TOPS, GEMM2 1.15-1.17 ms, 1650-1670;
+// one expert of 8192 rows: GEMM1 2370 TOPS (the library's large int8 product:
+// 2120).  What bounds them: with 256 rows an expert the weights of a K step come
+// from HBM (3.7 TB/s with the rest) in the time of its products, MFMA busy 50 %;
+// waves wait for issue 55 % of their time, on memory or the barrier 24 %.
+// H=2048, I=768, E=128, T=4096: GEMM1 138 us (1500 TOPS), GEMM2 112 us, whose N
+// tiles of six K steps are half epilogue.
+// From 64-row tiles up (layer, T=8192): streaming kernel 13.2 ms; tiles of 256
+// rows in runs of 16 N tiles 5.30, of 2 4.08; 288 rows 3.89; 16-byte stores of
+// the results 3.48; loads spread over the sub-tiles 3.43-3.46.
+// No gain: weights prefetched to L2 (GEMM1 2064 -> 2447 us), nontemporal weight
+// loads (2354), one barrier per two K steps (2091), nontemporal result stores
+// (layer at T=4096, Zipf 1.2: 343.5 -> 346), raised wave priority.
 #include <type_traits>
 
 #include "gemm_kernels.h"
@@ -347,7 +362,8 @@ __device__ __forceinline__ void tile_gemm2(const TokenBuffers& tb, RowInfo& ri, 
 // tiles that share weights meet in one L2.  Equal counts of one list of all
 // tiles, as the other formats' kernels deal them, give one XCD the tall tiles
 // of popular experts and another the short ones: Zipf 1.2 routing (H=2048,
-// I=768, E=128, top-8) took 171 us at T=512 and 398 at T=4096 that way.
+// I=768, E=128, top-8) took 171 us at T=512 and 398 at T=4096 that way, 124
+// and 346 this way.
 // The range's tiles come first, being the tall ones.
 template <int TMAX>
 struct TileChunk {   // experts c + 4 lane .. + 3: their rows and tile counts (0 past E)

@@ -32,9 +32,15 @@
 //     and the candidates are put in order by their full choices: the logits
 //     themselves, or, where neighbours lie closer than fp32's error, the
 //     biased logistic function in fp64;
-//   * what is left for the exact path: more close candidates than lanes, close
-//     choices of a biased softmax, and groups counted by sums of which a kept
-//     and a left one are closer than the error of both.
+//   * groups of which a kept and a left one are closer than the error of both
+//     are ranked by fp64 totals of their best choices;
+//   * what is left for the exact path: more close candidates than lanes, and
+//     close choices or close groups of softmax scores.
+// In a graph, 8192 tokens of 256 experts: softmax 6.3 us (bf16 logits 5.2),
+// sigmoid with bias 7.9, softmax with bias 11.9, groups by their maximum 7.2, by
+// the sum of two 14.0; 65537 tokens of 128: 16.4 us, 2.3 TB/s; one token 4.5 us.
+// Bound by the K rounds of maximum and removal (4 shuffle steps each), at few
+// tokens by the launch.
 #include "device_common.h"
 #include "fp8moe.h"
 #include "launch.h"
@@ -47,7 +53,7 @@ struct RouterArgs {
   const void* logits;
   const float* bias;
   int T, E, K, score, n_group, topk_group, group_top, renormalize;
-  int vec;   // fast path: logits and bias are read in 16-byte vectors
+  int vec;   // fast path: logits and bias are read in vectors
   float scale;
   int32_t* ids;
   float* weights;
@@ -284,11 +290,12 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
 #pragma unroll
   for (int i = 0; i < NV; ++i) x[i] = kNone;
   if (live) {
-    if (a.vec) {   // E == L NV
+    if (a.vec) {   // E % 8 == 0: a vector lies inside the row or past it
       const char* src = static_cast<const char*>(a.logits) + (t * E + rl * NV) * (BF16 ? 2 : 4);
       if constexpr (BF16 && NV % 8 == 0) {
 #pragma unroll
         for (int i = 0; i < NV; i += 8) {
+          if (rl * NV + i >= E) break;
           const uint4 v = *reinterpret_cast<const uint4*>(src + 2 * i);
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -300,6 +307,7 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
       } else if constexpr (BF16) {
 #pragma unroll
         for (int i = 0; i < NV; i += 4) {
+          if (rl * NV + i >= E) break;
           const uint2 v = *reinterpret_cast<const uint2*>(src + 2 * i);
           x[i] = __uint_as_float(v.x << 16);
           x[i + 1] = __uint_as_float(v.x & 0xffff0000u);
@@ -309,6 +317,7 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
       } else {
 #pragma unroll
         for (int i = 0; i < NV; i += 4) {
+          if (rl * NV + i >= E) break;
           const float4 v = *reinterpret_cast<const float4*>(src + 4 * i);
           x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
         }
@@ -331,11 +340,11 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
   if (softmax) {
     m = row_reduce_f32<L, true>(m);
     if (scored || !a.renormalize) {
-      z = 0.f;
+      float part[2] = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (x[i] > kNone) z += x[i] == m ? 1.f : fast_exp(x[i] - m);
-      z = row_reduce_f32<L, false>(z);
+        if (x[i] > kNone) part[i & 1] += x[i] == m ? 1.f : fast_exp(x[i] - m);
+      z = row_reduce_f32<L, false>(part[0] + part[1]);
     }
   }
   const float zinv = 1.0f / z;
@@ -350,11 +359,11 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
   if (biased) {
 #pragma unroll
     for (int i = 0; i < NV; i += 4) {
-      float b[4];
-      if (a.vec) {
+      float b[4] = {0.f, 0.f, 0.f, 0.f};
+      if (a.vec && rl * NV + i < E) {
         const float4 v = *reinterpret_cast<const float4*>(a.bias + rl * NV + i);
         b[0] = v.x; b[1] = v.y; b[2] = v.z; b[3] = v.w;
-      } else {
+      } else if (!a.vec) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) b[k] = rl * NV + i + k < E ? a.bias[rl * NV + i + k] : 0.f;
       }
@@ -370,7 +379,8 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
   }
   // Error of a choice c of score s, with margin: the logistic function is
   // within 2^-22, a softmax's score within 2^-19 of itself (the exponential's
-  // argument, and a sum of 16 terms a lane and 6 levels of lanes), and the bias
+  // argument, and a sum of up to twice 16 terms a lane and 4 levels of lanes, or
+  // twice 8 and 6), and the bias
   // adds half a step of c.
   auto choice_tol = [&](float s, float c) __attribute__((always_inline)) -> float {
     return (softmax ? s * 0x1p-18f : 0x1p-21f) + fabsf(c) * 0x1p-22f;
@@ -399,22 +409,66 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
       const float other = __shfl(total, (lane & ~(L - 1)) + h * gl);
       rank += other > total || (other == total && h < g);
     }
-    const bool keep = rank < a.topk_group;
+    bool keep = rank < a.topk_group;
     if (biased || sums) {
-      const float worst = -row_reduce_f32<L, true>(keep && rl < a.n_group * gl ? -total : kNone);
-      const float best = row_reduce_f32<L, true>(keep || rl >= a.n_group * gl ? kNone : total);
-      // two choices each (the tolerance has a margin of two); scores without a
-      // bias carry their argument's rounding relative to themselves
-      float tol = 2.f * choice_tol(1.f, fmaxf(fabsf(worst), fabsf(best)));
+      const bool real = rl < a.n_group * gl;   // lanes of a group
+      const float worst = -row_reduce_f32<L, true>(keep && real ? -total : kNone);
+      const float best = row_reduce_f32<L, true>(keep || !real ? kNone : total);
+      // two choices each (the tolerance has a margin of two), which may be far
+      // larger than their sum; scores without a bias carry their argument's
+      // rounding relative to themselves
+      float far = 0.f, tol;
       if (sums) {
-        float far = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
           if (fabsf(x[i]) < kRouterInf) far = fmaxf(far, fabsf(x[i]));
         tol = (2.f * row_reduce_f32<L, true>(far) + 32.f) * 0x1p-23f * fabsf(worst);
+      } else {
+        if (first > kNone) far = fabsf(first);
+        if (a.group_top > 1 && second > kNone) far += fabsf(second);
+        tol = 2.f * choice_tol(1.f, row_reduce_f32<L, true>(far));
       }
-      // (sums of scores next to fp32's smallest have no relative bound)
-      if (a.topk_group < a.n_group && best > kNone) unsure = !(worst - best > tol) || (sums && worst < 0x1p-100f);
+      const bool close = a.topk_group < a.n_group && best > kNone && !(worst - best > tol);
+      if (softmax || (sums && worst < 0x1p-100f)) {
+        // a softmax's sum would be needed in fp64, and sums of scores next to
+        // fp32's smallest have no relative bound: the exact path
+        unsure = close;
+      } else if (__ballot(close)) {
+        // Groups next to the border between kept and left ones are ranked by
+        // their fp64 totals, from those of their choices that may be among the
+        // largest; the others' places are certain.
+        const bool border = close && real && !((keep ? total - best : worst - total) > tol);
+        const float least = (a.group_top > 1 ? second : first) - tol;
+        uint32_t able = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (border && c[i] > kNone && !((sums ? score_of(c[i]) : c[i]) < least)) able |= 1u << i;
+        const double kNone64 = -__longlong_as_double(0x7ff0000000000000ll);
+        double f64 = kNone64, s64 = kNone64;
+        while (__ballot(able != 0)) {
+          double u = kNone64;
+          if (able != 0) {
+            const int e = rl * NV + __ffs(able) - 1;
+            able &= able - 1;
+            u = 1.0 / (1.0 + exp(-(double)router_logit<BF16>(a.logits, t * E + e)));
+            if (biased) u += (double)a.bias[e];
+          }
+          s64 = fmax(s64, fmin(f64, u));
+          f64 = fmax(f64, u);
+        }
+        for (int o = 1; o < gl; o <<= 1) {
+          const double f2 = shfl_xor_f64(f64, o), s2 = shfl_xor_f64(s64, o);
+          s64 = fmax(fmax(s64, s2), fmin(f64, f2));
+          f64 = fmax(f64, f2);
+        }
+        const double total64 = border ? (a.group_top > 1 ? f64 + s64 : f64) : (double)total;
+        int rank64 = 0;
+        for (int h = 0; h < a.n_group; ++h) {
+          const double other = shfl_any(total64, (lane & ~(L - 1)) + h * gl);
+          rank64 += other > total64 || (other == total64 && h < g);
+        }
+        if (close) keep = rank64 < a.topk_group;
+      }
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -549,19 +603,20 @@ hipError_t launch_router_topk(const void* logits, bool bf16, const float* bias, 
   // The fast path's rows: 16 lanes up to 256 experts and 14 slots, else 64 (at
   // least one further candidate has a lane).  Groups have to be whole lanes, a
   // power of two of them.
-  const int L = E <= 256 && K < 15 ? 16 : 64;
-  const int NV = L == 16 ? (E <= 64 ? 4 : E <= 128 ? 8 : 16) : E <= 512 ? 8 : 16;
+  const int L = E <= 512 && K < 15 ? 16 : 64;
+  const int NV = L == 16 ? (E <= 64 ? 4 : E <= 128 ? 8 : E <= 256 ? 16 : 32) : E <= 512 ? 8 : 16;
   const int per = E / n_group, gl = per / NV;
   const bool whole = n_group == 1 || (per % NV == 0 && (gl & (gl - 1)) == 0);
   const bool fast = K < L - 1 && whole;
-  const bool vec = E == L * NV && (uintptr_t)logits % 16 == 0 && (uintptr_t)bias % 16 == 0;
+  const bool vec = E % 8 == 0 && (uintptr_t)logits % 16 == 0 && (uintptr_t)bias % 16 == 0;
   const RouterArgs a{logits, bias, T, E, K, score, n_group, topk_group, group_top, (int)renormalize, (int)vec,
                      scale, ids, weights};
   if (fast) {
     if (L == 16) {
       if (NV == 4) router_launch<16, 4, true>(a, bf16, stream);
       else if (NV == 8) router_launch<16, 8, true>(a, bf16, stream);
-      else router_launch<16, 16, true>(a, bf16, stream);
+      else if (NV == 16) router_launch<16, 16, true>(a, bf16, stream);
+      else router_launch<16, 32, true>(a, bf16, stream);
     } else {
       if (NV == 8) router_launch<64, 8, true>(a, bf16, stream);
       else router_launch<64, 16, true>(a, bf16, stream);

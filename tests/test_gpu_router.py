@@ -107,6 +107,34 @@ def test_close_scores(score):
 
 
 @pytest.mark.parametrize("score", list(SCORES))
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("E,n_group,topk_group", [(256, 8, 4), (128, 16, 5), (512, 4, 1)])
+def test_close_groups(E, n_group, topk_group, group_top, score):
+    """Groups of the same logits in another order, moved by a few of fp32's smallest steps; equal groups; biases that
+    are far larger than the sums of a group's best choices."""
+    say("router close groups", E, n_group, topk_group, group_top, score)
+    g = torch.Generator().manual_seed(E + group_top)
+    G = E // n_group
+    one = torch.randn(40, 1, G, generator=g).expand(40, n_group, G)
+    order = torch.argsort(torch.rand(40, n_group, G, generator=g), 2)
+    logits = torch.gather(one, 2, order)
+    logits[20:] *= 1 + 2.0 ** -22 * torch.randint(-2, 3, (20, n_group, 1), generator=g)
+    logits = logits.reshape(40, E).contiguous()
+    kw = dict(n_group=n_group, topk_group=topk_group, group_top=group_top)
+    check(logits, 8, score, **kw)
+    check(logits, 8, score, torch.zeros(E), **kw)
+    check(logits, 8, score, torch.full((E,), 0.3), **kw)
+    check(logits, 8, score, torch.full((E,), -1000.0), **kw)
+    check(logits.bfloat16(), 8, score, torch.full((E,), 0.3), **kw)
+    # +1000 and -1000 on a group's best two: their sums are about a score's size
+    bias = torch.full((n_group, G), -2000.0)
+    bias[:, 1], bias[:, G - 1] = 1000.0, -1000.0
+    check(torch.randn(400, E, generator=g), 8, score, bias.view(-1), **kw)
+    bias[:, 1] += 2.0 ** -14 * torch.arange(n_group) % 3
+    check(0.001 * torch.randn(400, E, generator=g), 8, score, bias.view(-1), **kw)
+
+
+@pytest.mark.parametrize("score", list(SCORES))
 @pytest.mark.parametrize("biased", [False, True])
 @pytest.mark.parametrize("groups", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
 def test_masked_logits(score, biased, groups):
