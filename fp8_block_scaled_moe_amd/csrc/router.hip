@@ -22,11 +22,11 @@
 // fp64.  As the only path it measured 31 us for 8192 tokens of 256 experts in
 // groups, 121 us for 65537 tokens of 128.
 //
-// Fast path (route_fast): L = 16 lanes per token (64 beyond 256 experts or 14
-// slots), lane l holds experts l NV .. l NV + NV - 1, choices in fp32.  Each is
-// a 32-bit key: the order-preserving bits of the choice with the lowest
-// IB replaced by the complement of the expert's index, so keys are unique, the
-// largest key is the winner, and it is taken out by comparing.
+// Fast path (route_fast): L = 16 or 64 lanes per token, a lane holds up to NV
+// consecutive experts of one group, choices in fp32.  Each is a 32-bit key: the
+// order-preserving bits of the choice with the lowest IB replaced by the
+// complement of the expert's index, so keys are unique, the largest key is the
+// winner, and it is taken out by comparing.
 //   * bf16 logits without a bias: 16 value bits and the index fit, always exact;
 //   * else further keys are taken until the next cannot reach the last slot's,
 //     and the candidates are put in order by their full choices: the logits
@@ -36,11 +36,12 @@
 //     are ranked by fp64 totals of their best choices;
 //   * what is left for the exact path: more close candidates than lanes, and
 //     close choices or close groups of softmax scores.
-// In a graph, 8192 tokens of 256 experts: softmax 6.3 us (bf16 logits 5.2),
-// sigmoid with bias 7.9, softmax with bias 11.9, groups by their maximum 7.2, by
-// the sum of two 14.0; 65537 tokens of 128: 16.4 us, 2.3 TB/s; one token 4.5 us.
-// Bound by the K rounds of maximum and removal (4 shuffle steps each), at few
-// tokens by the launch.
+// In a graph, us for 8192 tokens of 256 experts, top-8: softmax 6.5 (bf16 logits
+// 5.3), sigmoid with bias 8.0, softmax with bias 12.4, groups by their maximum
+// 7.4, by the sum of two 10.1 (14 while close ones went the exact way); 65537
+// tokens of 128: 16.7, 2.3 TB/s; one token of 256: 3.9; 64: 4.2.
+// Bound by the K rounds of maximum and removal and their shuffles, at few tokens
+// by the launch and one trip to memory.
 #include "device_common.h"
 #include "fp8moe.h"
 #include "launch.h"
@@ -53,7 +54,9 @@ struct RouterArgs {
   const void* logits;
   const float* bias;
   int T, E, K, score, n_group, topk_group, group_top, renormalize;
-  int vec;   // fast path: logits and bias are read in vectors
+  // fast path: each group has `lanes` lanes (a power of two; without groups the
+  // row's all), a lane `width` of its experts; read in vectors of vec (1, 4, 8)
+  int lanes, width, vec;
   float scale;
   int32_t* ids;
   float* weights;
@@ -281,6 +284,10 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
   constexpr uint32_t kIdx = (1u << IB) - 1;
   const int E = a.E, K = a.K;
   const int rl = lane & (L - 1);                      // lane of the row
+  const int gl = a.lanes, g = rl / gl;                // lanes of a group, the lane's group
+  const int inside = (rl - g * gl) * a.width, per = E / a.n_group;
+  const int base = g * per + inside;                  // the lane's first expert
+  const int count = g < a.n_group ? min(a.width, per - inside) : 0;   // and their number, if positive
   const bool live = t < a.T;
   const bool biased = a.bias != nullptr, softmax = a.score == FP8MOE_SCORE_SOFTMAX;
   const bool sums = a.n_group > 1 && a.group_top > 1 && !biased;   // groups by sums of scores
@@ -290,12 +297,12 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
 #pragma unroll
   for (int i = 0; i < NV; ++i) x[i] = kNone;
   if (live) {
-    if (a.vec) {   // E % 8 == 0: a vector lies inside the row or past it
-      const char* src = static_cast<const char*>(a.logits) + (t * E + rl * NV) * (BF16 ? 2 : 4);
+    const char* src = static_cast<const char*>(a.logits) + (t * E + base) * (BF16 ? 2 : 4);
+    if (a.vec == 8 && BF16) {
       if constexpr (BF16 && NV % 8 == 0) {
 #pragma unroll
         for (int i = 0; i < NV; i += 8) {
-          if (rl * NV + i >= E) break;
+          if (i >= count) break;
           const uint4 v = *reinterpret_cast<const uint4*>(src + 2 * i);
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -304,10 +311,12 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
             x[i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
           }
         }
-      } else if constexpr (BF16) {
+      }
+    } else if (a.vec > 1) {
+      if constexpr (BF16) {
 #pragma unroll
         for (int i = 0; i < NV; i += 4) {
-          if (rl * NV + i >= E) break;
+          if (i >= count) break;
           const uint2 v = *reinterpret_cast<const uint2*>(src + 2 * i);
           x[i] = __uint_as_float(v.x << 16);
           x[i + 1] = __uint_as_float(v.x & 0xffff0000u);
@@ -317,7 +326,7 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
       } else {
 #pragma unroll
         for (int i = 0; i < NV; i += 4) {
-          if (rl * NV + i >= E) break;
+          if (i >= count) break;
           const float4 v = *reinterpret_cast<const float4*>(src + 4 * i);
           x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
         }
@@ -325,7 +334,7 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (rl * NV + i < E) x[i] = router_logit<BF16>(a.logits, t * E + rl * NV + i);
+        if (i < count) x[i] = router_logit<BF16>(a.logits, t * E + base + i);
     }
   }
   float m = kNone;
@@ -360,12 +369,12 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
 #pragma unroll
     for (int i = 0; i < NV; i += 4) {
       float b[4] = {0.f, 0.f, 0.f, 0.f};
-      if (a.vec && rl * NV + i < E) {
-        const float4 v = *reinterpret_cast<const float4*>(a.bias + rl * NV + i);
+      if (a.vec > 1 && i < count) {
+        const float4 v = *reinterpret_cast<const float4*>(a.bias + base + i);
         b[0] = v.x; b[1] = v.y; b[2] = v.z; b[3] = v.w;
-      } else if (!a.vec) {
+      } else if (a.vec == 1) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) b[k] = rl * NV + i + k < E ? a.bias[rl * NV + i + k] : 0.f;
+        for (int k = 0; k < 4; ++k) b[k] = i + k < count ? a.bias[base + i + k] : 0.f;
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -387,8 +396,6 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
   };
 
   if (a.n_group > 1) {
-    // a group is a whole number (a power of two) of the row's lanes
-    const int gl = E / a.n_group / NV;
     float first = kNone, second = kNone;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -403,7 +410,6 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
     }
     const float total = a.group_top > 1 ? (second > kNone ? first + second : kNone) : first;
     // rank of the lane's group, and the distance of kept and left groups
-    const int g = rl / gl;
     int rank = 0;
     for (int h = 0; h < a.n_group; ++h) {
       const float other = __shfl(total, (lane & ~(L - 1)) + h * gl);
@@ -448,7 +454,7 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
         while (__ballot(able != 0)) {
           double u = kNone64;
           if (able != 0) {
-            const int e = rl * NV + __ffs(able) - 1;
+            const int e = base + __ffs(able) - 1;
             able &= able - 1;
             u = 1.0 / (1.0 + exp(-(double)router_logit<BF16>(a.logits, t * E + e)));
             if (biased) u += (double)a.bias[e];
@@ -478,7 +484,7 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
   uint32_t key[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i)   // + 0: zeros of both signs are equal
-    key[i] = c[i] > kNone ? (sortable(c[i] + 0.f) & ~kIdx) | (kIdx - (uint32_t)(rl * NV + i)) : 0u;
+    key[i] = c[i] > kNone ? (sortable(c[i] + 0.f) & ~kIdx) | (kIdx - (uint32_t)(base + i)) : 0u;
   const bool cut = !BF16 || biased;   // keys hold a part of the choice
   uint32_t mine = 0, last = 0;
   auto take = [&](int j) __attribute__((always_inline)) {
@@ -600,17 +606,27 @@ static void router_launch(const RouterArgs& a, bool bf16, hipStream_t stream) {
 hipError_t launch_router_topk(const void* logits, bool bf16, const float* bias, int T, int E, int K, int score,
                               int n_group, int topk_group, int group_top, bool renormalize, float scale,
                               int32_t* ids, float* weights, hipStream_t stream) {
-  // The fast path's rows: 16 lanes up to 256 experts and 14 slots, else 64 (at
-  // least one further candidate has a lane).  Groups have to be whole lanes, a
-  // power of two of them.
-  const int L = E <= 512 && K < 15 ? 16 : 64;
-  const int NV = L == 16 ? (E <= 64 ? 4 : E <= 128 ? 8 : E <= 256 ? 16 : 32) : E <= 512 ? 8 : 16;
-  const int per = E / n_group, gl = per / NV;
-  const bool whole = n_group == 1 || (per % NV == 0 && (gl & (gl - 1)) == 0);
-  const bool fast = K < L - 1 && whole;
-  const bool vec = E % 8 == 0 && (uintptr_t)logits % 16 == 0 && (uintptr_t)bias % 16 == 0;
-  const RouterArgs a{logits, bias, T, E, K, score, n_group, topk_group, group_top, (int)renormalize, (int)vec,
-                     scale, ids, weights};
+  // The fast path's rows: 16 lanes, or 64: beyond 512 experts, 14 slots (at
+  // least one further candidate has a lane) or 16 groups, and, from 129 experts
+  // on, where the tokens are few: fewer values a lane are the shorter way until
+  // the waves queue.  16 and 64 lanes, us, fp32 softmax | biased sigmoid: 256
+  // experts, T=64 5.2, 4.2 | 6.5, 4.6; T=3000 6.0, 5.7 | 7.5, 6.2; T=4096 6.1,
+  // 6.1 | 7.6, 6.8; T=8192 6.7, 9.0 | 8.3, 10.1.  512 experts, T=64 7.6, 4.7;
+  // T=6000 10.3, 9.3; T=8192 10.7, 11.5.  128 experts, T=64 4.3, 4.2; T=2048
+  // 4.5, 4.7.
+  const bool few = E > 128 && T <= 12 * E;
+  const int L = !few && E <= 512 && K < 15 && n_group <= 16 ? 16 : 64;
+  const int NV = L == 16 ? (E <= 64 ? 4 : E <= 128 ? 8 : E <= 256 ? 16 : 32) : E <= 256 ? 4 : E <= 512 ? 8 : 16;
+  const int per = E / n_group;
+  int lanes = L;
+  while (lanes * n_group > L) lanes /= 2;
+  const bool aligned = (uintptr_t)logits % 16 == 0 && (uintptr_t)bias % 16 == 0;
+  const int vec = !aligned || per % 4 ? 1 : per % 8 || NV % 8 ? 4 : 8;
+  const int share = (per + lanes - 1) / lanes;
+  const int width = n_group == 1 ? NV : (share + vec - 1) / vec * vec;
+  const bool fast = K < L - 1 && width <= NV;
+  const RouterArgs a{logits, bias, T, E, K, score, n_group, topk_group, group_top, (int)renormalize,
+                     lanes, width, vec, scale, ids, weights};
   if (fast) {
     if (L == 16) {
       if (NV == 4) router_launch<16, 4, true>(a, bf16, stream);
@@ -618,7 +634,8 @@ hipError_t launch_router_topk(const void* logits, bool bf16, const float* bias, 
       else if (NV == 16) router_launch<16, 16, true>(a, bf16, stream);
       else router_launch<16, 32, true>(a, bf16, stream);
     } else {
-      if (NV == 8) router_launch<64, 8, true>(a, bf16, stream);
+      if (NV == 4) router_launch<64, 4, true>(a, bf16, stream);
+      else if (NV == 8) router_launch<64, 8, true>(a, bf16, stream);
       else router_launch<64, 16, true>(a, bf16, stream);
     }
   } else {

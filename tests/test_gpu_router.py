@@ -106,6 +106,25 @@ def test_close_scores(score):
     check(x, 8, score, (1.0 - s[0]).float())
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("E,n_group,K", [(160, 8, 8), (66, 6, 5), (231, 7, 9), (500, 10, 14), (384, 12, 8), (51, 17, 4),
+                                         (48, 16, 3), (63, 63, 20), (1023, 33, 8), (4, 2, 2), (392, 8, 7)])
+def test_groups_of_any_size(E, n_group, K, biased, dtype):
+    """Groups that are no whole numbers of lanes, or vectors, or fewer than lanes; rows that start unaligned."""
+    say("router group sizes", E, n_group, K, biased, dtype)
+    logits, bias = make(70, E, 3 * E + K, dtype)
+    for score in SCORES:
+        for group_top in range(1, min(2, E // n_group) + 1):
+            kw = dict(n_group=n_group, topk_group=max(1, n_group // 2), group_top=group_top)
+            check(logits, K, score, bias if biased else None, **kw)
+    far = torch.empty(70 * E + 1, dtype=dtype, device="cuda")[1:].view(70, E)
+    far.copy_(logits)
+    ids, w = fm.moe_router_topk(far, K, fm.SCORE_SIGMOID, bias=bias.cuda() if biased else None)
+    ids2, w2 = fm.moe_router_topk(logits.cuda(), K, fm.SCORE_SIGMOID, bias=bias.cuda() if biased else None)
+    assert torch.equal(ids, ids2) and torch.equal(w, w2)
+
+
 @pytest.mark.parametrize("score", list(SCORES))
 @pytest.mark.parametrize("group_top", [1, 2])
 @pytest.mark.parametrize("E,n_group,topk_group", [(256, 8, 4), (128, 16, 5), (512, 4, 1)])
