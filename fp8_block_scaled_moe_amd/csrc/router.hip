@@ -36,10 +36,10 @@
 //     are ranked by fp64 totals of their best choices;
 //   * what is left for the exact path: more close candidates than lanes, and
 //     close choices or close groups of softmax scores.
-// In a graph, us for 8192 tokens of 256 experts, top-8: softmax 6.5 (bf16 logits
-// 5.3), sigmoid with bias 8.0, softmax with bias 12.4, groups by their maximum
-// 7.4, by the sum of two 10.1 (14 while close ones went the exact way); 65537
-// tokens of 128: 16.7, 2.3 TB/s; one token of 256: 3.9; 64: 4.2.
+// In a graph, us for 8192 tokens of 256 experts, top-8: softmax 6.4 (bf16 logits
+// 5.1), sigmoid with bias 8.3, softmax with bias 12.4, groups by their maximum
+// 7.3, by the sum of two 10.2 (14 while close ones went the exact way); 65537
+// tokens of 128: 15.8, 2.4 TB/s; one token of 256: 3.6; 64: 3.9.
 // Bound by the K rounds of maximum and removal and their shuffles, at few tokens
 // by the launch and one trip to memory.
 #include "device_common.h"
@@ -576,10 +576,17 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
 }
 
 // FAST: the fast path, then the exact one for the rows it leaves; else the
-// exact path alone.
-template <int L, int NV, bool BF16, bool FAST>
+// exact path alone.  PLAIN: neither bias nor groups, with nothing kept in
+// registers for them (65537 tokens of 128 experts: 17.1 -> 15.8 us).
+template <int L, int NV, bool BF16, bool FAST, bool PLAIN>
 __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(RouterArgs a) {
   extern __shared__ double keys_lds[];
+  if constexpr (PLAIN) {
+    a.bias = nullptr;
+    a.n_group = a.topk_group = a.group_top = 1;
+    a.lanes = L;
+    a.width = NV;
+  }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   double* mine = keys_lds + wave * a.E;
   constexpr int ENV = (L * NV + 63) / 64;   // experts of a lane on the exact path
@@ -599,8 +606,15 @@ static void router_launch(const RouterArgs& a, bool bf16, hipStream_t stream) {
   constexpr int rows = kRouterWaves * (FAST ? 64 / L : 1);
   const dim3 grid((unsigned)(((int64_t)a.T + rows - 1) / rows)), block(64 * kRouterWaves);
   const size_t lds = a.n_group > 1 ? sizeof(double) * kRouterWaves * a.E : 0;   // at most 32 KB
-  if (bf16) hipLaunchKernelGGL((router_topk_kernel<L, NV, true, FAST>), grid, block, lds, stream, a);
-  else hipLaunchKernelGGL((router_topk_kernel<L, NV, false, FAST>), grid, block, lds, stream, a);
+  if constexpr (FAST) {
+    if (a.bias == nullptr && a.n_group == 1) {
+      if (bf16) hipLaunchKernelGGL((router_topk_kernel<L, NV, true, true, true>), grid, block, 0, stream, a);
+      else hipLaunchKernelGGL((router_topk_kernel<L, NV, false, true, true>), grid, block, 0, stream, a);
+      return;
+    }
+  }
+  if (bf16) hipLaunchKernelGGL((router_topk_kernel<L, NV, true, FAST, false>), grid, block, lds, stream, a);
+  else hipLaunchKernelGGL((router_topk_kernel<L, NV, false, FAST, false>), grid, block, lds, stream, a);
 }
 
 hipError_t launch_router_topk(const void* logits, bool bf16, const float* bias, int T, int E, int K, int score,
@@ -613,7 +627,7 @@ hipError_t launch_router_topk(const void* logits, bool bf16, const float* bias, 
   // experts, T=64 5.2, 4.2 | 6.5, 4.6; T=3000 6.0, 5.7 | 7.5, 6.2; T=4096 6.1,
   // 6.1 | 7.6, 6.8; T=8192 6.7, 9.0 | 8.3, 10.1.  512 experts, T=64 7.6, 4.7;
   // T=6000 10.3, 9.3; T=8192 10.7, 11.5.  128 experts, T=64 4.3, 4.2; T=2048
-  // 4.5, 4.7.
+  // 4.5, 4.7.  (With bias and groups compiled in.)
   const bool few = E > 128 && T <= 12 * E;
   const int L = !few && E <= 512 && K < 15 && n_group <= 16 ? 16 : 64;
   const int NV = L == 16 ? (E <= 64 ? 4 : E <= 128 ? 8 : E <= 256 ? 16 : 32) : E <= 256 ? 4 : E <= 512 ? 8 : 16;
