@@ -23,7 +23,7 @@
 // groups, 121 us for 65537 tokens of 128.
 //
 // Fast path (route_fast): L = 16 or 64 lanes per token, a lane holds up to NV
-// consecutive experts of one group, choices in fp32.  Each is a 32-bit key: the
+// experts of one group, choices in fp32.  Each is a 32-bit key: the
 // order-preserving bits of the choice with the lowest IB replaced by the
 // complement of the expert's index, so keys are unique, the largest key is the
 // winner, and it is taken out by comparing.
@@ -31,11 +31,11 @@
 //   * else further keys are taken until the next cannot reach the last slot's,
 //     and the candidates are put in order by their full choices: the logits
 //     themselves, or, where neighbours lie closer than fp32's error, the
-//     biased logistic function in fp64;
+//     biased scores in fp64;
 //   * groups of which a kept and a left one are closer than the error of both
 //     are ranked by fp64 totals of their best choices;
 //   * what is left for the exact path: more close candidates than lanes, and
-//     close choices or close groups of softmax scores.
+//     close groups whose scores are next to fp32's smallest.
 // In a graph, us for 8192 tokens of 256 experts, top-8: softmax 6.4 (bf16 logits
 // 5.1), sigmoid with bias 8.3, softmax with bias 12.4, groups by their maximum
 // 7.3, by the sum of two 10.2 (14 while close ones went the exact way); 65537
@@ -54,9 +54,10 @@ struct RouterArgs {
   const void* logits;
   const float* bias;
   int T, E, K, score, n_group, topk_group, group_top, renormalize;
-  // fast path: each group has `lanes` lanes (a power of two; without groups the
-  // row's all), a lane `width` of its experts; read in vectors of vec (1, 4, 8)
-  int lanes, width, vec;
+  // fast path: each group of `per` experts has `lanes` lanes (a power of two;
+  // without groups the row's all), a lane up to `width` of them, read in vectors
+  // of vec (1, 4, 8)
+  int per, lanes, width, vec;
   float scale;
   int32_t* ids;
   float* weights;
@@ -284,10 +285,13 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
   constexpr uint32_t kIdx = (1u << IB) - 1;
   const int E = a.E, K = a.K;
   const int rl = lane & (L - 1);                      // lane of the row
-  const int gl = a.lanes, g = rl / gl;                // lanes of a group, the lane's group
-  const int inside = (rl - g * gl) * a.width, per = E / a.n_group;
-  const int base = g * per + inside;                  // the lane's first expert
-  const int count = g < a.n_group ? min(a.width, per - inside) : 0;   // and their number, if positive
+  const int gl = a.lanes, log_gl = __ffs(gl) - 1;     // lanes of a group
+  const int g = rl >> log_gl, in = rl & (gl - 1), per = a.per;   // the lane's group, the lane in it
+  // the lane's experts: base + step i, i < count; read in vectors they are
+  // neighbours, else the group's lanes read neighbours
+  const bool wide = a.vec > 1;
+  const int base = g * per + (wide ? in * a.width : in), step = wide ? 1 : gl;
+  const int count = g >= a.n_group ? 0 : wide ? min(a.width, per - in * a.width) : (per - in + gl - 1) >> log_gl;
   const bool live = t < a.T;
   const bool biased = a.bias != nullptr, softmax = a.score == FP8MOE_SCORE_SOFTMAX;
   const bool sums = a.n_group > 1 && a.group_top > 1 && !biased;   // groups by sums of scores
@@ -312,7 +316,7 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
           }
         }
       }
-    } else if (a.vec > 1) {
+    } else if (wide) {
       if constexpr (BF16) {
 #pragma unroll
         for (int i = 0; i < NV; i += 4) {
@@ -334,7 +338,7 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (i < count) x[i] = router_logit<BF16>(a.logits, t * E + base + i);
+        if (i < count) x[i] = router_logit<BF16>(a.logits, t * E + base + i * step);
     }
   }
   float m = kNone;
@@ -362,6 +366,22 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
     return softmax ? (v == m ? 1.f : fast_exp(v - m)) * zinv : fast_sigmoid(v);
   };
 
+  // Scores in fp64, for choices that fp32 cannot tell apart; a softmax's take the
+  // row's sum in fp64, made where first needed.
+  double z64 = 0.0;
+  auto need_z64 = [&]() __attribute__((always_inline)) {
+    if (!softmax || z64 != 0.0) return;
+    for (int i = 0; i < a.width; ++i) {
+      const float v = live && i < count ? router_logit<BF16>(a.logits, t * E + base + i * step) : kNone;
+      if (v > kNone) z64 += v == m ? 1.0 : exp((double)v - (double)m);
+    }
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) z64 += shfl_xor_f64(z64, o);
+  };
+  auto score64 = [&](float v) __attribute__((always_inline)) -> double {
+    return softmax ? (v == m ? 1.0 : exp((double)v - (double)m)) / z64 : 1.0 / (1.0 + exp(-(double)v));
+  };
+
   // choices: x itself without a bias; groups by sums look at the scores
   bool unsure = false;
   float c[NV];
@@ -369,12 +389,12 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
 #pragma unroll
     for (int i = 0; i < NV; i += 4) {
       float b[4] = {0.f, 0.f, 0.f, 0.f};
-      if (a.vec > 1 && i < count) {
+      if (wide && i < count) {
         const float4 v = *reinterpret_cast<const float4*>(a.bias + base + i);
         b[0] = v.x; b[1] = v.y; b[2] = v.z; b[3] = v.w;
-      } else if (a.vec == 1) {
+      } else if (!wide) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) b[k] = i + k < count ? a.bias[base + i + k] : 0.f;
+        for (int k = 0; k < 4; ++k) b[k] = i + k < count ? a.bias[base + (i + k) * step] : 0.f;
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -435,11 +455,10 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
         tol = 2.f * choice_tol(1.f, row_reduce_f32<L, true>(far));
       }
       const bool close = a.topk_group < a.n_group && best > kNone && !(worst - best > tol);
-      if (softmax || (sums && worst < 0x1p-100f)) {
-        // a softmax's sum would be needed in fp64, and sums of scores next to
-        // fp32's smallest have no relative bound: the exact path
-        unsure = close;
-      } else if (__ballot(close)) {
+      // (sums of scores next to fp32's smallest have no relative bound)
+      if (sums) unsure = close && worst < 0x1p-100f;
+      if (__ballot(close && !unsure)) {
+        need_z64();
         // Groups next to the border between kept and left ones are ranked by
         // their fp64 totals, from those of their choices that may be among the
         // largest; the others' places are certain.
@@ -454,9 +473,9 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
         while (__ballot(able != 0)) {
           double u = kNone64;
           if (able != 0) {
-            const int e = base + __ffs(able) - 1;
+            const int e = base + (__ffs(able) - 1) * step;
             able &= able - 1;
-            u = 1.0 / (1.0 + exp(-(double)router_logit<BF16>(a.logits, t * E + e)));
+            u = score64(router_logit<BF16>(a.logits, t * E + e));
             if (biased) u += (double)a.bias[e];
           }
           s64 = fmax(s64, fmin(f64, u));
@@ -484,7 +503,7 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
   uint32_t key[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i)   // + 0: zeros of both signs are equal
-    key[i] = c[i] > kNone ? (sortable(c[i] + 0.f) & ~kIdx) | (kIdx - (uint32_t)(base + i)) : 0u;
+    key[i] = c[i] > kNone ? (sortable(c[i] + 0.f) & ~kIdx) | (kIdx - (uint32_t)(base + i * step)) : 0u;
   const bool cut = !BF16 || biased;   // keys hold a part of the choice
   uint32_t mine = 0, last = 0;
   auto take = [&](int j) __attribute__((always_inline)) {
@@ -553,10 +572,9 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
       const int e2 = __shfl(e, lane + 1);
       const bool close = rl < K && rl + 1 < taken && e2 >= 0 && !(ch - ch2 > tol + tol2);
       if (__ballot(close)) {
-        // neighbours too close for fp32: the logistic function's choices in
-        // fp64; a softmax's need its sum in fp64 and go the exact way
-        if (softmax) unsure = unsure || close;
-        else sort(e >= 0 ? 1.0 / (1.0 + exp(-(double)v)) + (double)a.bias[e] : -(double)kRouterInf);
+        // neighbours too close for fp32: in the order of their fp64 choices
+        need_z64();
+        sort(e >= 0 ? score64(v) + (double)a.bias[e] : -(double)kRouterInf);
       }
     }
   }
@@ -584,8 +602,8 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(RouterAr
   if constexpr (PLAIN) {
     a.bias = nullptr;
     a.n_group = a.topk_group = a.group_top = 1;
+    a.per = a.E;
     a.lanes = L;
-    a.width = NV;
   }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   double* mine = keys_lds + wave * a.E;
@@ -637,10 +655,10 @@ hipError_t launch_router_topk(const void* logits, bool bf16, const float* bias, 
   const bool aligned = (uintptr_t)logits % 16 == 0 && (uintptr_t)bias % 16 == 0;
   const int vec = !aligned || per % 4 ? 1 : per % 8 || NV % 8 ? 4 : 8;
   const int share = (per + lanes - 1) / lanes;
-  const int width = n_group == 1 ? NV : (share + vec - 1) / vec * vec;
+  const int width = (share + vec - 1) / vec * vec;
   const bool fast = K < L - 1 && width <= NV;
   const RouterArgs a{logits, bias, T, E, K, score, n_group, topk_group, group_top, (int)renormalize,
-                     lanes, width, vec, scale, ids, weights};
+                     per, lanes, width, vec, scale, ids, weights};
   if (fast) {
     if (L == 16) {
       if (NV == 4) router_launch<16, 4, true>(a, bf16, stream);
