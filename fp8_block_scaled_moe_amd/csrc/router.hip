@@ -36,10 +36,10 @@
 //     are ranked by fp64 totals of their best choices;
 //   * what is left for the exact path: more close candidates than lanes, and
 //     close groups whose scores are next to fp32's smallest.
-// In a graph, us for 8192 tokens of 256 experts, top-8: softmax 6.4 (bf16 logits
-// 5.1), sigmoid with bias 8.3, softmax with bias 12.4, groups by their maximum
-// 7.3, by the sum of two 10.2 (14 while close ones went the exact way); 65537
-// tokens of 128: 15.8, 2.4 TB/s; one token of 256: 3.6; 64: 3.9.
+// In a graph, us for 8192 tokens of 256 experts, top-8: softmax 6.6 (bf16 logits
+// 5.3), sigmoid with bias 8.2, softmax with bias 12.1, groups by their maximum
+// 7.3, by the sum of two 9.8 (14 while close ones went the exact way); 65537
+// tokens of 128: 15.8, 2.4 TB/s; one token of 256: 3.7; 64: 4.0.
 // Bound by the K rounds of maximum and removal and their shuffles, at few tokens
 // by the launch and one trip to memory.
 #include "device_common.h"
@@ -642,11 +642,10 @@ hipError_t launch_router_topk(const void* logits, bool bf16, const float* bias, 
   // least one further candidate has a lane) or 16 groups, and, from 129 experts
   // on, where the tokens are few: fewer values a lane are the shorter way until
   // the waves queue.  16 and 64 lanes, us, fp32 softmax | biased sigmoid: 256
-  // experts, T=64 5.2, 4.2 | 6.5, 4.6; T=3000 6.0, 5.7 | 7.5, 6.2; T=4096 6.1,
-  // 6.1 | 7.6, 6.8; T=8192 6.7, 9.0 | 8.3, 10.1.  512 experts, T=64 7.6, 4.7;
-  // T=6000 10.3, 9.3; T=8192 10.7, 11.5.  128 experts, T=64 4.3, 4.2; T=2048
-  // 4.5, 4.7.  (With bias and groups compiled in.)
-  const bool few = E > 128 && T <= 12 * E;
+  // experts, T=64 5.2, 4.0 | 6.5, 4.4; T=4096 6.0, 5.7 | 7.4, 6.6; T=8192 6.6,
+  // 8.4 | 8.2, 9.8.  512 experts, T=64 7.6, 4.6; T=8192 11.0, 10.4; T=16384
+  // 15.5, 17.6.  128 experts, T=64 4.3, 4.2; T=2048 4.5, 4.7.
+  const bool few = E > 128 && T <= 16 * E;
   const int L = !few && E <= 512 && K < 15 && n_group <= 16 ? 16 : 64;
   const int NV = L == 16 ? (E <= 64 ? 4 : E <= 128 ? 8 : E <= 256 ? 16 : 32) : E <= 256 ? 4 : E <= 512 ? 8 : 16;
   const int per = E / n_group;
