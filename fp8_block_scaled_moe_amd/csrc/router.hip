@@ -647,7 +647,7 @@ hipError_t launch_router_topk(const void* logits, bool bf16, const float* bias, 
   // 15.5, 17.6.  128 experts, T=64 4.3, 4.2; T=2048 4.5, 4.7.
   const bool few = E > 128 && T <= 16 * E;
   const int L = !few && E <= 512 && K < 15 && n_group <= 16 ? 16 : 64;
-  const int NV = L == 16 ? (E <= 64 ? 4 : E <= 128 ? 8 : E <= 256 ? 16 : 32) : E <= 256 ? 4 : E <= 512 ? 8 : 16;
+  int NV = L == 16 ? (E <= 64 ? 4 : E <= 128 ? 8 : E <= 256 ? 16 : 32) : E <= 256 ? 4 : E <= 512 ? 8 : 16;
   const int per = E / n_group;
   int lanes = L;
   while (lanes * n_group > L) lanes /= 2;
@@ -655,6 +655,7 @@ hipError_t launch_router_topk(const void* logits, bool bf16, const float* bias, 
   const int vec = !aligned || per % 4 ? 1 : per % 8 || NV % 8 ? 4 : 8;
   const int share = (per + lanes - 1) / lanes;
   const int width = (share + vec - 1) / vec * vec;
+  while (NV < width && NV < (L == 16 ? 32 : 16)) NV *= 2;   // groups of a size that leaves lanes empty
   const bool fast = K < L - 1 && width <= NV;
   const RouterArgs a{logits, bias, T, E, K, score, n_group, topk_group, group_top, (int)renormalize,
                      per, lanes, width, vec, scale, ids, weights};

@@ -638,8 +638,8 @@ def moe_fused_int8(x, x_scale, w13, w13_scale, w2, w2_scale, topk_ids, topk_weig
     out = _out(out, torch.bfloat16, (T, H), x, "out")
     if workspace is None:
         workspace = alloc_workspace_int8(T, H, I, E, K, x.device)
-    elif workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous and on the tensors' device")
+    else:
+        _check(workspace, workspace.dtype, workspace.shape, index, "workspace")
     _launch(index, lib().moe_fused_int8, x.data_ptr(), x_scale.data_ptr(), w13.data_ptr(), w13_scale.data_ptr(),
             w2.data_ptr(), w2_scale.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), T, H, I, E, K,
             out.data_ptr(), workspace.data_ptr(), workspace.nbytes, tile_m, weight_layout)
@@ -756,11 +756,11 @@ def add_rmsnorm_quant(x, weight, eps, format, residual=None, want_norm=False, q=
     _need(x, torch.bfloat16, "x", 2)
     T, H = shape = x.shape
     index = x.get_device()
-    weight_f32 = weight.dtype == torch.float32
+    weight_f32 = getattr(weight, "dtype", None) == torch.float32
     _check(weight, torch.float32 if weight_f32 else torch.bfloat16, (H,), index, "weight")
     residual_f32 = False
     if residual is not None:
-        residual_f32 = residual.dtype == torch.float32
+        residual_f32 = getattr(residual, "dtype", None) == torch.float32
         _check(residual, torch.float32 if residual_f32 else torch.bfloat16, shape, index, "residual")
         residual_out = _out(residual_out, residual.dtype, shape, x, "residual_out")
     elif residual_out is not None:
@@ -794,7 +794,7 @@ def moe_router_topk(logits, K, score=SCORE_SOFTMAX, bias=None, n_group=1, topk_g
     softmax or sigmoid, chosen by score + bias (fp32 [E]) among the topk_group best of n_group expert
     groups, ties to the lower index; weights are the scores, renormalised and scaled (see
     moe_router_topk in include/fp8moe.h).  Returns (ids int32 [T, K], weights fp32 [T, K])."""
-    bf16 = logits.dtype == torch.bfloat16
+    bf16 = getattr(logits, "dtype", None) == torch.bfloat16
     _need(logits, torch.bfloat16 if bf16 else torch.float32, "logits", 2)
     T, E = logits.shape
     index = logits.get_device()

@@ -109,7 +109,8 @@ def test_close_scores(score):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("biased", [False, True])
 @pytest.mark.parametrize("E,n_group,K", [(160, 8, 8), (66, 6, 5), (231, 7, 9), (500, 10, 14), (384, 12, 8), (51, 17, 4),
-                                         (48, 16, 3), (63, 63, 20), (1023, 33, 8), (4, 2, 2), (392, 8, 7)])
+                                         (48, 16, 3), (63, 63, 20), (1023, 33, 8), (4, 2, 2), (392, 8, 7),
+                                         (240, 6, 8), (252, 12, 8), (60, 5, 6), (120, 3, 8), (448, 14, 8), (990, 6, 30)])
 def test_groups_of_any_size(E, n_group, K, biased, dtype):
     """Groups that are no whole numbers of lanes, or vectors, or fewer than lanes; rows that start unaligned."""
     say("router group sizes", E, n_group, K, biased, dtype)
