@@ -871,13 +871,12 @@ bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 //     2233, 2114, 2100 | 1979; T=2048: 5174, 4374, 4212 | 2261
 //   layer, one expert, H=7168, I=2048:   T=64: 33, 32, 39 | 60; T=384: 113, 100,
 //     96 | 94; T=512: 141, 124, 115 | 114; T=1024: 266, 228, 210 | 116
-//   GEMM1, H=2048, I=768, by rows x experts (W, rows x N tiles):
-//     1024x1 (24, 6144): 24, 20, 20 | 27; 2048x1 (48, 12288): 45, 40, 37 | 27;
-//     64x8 (54, 3072): 15, 15, 20 | 15; 128x8 (66, 6144): 25, 23, 24 | 19;
-//     64x12 (84, 4608): 21, 21, 24 | 18; 32x16 (96, 3072): 17, 18, 18 | 13
-//   GEMM1, H=7168, I=2048: 64x2 (32, 2048): 28, 28, 31 | 43; 32x4 (64, 2048): 30,
-//     29, 26 | 36; 64x4 (64, 4096): 46, 43, 47 | 47; 32x8 (128, 4096): 57, 54,
-//     44 | 36
+//   GEMM1, H=2048, I=768, rows x experts (W; rows x N tiles a CU): 1024x1 (24;
+//     24): 24, 20, 20 | 27; 2048x1 (48; 48): 45, 40, 37 | 27; 64x8 (54; 12): 15,
+//     15, 20 | 15; 128x8 (66; 24): 25, 23, 24 | 19; 64x12 (84; 18): 21, 21, 24 |
+//     18; 32x16 (96; 12): 17, 18, 18 | 13
+//   GEMM1, H=7168, I=2048: 64x2 (32; 8): 28, 28, 31 | 43; 32x4 (64; 8): 30, 29,
+//     26 | 36; 64x4 (64; 16): 46, 43, 47 | 47; 32x8 (128; 16): 57, 54, 44 | 36
 int int8_tile_m(int requested, int64_t R, int E, int64_t NT) {
   if (requested != -1) return requested;
   const int64_t active = R < E ? R : E, rows = active > 0 ? (R + active - 1) / active : 0;
