@@ -858,31 +858,30 @@ bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 // Tile height of one of the int8 products, of NT N tiles of 256 weight rows.
 //
 // Beyond an even share of 8 rows an expert, the tile kernels, if their
-// workgroups W fill 3/8 of the chip, or 3/16 of it and the streaming kernel
-// would have more than 16 rows x N tiles for each CU: a K step of that one
-// takes as long as it has rows, a tile's about the same however few there are.
-// Else the streaming kernel: 16 rows to a share, 32 (whose waves hold more
-// weights in flight) up to 64 rows, 64 beyond, where weights read once for 64
-// rows win.  Packed weights, us for heights 16, 32, 64 | tiles:
+// workgroups W fill 3/8 of the chip, or each CU has 12 rows x N tiles to do: a
+// K step of the streaming kernel takes as long as it has rows.  Else the
+// streaming kernel: 16 rows to a share, or 32, whose waves hold more weights in
+// flight (64 rows, for calls that ask for them, win by a few percent from 256
+// rows of one expert on, where the tile kernels do by far).  Packed weights, us
+// for heights 16, 32, 64 | tiles:
 //   layer, E=128, top-8, H=2048, I=768:  T=128: 136, 143, 168 | 144; T=256: 163,
 //     171, 194 | 152; T=512: 227, 233, 238 | 161; T=4096: 1175, 1066, 1047 | 307
 //     (Zipf 1.2: T=128: 96, 107, 146 | 89; T=512: 225, 220, 265 | 123)
 //   layer, E=256, top-8, H=7168, I=2048: T=256: 1888, 1907, 1951 | 1934; T=512:
 //     2233, 2114, 2100 | 1979; T=2048: 5174, 4374, 4212 | 2261
-//   layer, one expert, H=7168, I=2048:   T=64: 33, 32, 39 | 60; T=384: 113, 100,
-//     96 | 94; T=512: 141, 124, 115 | 114; T=1024: 266, 228, 210 | 116
-//   GEMM1, H=2048, I=768, rows x experts (W; rows x N tiles a CU): 1024x1 (24;
-//     24): 24, 20, 20 | 27; 2048x1 (48; 48): 45, 40, 37 | 27; 64x8 (54; 12): 15,
-//     15, 20 | 15; 128x8 (66; 24): 25, 23, 24 | 19; 64x12 (84; 18): 21, 21, 24 |
-//     18; 32x16 (96; 12): 17, 18, 18 | 13
-//   GEMM1, H=7168, I=2048: 64x2 (32; 8): 28, 28, 31 | 43; 32x4 (64; 8): 30, 29,
-//     26 | 36; 64x4 (64; 16): 46, 43, 47 | 47; 32x8 (128; 16): 57, 54, 44 | 36
+//   layer, one expert, H=7168, I=2048:   T=64: 33, 32, 39 | 51; T=256: 82, 72,
+//     70 | 56; T=512: 141, 124, 115 | 61; T=1024: 266, 228, 210 | 85
+//   layer, rows x experts, top-1 (W of GEMM1; rows x N tiles a CU): H=2048,
+//     I=768: 64x4 (24; 6): 30, 29, 29 | 34; 512x1 (12; 12): 37, 36, 36 | 36;
+//     1024x1 (24; 24): 55, 53, 51 | 40; 64x12 (84; 18): 49, 50, 55 | 40; 32x16
+//     (96; 12): 41, 43, 43 | 37; H=7168, I=2048: 64x2 (32; 8): 55, 56, 62 | 54;
+//     64x4 (64; 16): 87, 82, 91 | 63; 32x8 (128; 16): 123, 115, 110 | 93
 int int8_tile_m(int requested, int64_t R, int E, int64_t NT) {
   if (requested != -1) return requested;
   const int64_t active = R < E ? R : E, rows = active > 0 ? (R + active - 1) / active : 0;
   const int64_t W = (R / kTileMaxInt8 + active) * NT, cus = device_num_cu();
-  if (rows > 8 && (8 * W >= 3 * cus || (16 * W >= 3 * cus && R * NT > 16 * cus))) return kTileMaxInt8;
-  return rows <= 16 ? 16 : rows <= 64 ? 32 : 64;
+  if (rows > 8 && (8 * W >= 3 * cus || R * NT >= 12 * cus)) return kTileMaxInt8;
+  return rows <= 16 ? 16 : 32;
 }
 
 int check_int8_stage(int64_t T, int32_t H, int32_t I, int32_t E, int32_t K, int32_t align, int64_t cap,

@@ -1,8 +1,8 @@
 // Tile kernels of the experts' int8 products, for experts of many rows: the
 // same results as the streaming kernels of experts_int8.hip.
 //
-// A workgroup of 8 waves owns an M tile of up to 288 tokens and a run of N
-// tiles of 256 weight rows (GEMM1: the gate and up rows of 128 columns).
+// A workgroup of 8 waves owns an M tile of up to 288 tokens (fewer where few
+// tiles would leave CUs without work) and a run of N tiles of 256 weight rows (GEMM1: the gate and up rows of 128 columns).
 // The waves form a WM x 8/WM grid: WM token parts, 8/WM weight parts of 32 WM
 // rows.  With WM = 2 each wave holds 64 weight rows x up to 144 tokens of
 // int32 sums (144 VGPRs), so a 128-byte K step reads each token row from LDS
@@ -364,22 +364,27 @@ __device__ __forceinline__ void tile_gemm2(const TokenBuffers& tb, RowInfo& ri, 
 // of popular experts and another the short ones: Zipf 1.2 routing (H=2048,
 // I=768, E=128, top-8) took 171 us at T=512 and 398 at T=4096 that way, 124
 // and 346 this way.
-// The range's tiles come first, being the tall ones.
-template <int TMAX>
+// The range's tiles come first, being the tall ones.  lone = 0: all tiles are
+// dealt out evenly.
 struct TileChunk {   // experts c + 4 lane .. + 3: their rows and tile counts (0 past E)
   int start[5], nt[4];
-  __device__ __forceinline__ void load(const int32_t* __restrict__ padded, int E, int c, int lane) {
+  // inv: (2^32 - 1) / tmax, whose product with a length is its quotient or one less
+  __device__ __forceinline__ void load(const int32_t* __restrict__ padded, int E, int tmax, uint32_t inv, int c,
+                                       int lane) {
     const int e0 = c + 4 * lane;
 #pragma unroll
     for (int k = 0; k < 5; ++k) start[k] = padded[min(e0 + k, E)];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) nt[k] = e0 + k < E ? tiles_of<TMAX>(start[k + 1] - start[k]) : 0;
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t len = start[k + 1] - start[k] + tmax - 1, n = __umulhi(len, inv);
+      nt[k] = e0 + k >= E ? 0 : len - n * tmax >= (uint32_t)tmax ? n + 1 : n;
+    }
   }
-  // inclusive prefix over the lanes of the tiles of experts with more than one
-  __device__ __forceinline__ int many(int lane) const {
+  // inclusive prefix over the lanes of the tiles of experts with more than `lone`
+  __device__ __forceinline__ int many(int lone, int lane) const {
     int sum = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sum += nt[k] > 1 ? nt[k] : 0;
+    for (int k = 0; k < 4; ++k) sum += nt[k] > lone ? nt[k] : 0;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const int v = __shfl_up(sum, o);
@@ -409,16 +414,16 @@ struct TileChunk {   // experts c + 4 lane .. + 3: their rows and tile counts (0
   }
 };
 
-template <int TMAX>
-__device__ __forceinline__ bool tile_item(const int32_t* __restrict__ padded,
-                                              const int32_t* __restrict__ sorted_src, int E, int NG, int x, int slot,
-                                              TileCoord& tc) {
+__device__ __forceinline__ bool tile_item(const int32_t* __restrict__ padded, const int32_t* __restrict__ sorted_src,
+                                          int E, int tmax, int lone, int NG, int x, int slot,
+                                          TileCoord& tc) {
   const int lane = threadIdx.x & 63;
-  TileChunk<TMAX> ch;
+  const uint32_t inv = 0xffffffffu / (uint32_t)tmax;
+  TileChunk ch;
   int many = 0;
   for (int c = 0; c < E; c += 256) {
-    ch.load(padded, E, c, lane);
-    many += __builtin_amdgcn_readlane(ch.many(lane), 63);
+    ch.load(padded, E, tmax, inv, c, lane);
+    many += __builtin_amdgcn_readlane(ch.many(lone, lane), 63);
   }
   const int share = (many * NG + kNumXcd - 1) / kNumXcd;
   const int a0 = min(x * share, many * NG), a1 = min(a0 + share, many * NG);
@@ -427,8 +432,8 @@ __device__ __forceinline__ bool tile_item(const int32_t* __restrict__ padded,
     const int t = (a0 + slot) / NG;   // its tile among those of experts with more than one
     int base = 0, incl;
     for (;; c += 256) {
-      ch.load(padded, E, c, lane);
-      incl = ch.many(lane);
+      ch.load(padded, E, tmax, inv, c, lane);
+      incl = ch.many(lone, lane);
       const int total = __builtin_amdgcn_readlane(incl, 63);
       if (base + total > t) break;   // t < many, so this stops at a chunk of the experts
       base += total;
@@ -439,7 +444,7 @@ __device__ __forceinline__ bool tile_item(const int32_t* __restrict__ padded,
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int n = __builtin_amdgcn_readlane(ch.nt[i], own);
-      o_nt[i] = n > 1 ? n : 0;
+      o_nt[i] = n > lone ? n : 0;
     }
 #pragma unroll
     for (int i = 0; i < 3; ++i)   // skip the lane's experts whose tiles all precede t
@@ -457,8 +462,8 @@ __device__ __forceinline__ bool tile_item(const int32_t* __restrict__ padded,
     tc.run = rest - ord * NG;
     uint64_t m = 0;
     for (;; c += 256) {
-      if (c >= E) return false;
-      ch.load(padded, E, c, lane);
+      if (c >= E || lone == 0) return false;
+      ch.load(padded, E, tmax, inv, c, lane);
       m = ch.single(x);
       const int n = __popcll(m);
       if (ord < n) break;
@@ -476,15 +481,6 @@ __device__ __forceinline__ bool tile_item(const int32_t* __restrict__ padded,
   tc.h = min(tc.tm, len - mt * tc.tm);
   tc.e = c + 4 * own + k;
   return sorted_src[tc.p0] >= 0;   // false: segment padding only, nothing to compute
-}
-
-// Workgroups for every possible item; those past the actual ones (known on the
-// device only) exit at once.  An expert of more than one tile has more than
-// TMAX padded rows, so their tiles are at most twice the padded rows / TMAX.
-static unsigned tile_grid(const GroupedRows& g, int NG) {
-  const int64_t singles = (g.E < g.rows ? (g.E + kNumXcd - 1) / kNumXcd : g.rows) * NG;
-  const int64_t many = (2 * g.cap / kTileMaxInt8 * NG + kNumXcd - 1) / kNumXcd;
-  return (unsigned)(kNumXcd * (singles + many));
 }
 
 // one uniform branch per workgroup on its tile height, in steps of 32 rows
@@ -505,15 +501,15 @@ template <bool PACKED>
 __global__ __launch_bounds__(kThreads) void gemm1_tile_int8_kernel(
     const uint8_t* __restrict__ x, const float* __restrict__ x_scale, const uint8_t* __restrict__ w13,
     const float* __restrict__ w13_scale, const int32_t* __restrict__ padded, const int32_t* __restrict__ sorted_src,
-    int E, int K, int H, int I, int NB, uint32_t x_bytes, uint16_t* __restrict__ act) {
+    int E, int K, int H, int I, int tmax, int lone, int NB, uint32_t x_bytes, uint16_t* __restrict__ act) {
   __shared__ __attribute__((aligned(1024))) uint8_t tb0[kTileMaxInt8 * kKB], tb1[kTileMaxInt8 * kKB],
       tb2[kTileMaxInt8 * kKB], tb3[kTileMaxInt8 * kKB];
   __shared__ RowInfo ri;
   const TokenBuffers tb{{tb0, tb1, tb2, tb3}};
   const int NT = I / 128;
   TileCoord tc;
-  if (!tile_item<kTileMaxInt8>(padded, sorted_src, E, (NT + NB - 1) / NB, blockIdx.x % kNumXcd, blockIdx.x / kNumXcd,
-                               tc))
+  if (!tile_item(padded, sorted_src, E, tmax, lone, (NT + NB - 1) / NB, blockIdx.x % kNumXcd, blockIdx.x / kNumXcd,
+                 tc))
     return;
 #define FP8MOE_BODY(TM, WM) \
   tile_gemm1<TM, WM, PACKED>(tb, ri, tc, x, x_scale, w13, w13_scale, sorted_src, K, H, I, NB, x_bytes, act)
@@ -525,15 +521,15 @@ template <bool PACKED, typename YT>
 __global__ __launch_bounds__(kThreads) void gemm2_tile_int8_kernel(
     const uint8_t* __restrict__ q, const float* __restrict__ q_scale, const uint8_t* __restrict__ w2,
     const float* __restrict__ w2_scale, const float* __restrict__ topk_weights, const int32_t* __restrict__ padded,
-    const int32_t* __restrict__ sorted_src, int E, int H, int I, int NB, YT* __restrict__ Y) {
+    const int32_t* __restrict__ sorted_src, int E, int H, int I, int tmax, int lone, int NB, YT* __restrict__ Y) {
   __shared__ __attribute__((aligned(1024))) uint8_t tb0[kTileMaxInt8 * kKB], tb1[kTileMaxInt8 * kKB],
       tb2[kTileMaxInt8 * kKB], tb3[kTileMaxInt8 * kKB];
   __shared__ RowInfo ri;
   const TokenBuffers tb{{tb0, tb1, tb2, tb3}};
   const int NT = (H + kTN - 1) / kTN;
   TileCoord tc;
-  if (!tile_item<kTileMaxInt8>(padded, sorted_src, E, (NT + NB - 1) / NB, blockIdx.x % kNumXcd, blockIdx.x / kNumXcd,
-                               tc))
+  if (!tile_item(padded, sorted_src, E, tmax, lone, (NT + NB - 1) / NB, blockIdx.x % kNumXcd, blockIdx.x / kNumXcd,
+                 tc))
     return;
 #define FP8MOE_BODY(TM, WM) \
   tile_gemm2<TM, WM, PACKED, YT>(tb, ri, tc, q, q_scale, w2, w2_scale, topk_weights, sorted_src, H, I, NB, Y)
@@ -548,14 +544,56 @@ __global__ __launch_bounds__(kThreads) void gemm2_tile_int8_kernel(
 // of 56 steps 2013, 2039, -, 2041 and GEMM2 of 16 steps 1135, 1100, 1107, 1152
 // (T=8192, H=7168, I=2048, E=256, top-8); GEMM1 of 16 steps 215, 190, 186, 228
 // (T=4096, H=2048, I=768, E=128, top-8, Zipf 1.2).
-static int run_int8(const GroupedRows& g, int NT, int KT) {
+static int run_int8(const GroupedRows& g, int tmax, int NT, int KT) {
   if (KT % 4) return 1;   // N tiles of a run end on whole rounds of the token buffers
   const int64_t cu = g.num_cu > 0 ? g.num_cu : 256;
-  const int64_t mt = g.rows / kTileMaxInt8 + (g.E < g.rows ? g.E : g.rows);
+  const int64_t mt = g.rows / tmax + (g.E < g.rows ? g.E : g.rows);
   int nb = (31 + KT) / KT;
   if (nb > NT) nb = NT;
   while (nb > 1 && mt * NT < 2 * cu * nb) nb /= 2;
   return nb;
+}
+
+// tmax: the tallest tile; lone: experts of up to that many tiles go to one XCD
+// each; NB: N tiles of a run.
+struct TilePlan {
+  int tmax, lone, NB;
+  unsigned grid;
+};
+
+static TilePlan tile_plan(const GroupedRows& g, int NT, int KT) {
+  const int64_t cu = g.num_cu > 0 ? g.num_cu : 256, active = g.E < g.rows ? g.E : g.rows;
+  const int64_t share = (g.rows + active - 1) / active;
+  TilePlan p{kTileMaxInt8, 1, 1, 0};
+  // Where few experts leave the chip empty, tiles of the smallest of these
+  // heights whose workgroups fill it no more than once: a K step of a short
+  // tile is shorter, and weights that more tiles read come from L2.  The count
+  // is of an even share, or with half a tile an expert left over.  Tiles of
+  // 288, 160, 96, 64 rows (us, packed): one expert, H=7168, I=2048, GEMM1 and
+  // GEMM2: T=256 67, 45, 44, 29 and 26, 17, 16, 11; T=1024 68, 51, 46, 37 and
+  // 29, 23, 33, 27; T=2048 72, 57, 90, 77 and 33, 43, 52, 52; H=2048, I=768,
+  // 128 rows of 8 experts each 19, 20, 16, 13 and 12, 12, 10, 9; T=4096, Zipf
+  // 1.2, E=128: 159, 172, 210, 212 and 127, 157, 196, 220.  (32 rows: 27, 59,
+  // 115, 12, 327 and 11, 42, 68, 13, 361.)
+  for (const int tm : {160, 96, 64}) {
+    const int64_t even = active * ((share + tm - 1) / tm), half = g.rows / tm + active / 2;
+    if ((even > half ? even : half) * NT <= cu) p.tmax = tm;
+  }
+  p.NB = run_int8(g, p.tmax, NT, KT);
+  const int NG = (NT + p.NB - 1) / p.NB;
+  // few of them: all are dealt out evenly (two experts of 64 rows, tiles of 64:
+  // GEMM1 33 -> 30 us, GEMM2 26 -> 13)
+  if ((g.rows / p.tmax + active) * NG <= cu) p.lone = 0;
+  // Workgroups for every possible item; those past the actual ones (known on
+  // the device only) exit at once.  An expert of more than one tile has more
+  // than tmax padded rows, so their tiles are at most twice the padded rows /
+  // tmax; those of all experts, at most one an expert and the padded rows /
+  // tmax.
+  const int64_t class_size = (g.E + kNumXcd - 1) / kNumXcd, singles = (class_size < g.rows ? class_size : g.rows) * NG;
+  const int64_t tiles = p.lone ? 2 * g.cap / p.tmax : g.cap / p.tmax + active;
+  const int64_t many = (tiles * NG + kNumXcd - 1) / kNumXcd;
+  p.grid = (unsigned)(kNumXcd * ((p.lone ? singles : 0) + many));
+  return p;
 }
 
 hipError_t launch_gemm1_int8_tile(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
@@ -563,14 +601,14 @@ hipError_t launch_gemm1_int8_tile(const uint8_t* x, const float* x_scale, const 
                                   hipStream_t stream) {
   if (g.rows / g.K * H >= (int64_t)1 << 32) return hipErrorInvalidValue;   // x: 32-bit offsets of its rows
   const uint32_t x_bytes = (uint32_t)(g.rows / g.K * H);
-  const int NT = I / 128, NB = run_int8(g, NT, H / kKB), NG = (NT + NB - 1) / NB;
-  const dim3 grid(tile_grid(g, NG)), block(kThreads);
+  const TilePlan p = tile_plan(g, I / 128, H / kKB);
+  const dim3 grid(p.grid), block(kThreads);
   if (packed)
     hipLaunchKernelGGL((gemm1_tile_int8_kernel<true>), grid, block, 0, stream, x, x_scale, w13, w13_scale,
-                       g.padded_indptr, g.sorted_src, g.E, g.K, H, I, NB, x_bytes, act);
+                       g.padded_indptr, g.sorted_src, g.E, g.K, H, I, p.tmax, p.lone, p.NB, x_bytes, act);
   else
     hipLaunchKernelGGL((gemm1_tile_int8_kernel<false>), grid, block, 0, stream, x, x_scale, w13, w13_scale,
-                       g.padded_indptr, g.sorted_src, g.E, g.K, H, I, NB, x_bytes, act);
+                       g.padded_indptr, g.sorted_src, g.E, g.K, H, I, p.tmax, p.lone, p.NB, x_bytes, act);
   return hipGetLastError();
 }
 
@@ -578,14 +616,14 @@ template <typename YT>
 hipError_t launch_gemm2_int8_tile(const uint8_t* q, const float* q_scale, const uint8_t* w2, const float* w2_scale,
                                   const float* topk_weights, const GroupedRows& g, int H, int I, YT* Y,
                                   bool packed, hipStream_t stream) {
-  const int NT = (H + kTN - 1) / kTN, NB = run_int8(g, NT, I / kKB), NG = (NT + NB - 1) / NB;
-  const dim3 grid(tile_grid(g, NG)), block(kThreads);
+  const TilePlan p = tile_plan(g, (H + kTN - 1) / kTN, I / kKB);
+  const dim3 grid(p.grid), block(kThreads);
   if (packed)
     hipLaunchKernelGGL((gemm2_tile_int8_kernel<true, YT>), grid, block, 0, stream, q, q_scale, w2, w2_scale,
-                       topk_weights, g.padded_indptr, g.sorted_src, g.E, H, I, NB, Y);
+                       topk_weights, g.padded_indptr, g.sorted_src, g.E, H, I, p.tmax, p.lone, p.NB, Y);
   else
     hipLaunchKernelGGL((gemm2_tile_int8_kernel<false, YT>), grid, block, 0, stream, q, q_scale, w2, w2_scale,
-                       topk_weights, g.padded_indptr, g.sorted_src, g.E, H, I, NB, Y);
+                       topk_weights, g.padded_indptr, g.sorted_src, g.E, H, I, p.tmax, p.lone, p.NB, Y);
   return hipGetLastError();
 }
 

@@ -135,6 +135,22 @@ def test_stages(align, tile_m):
     assert not Yn[p.ids.numpy().reshape(-1) < 0].any()
 
 
+@pytest.mark.parametrize("T,H,I,E,K,skew,drop", [
+    (400, 512, 256, 1, 1, 0.0, 0.0), (4096, 256, 640, 1, 1, 0.0, 0.0), (4100, 128, 1024, 1, 1, 0.0, 0.0),
+    (4097, 256, 2048, 1, 1, 0.0, 0.1), (900, 256, 512, 3, 2, 1.2, 0.3), (300, 384, 1152, 20, 4, 1.2, 0.0),
+    (597, 256, 1024, 34, 7, 1.2, 0.0), (129, 640, 384, 2, 1, 0.0, 0.0), (65, 128, 128, 9, 9, 0.0, 0.5)])
+def test_few_tiles(T, H, I, E, K, skew, drop):
+    """Launches whose tiles leave CUs without work: their heights and their order over the XCDs change no bit."""
+    say("int8 few tiles", T, H, I, E, K, skew, drop)
+    p = Problem(T, H, I, E, K, seed=T, skew=skew, drop=drop)
+    ref = p.run(tile_m=32)
+    for packed in (False, True):
+        assert torch.equal(p.run(tile_m=288, packed=packed), ref)
+        assert torch.equal(p.run(packed=packed), ref)
+    if T * K < 1000:
+        assert_rows_close_to_oracle(ref, p.oracle(), "int8 few tiles")
+
+
 @pytest.mark.parametrize("H,low", [(16384, -128), (16256, -127)])
 def test_largest_sums_are_exact(H, low):
     """Every product at its largest: the int32 sums reach 16384 * 128 * 128 = 2^28."""
