@@ -2,7 +2,8 @@
 // same results as the streaming kernels of experts_int8.hip.
 //
 // A workgroup of 8 waves owns an M tile of up to 288 tokens (fewer where few
-// tiles would leave CUs without work) and a run of N tiles of 256 weight rows (GEMM1: the gate and up rows of 128 columns).
+// tiles would leave CUs without work) and a run of N tiles of 256 weight rows
+// (GEMM1: the gate and up rows of 128 columns).
 // The waves form a WM x 8/WM grid: WM token parts, 8/WM weight parts of 32 WM
 // rows.  With WM = 2 each wave holds 64 weight rows x up to 144 tokens of
 // int32 sums (144 VGPRs), so a 128-byte K step reads each token row from LDS
