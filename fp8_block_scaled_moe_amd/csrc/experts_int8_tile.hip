@@ -364,7 +364,7 @@ __device__ __forceinline__ void tile_gemm2(const TokenBuffers& tb, RowInfo& ri, 
 // tiles, as the other formats' kernels deal them, give one XCD the tall tiles
 // of popular experts and another the short ones: Zipf 1.2 routing (H=2048,
 // I=768, E=128, top-8) took 171 us at T=512 and 398 at T=4096 that way, 124
-// and 346 this way.
+// and 350 this way.
 // The range's tiles come first, being the tall ones.  lone = 0: all tiles are
 // dealt out evenly.
 struct TileChunk {   // experts c + 4 lane .. + 3: their rows and tile counts (0 past E)
