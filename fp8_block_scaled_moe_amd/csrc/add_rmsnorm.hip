@@ -20,7 +20,7 @@
 // and one trip to memory and back.
 #include "device_common.h"
 #include "fp8moe.h"
-#include "launch.h"
+#include "launch_ops.h"
 
 namespace fp8moe {
 

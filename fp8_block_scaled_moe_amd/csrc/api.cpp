@@ -14,7 +14,7 @@
 #include <type_traits>
 
 #include "fp8moe.h"
-#include "launch.h"
+#include "launch_ops.h"
 #include "tile_select.h"
 
 using namespace fp8moe;

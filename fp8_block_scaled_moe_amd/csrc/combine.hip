@@ -5,7 +5,7 @@
 // written by exactly one thread, no atomics, bit-for-bit deterministic.
 // HBM-bound: each thread moves 16-byte vectors (8 bf16) of the K source rows.
 #include "combine_body.h"
-#include "launch.h"
+#include "launch_ops.h"
 
 namespace fp8moe {
 

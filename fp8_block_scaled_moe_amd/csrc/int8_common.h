@@ -3,6 +3,7 @@
 #pragma once
 
 #include "device_common.h"
+#include "launch_ops.h"
 
 namespace fp8moe {
 

@@ -25,14 +25,12 @@ size_t route_lds_bytes(int E);
 // zero2 (nullable): kSmallBarrierWords words the one-workgroup path
 // (R <= 4096) sets to zero in the same launch (the small-T layer's barrier
 // counters and error flag); hipErrorInvalidValue if given with more rows.
-// inverse false: the caller does not read src_to_sorted, which then holds
-// anything where there are many rows (its launch is left out).
 constexpr int kRouteOneBlockRows = 4096;
 constexpr int kSmallBarrierWords = 16;   // 8 group counters, the top counter, the error flag, spare
 hipError_t launch_route_permute(const int32_t* ids, int R, int E, int align, int cap,
                                 int32_t* counts, int32_t* m_indptr, int32_t* padded_indptr,
                                 int32_t* sorted_src, int32_t* src_to_sorted, hipStream_t stream,
-                                uint32_t* zero2 = nullptr, bool inverse = true);
+                                uint32_t* zero2 = nullptr);
 
 // Largest tile heights.  GEMM2's body fits 256 VGPRs up to 160 rows.  GEMM1's
 // body (with its SwiGLU/requant epilogue) reaches the VGPR limit at 144 rows
@@ -88,47 +86,6 @@ hipError_t launch_gemm1_bf16(const uint16_t* x, const uint16_t* w13, const Group
 hipError_t launch_gemm2_bf16(const uint16_t* q, const uint16_t* w2, const float* topk_weights, const GroupedRows& g,
                              int H, int I, uint16_t* Y, int tile_m, int tile_n, bool packed, hipStream_t stream);
 
-// Int8 variants: one scale per token row and per weight row.  GEMM1 writes the
-// SwiGLU output as bf16 (act [cap][I]), launch_quant_rows_int8 quantises its
-// rows (those with sorted_src >= 0; every row if NULL), GEMM2 takes the codes
-// and row scales.  tile_m in {16, 32, 64} (streaming kernels) or kTileMaxInt8
-// (tile kernels).
-constexpr int kTileMaxInt8 = 288;
-hipError_t launch_gemm1_int8(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
-                             const GroupedRows& g, int H, int I, uint16_t* act, int tile_m, bool packed,
-                             hipStream_t stream);
-hipError_t launch_quant_rows_int8(const uint16_t* in, const int32_t* sorted_src, int64_t rows, int N, uint8_t* q,
-                                  float* scale, hipStream_t stream);
-// YT: uint16_t (bf16 rows) or float
-template <typename YT>
-hipError_t launch_gemm2_int8(const uint8_t* q, const float* q_scale, const uint8_t* w2, const float* w2_scale,
-                             const float* topk_weights, const GroupedRows& g, int H, int I, YT* Y, int tile_m,
-                             bool packed, hipStream_t stream);
-
-// The whole layer without routing for at most kDirectMaxRows routed rows of at
-// most kDirectMaxSlots slots; act [T*K][I].
-constexpr int kDirectMaxRows = 16, kDirectMaxSlots = 8;
-hipError_t launch_moe_direct_int8(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
-                                  const uint8_t* w2, const float* w2_scale, const int32_t* topk_ids,
-                                  const float* topk_weights, int T, int H, int I, int E, int K, uint16_t* act,
-                                  uint16_t* out, bool packed, hipStream_t stream);
-// The tile kernels; GEMM1's takes x of less than 4 GiB (hipErrorInvalidValue).
-hipError_t launch_gemm1_int8_tile(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
-                                  const GroupedRows& g, int H, int I, uint16_t* act, bool packed, hipStream_t stream);
-template <typename YT>
-hipError_t launch_gemm2_int8_tile(const uint8_t* q, const float* q_scale, const uint8_t* w2, const float* w2_scale,
-                                  const float* topk_weights, const GroupedRows& g, int H, int I, YT* Y,
-                                  bool packed, hipStream_t stream);
-
-// Residual addition + RMS norm + quantisation (format: FP8MOE_NORM_*), and the
-// router's choice of experts (score: FP8MOE_SCORE_*).
-hipError_t launch_add_rmsnorm(const uint16_t* x, const void* residual, bool residual_f32, const void* weight,
-                              bool weight_f32, float eps, int64_t T, int H, int format, void* residual_out,
-                              uint16_t* norm_out, uint8_t* q, void* scale, hipStream_t stream);
-hipError_t launch_router_topk(const void* logits, bool bf16, const float* bias, int T, int E, int K, int score,
-                              int n_group, int topk_group, int group_top, bool renormalize, float scale,
-                              int32_t* ids, float* weights, hipStream_t stream);
-
 // Device address, on the current device, of the allocation-free layer's
 // scratch array (FP8MOE_NOALLOC_SCRATCH_BYTES; noalloc.hip).
 hipError_t noalloc_scratch(void** ptr);
@@ -150,9 +107,6 @@ hipError_t launch_pack_mx_scales(const uint8_t* in, int64_t E, int N, int K, int
 
 hipError_t launch_combine(const uint16_t* Y, const int32_t* topk_ids, int T, int H, int E, int K,
                           uint16_t* out, hipStream_t stream);
-// The same over fp32 rows.
-hipError_t launch_combine_f32(const float* Y, const int32_t* topk_ids, int T, int H, int E, int K, uint16_t* out,
-                              hipStream_t stream);
 
 // The FP8 layer for small T in one cooperative persistent launch (after the
 // routing launch, which zeroes ctr_err[0..1]): GEMM1 + SwiGLU + requant over

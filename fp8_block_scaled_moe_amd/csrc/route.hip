@@ -17,7 +17,7 @@
 //      offset carries the order across chunks.  Every position is therefore a
 //      pure function of the input: the map is bit-for-bit deterministic.
 #include "device_common.h"
-#include "launch.h"
+#include "launch_ops.h"
 
 namespace fp8moe {
 
@@ -289,6 +289,14 @@ hipError_t launch_route_permute(const int32_t* ids, int R, int E, int align, int
   hipLaunchKernelGGL(route_inverse_kernel, dim3(inv_blocks), dim3(256), 0, stream, ids, R, E, padded_indptr,
                      sorted_src, src_to_sorted);
   return hipGetLastError();
+}
+
+hipError_t launch_route_permute(const int32_t* ids, int R, int E, int align, int cap,
+                                int32_t* counts, int32_t* m_indptr, int32_t* padded_indptr,
+                                int32_t* sorted_src, int32_t* src_to_sorted, hipStream_t stream,
+                                uint32_t* zero2) {
+  return launch_route_permute(ids, R, E, align, cap, counts, m_indptr, padded_indptr, sorted_src, src_to_sorted,
+                              stream, zero2, true);
 }
 
 }  // namespace fp8moe

@@ -44,7 +44,7 @@
 // by the launch and one trip to memory.
 #include "device_common.h"
 #include "fp8moe.h"
-#include "launch.h"
+#include "launch_ops.h"
 
 namespace fp8moe {
 
