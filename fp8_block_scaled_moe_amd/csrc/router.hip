@@ -16,7 +16,8 @@
 // weight 0, which the layer treats as dropped.
 //
 // Which expert is chosen hangs on the order of close scores, and is decided as
-// if in 64 bits.  Two paths give the same answer:
+// if in 64 bits.  Two paths give the same choices, and weights to fp32's
+// rounding:
 //
 // Exact path (route_exact): one wave64 per token, every score and choice in
 // fp64.  As the only path it measured 31 us for 8192 tokens of 256 experts in
@@ -35,7 +36,7 @@
 //   * groups of which a kept and a left one are closer than the error of both
 //     are ranked by fp64 totals of their best choices;
 //   * what is left for the exact path: more close candidates than lanes, and
-//     close groups whose scores are next to fp32's smallest.
+//     chosen experts or close groups whose scores are next to fp32's smallest.
 // In a graph, us for 8192 tokens of 256 experts, top-8: softmax 6.6 (bf16 logits
 // 5.3), sigmoid with bias 8.2, softmax with bias 12.1, groups by their maximum
 // 7.3, by the sum of two 9.8 (14 while close ones went the exact way); 65537
@@ -580,6 +581,10 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
   }
 
   float w = rl < K && e >= 0 ? (softmax ? (v == m ? 1.f : expf(v - m)) * zinv : 1.0f / (1.0f + expf(-v))) : 0.f;
+  // next to fp32's smallest a score has lost bits, or all of them, which the sum
+  // or the scale may bring back (logistic function below about -69; a softmax
+  // whose choices lie as far below the row's largest logit)
+  if (rl < K && e >= 0 && w < 0x1p-100f) unsure = true;
   if (a.renormalize) {
     const float sum = row_reduce_f32<L, false>(w);
     w = sum > 0.f ? w / sum : 0.f;

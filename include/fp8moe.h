@@ -420,7 +420,9 @@ int add_rmsnorm_quant(const void* x, const void* residual, int32_t residual_f32,
  *   topk_weights score_e (without the bias), divided by the chosen ones' sum if
  *                renormalize != 0 (0 where that sum is 0), times scale
  * Which experts are chosen is decided as if in 64 bits; weights are computed in
- * fp32.
+ * fp32, or in 64 bits and rounded once where a chosen score is below 2^-100, so
+ * that scores that fp32 cannot hold keep their shares of the sum.  A weight's
+ * last bits may differ with T.
  *
  *   logits  fp32 or bf16 (logits_bf16 != 0) [T, E]
  *   bias    fp32 [E] or NULL

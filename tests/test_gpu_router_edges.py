@@ -1,0 +1,74 @@
+"""moe_router_topk where fp32 underflows, where choices lie closer than its error, and with infinite biases, against
+the float64 oracle.
+
+Chosen experts must be equal.  A weight is a score, over the sum of up to 64 of them if asked, times scale.  Roundings
+of 2^-24 relative on its way: the exponential's argument, rounded to fp32 (a softmax's is a difference of up to twice
+the row's reach |x|): 2 reach; the exponential itself 2; a softmax's sum of up to 16 terms a lane and 6 levels of
+lanes, or 32 and 4, of terms with 4 each: 40; quotients, products, the sum of the chosen: 20.  Weights that fp32 holds
+as subnormals are rounded to its smallest step, 2^-149.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_block_scaled_moe_amd as fm
+from oracle.router import router_reference
+from tests.gpu_helpers import say
+
+pytestmark = pytest.mark.gpu
+
+SCORES = {"softmax": fm.SCORE_SOFTMAX, "sigmoid": fm.SCORE_SIGMOID}
+INF, NAN = float("inf"), float("nan")
+
+
+def check(logits, K, score, bias=None, rows=slice(None), **kw):
+    ids, w = fm.moe_router_topk(logits.cuda(), K, SCORES[score], bias=None if bias is None else bias.cuda(), **kw)
+    torch.cuda.synchronize()
+    ids, w = ids.cpu().numpy()[rows], w.cpu().double().numpy()[rows]
+    x = logits.double().numpy()[rows]
+    rid, rw = router_reference(x, K, score, None if bias is None else bias.double().numpy(), **kw)
+    assert np.array_equal(ids, rid), f"rows {np.flatnonzero((ids != rid).any(1))[:8]}"
+    reach = np.abs(np.where(np.isfinite(x), x, 0.0)).max(1) * (2 if score == "softmax" else 1)
+    assert np.all(np.abs(w - rw) <= np.abs(rw) * ((2 * reach + 64) * 2.0 ** -24)[:, None] + 2.0 ** -149)
+    return ids, w
+
+
+@pytest.mark.parametrize("E,K", [(8, 4), (128, 8), (512, 8), (1024, 20)])
+@pytest.mark.parametrize("at", [-60.0, -70.0, -86.0, -87.5, -89.0, -100.0, -600.0])
+def test_sigmoid_scores_that_underflow_in_fp32(E, K, at):
+    say("router far sigmoid", E, K, at)
+    g = torch.Generator().manual_seed(E)
+    logits = at + torch.randn(9, E, generator=g)
+    bias = 0.1 * torch.randn(E, generator=g)
+    for renormalize in (True, False):
+        for b in (None, bias):
+            _, w = check(logits, K, "sigmoid", b, renormalize=renormalize)
+            if renormalize:
+                assert np.allclose(w.sum(1), 1.0, rtol=1e-4)
+    check(logits, K, "sigmoid", bias, renormalize=False, scale=2.0 ** 100)
+    check(logits, K, "sigmoid", n_group=4, topk_group=2, group_top=2)
+    check(logits.bfloat16(), K, "sigmoid", n_group=4, topk_group=2)
+
+
+@pytest.mark.parametrize("E,K", [(8, 4), (128, 8), (512, 8), (1024, 20)])
+@pytest.mark.parametrize("below", [60.0, 80.0, 100.0, 110.0, 500.0])
+def test_softmax_scores_that_underflow_in_fp32(E, K, below):
+    """The row's largest logit belongs to an expert that its bias, or its group's, rules out."""
+    say("router far softmax", E, K, below)
+    g = torch.Generator().manual_seed(E + 1)
+    logits = torch.randn(9, E, generator=g)
+    logits[:, 2] += below
+    bias = torch.zeros(E)
+    bias[2] = -INF
+    _, w = check(logits, K, "softmax", bias)
+    assert np.allclose(w.sum(1), 1.0, rtol=1e-4)
+    check(logits, K, "softmax", bias, renormalize=False, scale=2.0 ** 100)
+    per = E // 4
+    bias = torch.zeros(E)
+    bias[:per] = -1.0
+    bias[2] = -3.0
+    check(logits, min(K, per), "softmax", bias, n_group=4, topk_group=1)
+    # chosen beside the largest: a weight of its own, however small
+    check(logits, K, "softmax", renormalize=False, scale=2.0 ** 100)
+    check(logits, K, "softmax", scale=2.0 ** 100)
