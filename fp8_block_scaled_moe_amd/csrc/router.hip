@@ -487,7 +487,8 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
           s64 = fmax(fmax(s64, s2), fmin(f64, f2));
           f64 = fmax(f64, f2);
         }
-        const double total64 = border ? (a.group_top > 1 ? f64 + s64 : f64) : (double)total;
+        const double sum64 = a.group_top == 1 ? f64 : s64 > kNone64 ? f64 + s64 : kNone64;   // no inf - inf
+        const double total64 = border ? sum64 : (double)total;
         int rank64 = 0;
         for (int h = 0; h < a.n_group; ++h) {
           const double other = shfl_any(total64, (lane & ~(L - 1)) + h * gl);

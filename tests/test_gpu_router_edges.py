@@ -72,3 +72,31 @@ def test_softmax_scores_that_underflow_in_fp32(E, K, below):
     # chosen beside the largest: a weight of its own, however small
     check(logits, K, "softmax", renormalize=False, scale=2.0 ** 100)
     check(logits, K, "softmax", scale=2.0 ** 100)
+
+
+@pytest.mark.parametrize("score", list(SCORES))
+@pytest.mark.parametrize("E,n_group", [(16, 4), (256, 8), (60, 4)])
+def test_infinite_biases_in_groups(score, E, n_group):
+    """A group whose only expert left has the bias +inf counts as -inf where two choices are asked of it."""
+    say("router infinite biases", score, E, n_group)
+    per = E // n_group
+    g = torch.Generator().manual_seed(E)
+    logits = torch.randn(20, E, generator=g)
+    bias = 0.1 * torch.randn(E, generator=g)
+    last = (n_group - 1) * per
+    bias[last + 1] = INF
+    logits[:, last:] = -INF
+    logits[:, last + 1] = torch.randn(20, generator=g)
+    K = min(8, per)
+    ids, _ = check(logits, K, score, bias, n_group=n_group, topk_group=2, group_top=2)
+    assert not (ids >= last).any()
+    for top in (1, 2):      # two infinite choices, and one of each sign
+        logits[:, last] = 0.5
+        check(logits, K, score, bias, n_group=n_group, topk_group=2, group_top=top)
+        bias[last] = INF
+        check(logits, K, score, bias, n_group=n_group, topk_group=2, group_top=top)
+        bias[0] = -INF
+        check(logits, K, score, bias, n_group=n_group, topk_group=1, group_top=top)
+        bias[0] = 3.4e38
+        bias[1] = 3.4e38    # a sum beyond fp32
+        check(logits, K, score, bias, n_group=n_group, topk_group=2, group_top=top)
