@@ -443,13 +443,14 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
       const float best = row_reduce_f32<L, true>(keep || !real ? kNone : total);
       // two choices each (the tolerance has a margin of two), which may be far
       // larger than their sum; scores without a bias carry their argument's
-      // rounding relative to themselves
+      // roundings relative to themselves: two of |x| 2^-24 and log2 e's own, and a
+      // softmax's |x - m| is up to 2 far
       float far = 0.f, tol;
       if (sums) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
           if (fabsf(x[i]) < kRouterInf) far = fmaxf(far, fabsf(x[i]));
-        tol = (2.f * row_reduce_f32<L, true>(far) + 32.f) * 0x1p-23f * fabsf(worst);
+        tol = ((softmax ? 5.f : 2.f) * row_reduce_f32<L, true>(far) + 32.f) * 0x1p-23f * fabsf(worst);
       } else {
         if (first > kNone) far = fabsf(first);
         if (a.group_top > 1 && second > kNone) far += fabsf(second);

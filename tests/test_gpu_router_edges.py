@@ -100,3 +100,22 @@ def test_infinite_biases_in_groups(score, E, n_group):
         bias[0] = 3.4e38
         bias[1] = 3.4e38    # a sum beyond fp32
         check(logits, K, score, bias, n_group=n_group, topk_group=2, group_top=top)
+
+
+# m, a, b, c: s(a) + s(b) exceeds 2 s(c) by less than 2^-23 of it, where s(v) = exp(v - m); the fp32 roundings of
+# the differences from m and of the exponentials' arguments add up to 100 of those steps the other way
+FAR = [(32.300010681152344, -32.12515640258789, -32.02237319946289, -32.072444915771484),
+       (32.099998474121094, -32.00337600708008, -32.10615921020508, -32.05344772338867),
+       (32.400001525878906, -32.25282669067383, -32.35560989379883, -32.30289840698242),
+       (32.400001525878906, -32.345890045166016, -32.448673248291016, -32.39596176147461)]
+
+
+@pytest.mark.parametrize("m,a,b,c", FAR)
+def test_close_groups_far_below_the_largest_logit(m, a, b, c):
+    """Groups by sums of scores so small that their roundings exceed a fixed multiple of fp32's step."""
+    say("router far groups", m, a, b, c)
+    rows = torch.tensor([[m, m, a, b, c, c, -INF, -INF], [m, m, c, c, a, b, -INF, -INF]])
+    s = lambda v: np.exp(np.float64(v) - m)
+    assert 0 < (s(a) + s(b)) / (2 * s(c)) - 1 < 2.0 ** -23
+    ids, _ = check(rows, 4, "softmax", n_group=4, topk_group=2, group_top=2)
+    assert sorted(ids[0].tolist()) == [0, 1, 2, 3] and sorted(ids[1].tolist()) == [0, 1, 4, 5]
