@@ -408,12 +408,12 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
     for (int i = 0; i < NV; ++i) c[i] = x[i];
   }
   // Error of a choice c of score s, with margin: the logistic function is
-  // within 2^-22, a softmax's score within 2^-19 of itself (the exponential's
-  // argument, and a sum of up to twice 16 terms a lane and 4 levels of lanes, or
-  // twice 8 and 6), and the bias
-  // adds half a step of c.
-  auto choice_tol = [&](float s, float c) __attribute__((always_inline)) -> float {
-    return (softmax ? s * 0x1p-18f : 0x1p-21f) + fabsf(c) * 0x1p-22f;
+  // within 2^-22, a softmax's score, of a logit d below the row's largest, within
+  // 2^-19 + 2.25 d 2^-24 of itself (a sum of up to twice 16 terms a lane and 4
+  // levels of lanes, or twice 8 and 6, and the exponential's argument), and the
+  // bias adds half a step of c.  s = 1 and d = 0 bound every score.
+  auto choice_tol = [&](float s, float c, float d) __attribute__((always_inline)) -> float {
+    return (softmax ? s * (0x1p-18f + d * 0x1p-22f) : 0x1p-21f) + fabsf(c) * 0x1p-22f;
   };
 
   if (a.n_group > 1) {
@@ -454,7 +454,7 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
       } else {
         if (first > kNone) far = fabsf(first);
         if (a.group_top > 1 && second > kNone) far += fabsf(second);
-        tol = 2.f * choice_tol(1.f, row_reduce_f32<L, true>(far));
+        tol = 2.f * choice_tol(1.f, row_reduce_f32<L, true>(far), 0.f);
       }
       const bool close = a.topk_group < a.n_group && best > kNone && !(worst - best > tol);
       // (sums of scores next to fp32's smallest have no relative bound)
@@ -527,7 +527,7 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
     // are then among them.
     const uint32_t kth = last;
     const float kmin = key_value(kth & ~kIdx);
-    const float margin = biased ? 2.f * choice_tol(1.f, kmin) : 0.f;
+    const float margin = biased ? 2.f * choice_tol(1.f, kmin, 0.f) : 0.f;
     bool open = kth != 0;
     while (taken < L - 1 && __ballot(open)) {
       take(taken++);
@@ -570,7 +570,7 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
       sort(v);
     } else {
       const float ch = sort(e >= 0 ? score_of(v) + a.bias[e] : kNone);
-      const float tol = e >= 0 ? choice_tol(score_of(v), ch) : 0.f;
+      const float tol = e >= 0 ? choice_tol(score_of(v), ch, m - v) : 0.f;
       const float ch2 = __shfl(ch, lane + 1), tol2 = __shfl(tol, lane + 1);
       const int e2 = __shfl(e, lane + 1);
       const bool close = rl < K && rl + 1 < taken && e2 >= 0 && !(ch - ch2 > tol + tol2);

@@ -119,3 +119,34 @@ def test_close_groups_far_below_the_largest_logit(m, a, b, c):
     assert 0 < (s(a) + s(b)) / (2 * s(c)) - 1 < 2.0 ** -23
     ids, _ = check(rows, 4, "softmax", n_group=4, topk_group=2, group_top=2)
     assert sorted(ids[0].tolist()) == [0, 1, 2, 3] and sorted(ids[1].tolist()) == [0, 1, 4, 5]
+
+
+@pytest.mark.parametrize("m", [32.4, 33.0])
+def test_biases_of_the_size_of_far_scores(m):
+    """Softmax scores of 2^-93 and biases of that size: the larger score's rounding up and the smaller's down must not
+    decide."""
+    f = np.float32
+    m = f(m)
+    v = np.unique(-(f(31.7) + np.random.default_rng(3).random(200000).astype(f)))
+    a = ((v - m) * f(1.4426950408889634)).astype(np.float64)      # the exponential's argument in fp32
+    true = np.exp(v.astype(np.float64) - np.float64(m))
+    err = np.exp2(a) / true - 1
+    v1, v2 = np.argmax(err), np.argmin(err)
+    assert err[v1] - err[v2] > 90 * 2.0 ** -23
+    b2 = f((true[v1] - true[v2]) + 3 * 2.0 ** -23 * true[v1])      # expert 2 leads by three steps
+    assert 0 < true[v2] + np.float64(b2) - true[v1] < 5 * 2.0 ** -23 * true[v1]
+    logits = torch.tensor([[m, v[v1], v[v2]] + [-200.0] * 5])
+    bias = torch.zeros(8)
+    bias[2] = float(b2)
+    say("router far biases", m, v[v1], v[v2], b2)
+    ids, _ = check(logits, 3, "softmax", bias)
+    assert ids[0].tolist() == [0, 2, 1]
+
+
+def test_biases_of_the_size_of_subnormal_scores():
+    """A score below fp32's smallest normal value against a bias just below it."""
+    logits = torch.tensor([[0.0, -88.0, -100.0] + [-200.0] * 5])
+    bias = torch.zeros(8)
+    bias[2] = 5e-39
+    ids, _ = check(logits, 3, "softmax", bias)
+    assert ids[0].tolist() == [0, 1, 2]
