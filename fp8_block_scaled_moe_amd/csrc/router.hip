@@ -573,7 +573,9 @@ __device__ __forceinline__ bool route_fast(const RouterArgs& a, int64_t t, int l
       const float tol = e >= 0 ? choice_tol(score_of(v), ch, m - v) : 0.f;
       const float ch2 = __shfl(ch, lane + 1), tol2 = __shfl(tol, lane + 1);
       const int e2 = __shfl(e, lane + 1);
-      const bool close = rl < K && rl + 1 < taken && e2 >= 0 && !(ch - ch2 > tol + tol2);
+      // (a softmax's errors grow with the score: a choice behind slot K - 1 may be
+      // less sure than its neighbours)
+      const bool close = (softmax || rl < K) && rl + 1 < taken && e2 >= 0 && !(ch - ch2 > tol + tol2);
       if (__ballot(close)) {
         // neighbours too close for fp32: in the order of their fp64 choices
         need_z64();

@@ -150,3 +150,23 @@ def test_biases_of_the_size_of_subnormal_scores():
     bias[2] = 5e-39
     ids, _ = check(logits, 3, "softmax", bias)
     assert ids[0].tolist() == [0, 1, 2]
+
+
+def test_a_later_choice_of_a_larger_error():
+    """Softmax, one slot: two choices of tiny scores, further apart than their errors, stand ahead of one whose score is
+    near 1 and whose fp32 value is too low by more than what parts it from them."""
+    f = np.float32
+    low = -np.random.default_rng(5).uniform(3.5, 4.5, 20000).astype(f)
+    z = 1 + np.exp(low.astype(np.float64))
+    z32 = z.astype(f)
+    s32 = (f(1) / z32).astype(np.float64)
+    delta = np.where(np.abs(z - z32) < 0.45 * 2.0 ** -23, 1 / z - s32, 0)      # z away from a tie of its rounding
+    i = np.argmax(delta)
+    assert delta[i] > 2.0 ** -24
+    b0 = f(0.01 - s32[i])
+    c0 = s32[i] + np.float64(b0)      # expert 0's choice in fp32, where the difference is exact; delta more in truth
+    logits = torch.tensor([[0.0, low[i], -40.0, -40.0] + [-60.0] * 4])
+    bias = torch.tensor([b0, -1.0, c0 + 0.6 * delta[i], c0 + 0.3 * delta[i], 0, 0, 0, 0], dtype=torch.float32)
+    say("router later choice", low[i], bias.tolist())
+    ids, _ = check(logits, 1, "softmax", bias)
+    assert ids[0].tolist() == [0]
