@@ -170,3 +170,31 @@ def test_a_later_choice_of_a_larger_error():
     say("router later choice", low[i], bias.tolist())
     ids, _ = check(logits, 1, "softmax", bias)
     assert ids[0].tolist() == [0]
+
+
+# T > 16 E or E <= 128, K <= 14 and at most 16 groups: 16 lanes a token, of 4, 8, 16 and 32 values
+@pytest.mark.parametrize("T,E,K,groups", [
+    (4200, 256, 8, (1, 1, 1)), (4117, 256, 14, (8, 4, 2)), (3500, 200, 5, (1, 1, 1)), (2500, 150, 3, (10, 4, 1)),
+    (8200, 512, 8, (1, 1, 1)), (8200, 512, 8, (8, 4, 2)), (6200, 384, 8, (1, 1, 1)), (6203, 384, 14, (16, 5, 1)),
+    (5000, 301, 6, (1, 1, 1)), (4400, 259, 11, (7, 3, 2)), (900, 64, 8, (1, 1, 1)), (901, 128, 8, (16, 6, 2))])
+def test_many_tokens_in_16_lanes(T, E, K, groups):
+    say("router 16 lanes", T, E, K, groups)
+    kw = dict(zip(("n_group", "topk_group", "group_top"), groups))
+    g = torch.Generator().manual_seed(T)
+    logits, bias = 2 * torch.randn(T, E, generator=g), 0.1 * torch.randn(E, generator=g)
+    logits[7, ::2] = -INF      # masked rows among them, and equal choices
+    logits[8, 5:] = NAN
+    logits[9] = 0
+    logits[10, 3] = INF
+    logits[11] = torch.finfo(torch.float32).min
+    logits[12] = 1 + 2.0 ** -23 * torch.randperm(E, generator=g)
+    logits[13] = -100
+    half = logits.clamp(-1e30, 1e30).bfloat16()
+    # the oracle goes token by token: the first and last rows and a thousand between them
+    kw["rows"] = np.unique(np.r_[:40, T - 40:T, np.random.default_rng(T).integers(0, T, 1000)])
+    check(logits, K, "softmax", **kw)
+    check(logits, K, "sigmoid", bias, **kw)
+    check(logits, K, "softmax", bias, renormalize=False, **kw)
+    check(half, K, "softmax", renormalize=False, **kw)
+    check(half, K, "sigmoid", bias, scale=2.5, **kw)
+    check(half, K, "sigmoid", **kw)
