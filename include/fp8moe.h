@@ -395,7 +395,8 @@ int moe_gemm2_weighted_bf16(const void* q, const void* w2,
  * FP8MOE_MAX_DIM; T < 2^24 (FP8MOE_ERR_LIMIT).  T == 0 launches nothing.
  * A row whose v holds an infinity or NaN gives NaN: norm_out, e4m3 codes 0x7F,
  * scale NaN (E8M0 code 255), int8 codes 0.  So does a block (INT8: a row) whose
- * n does, its norm_out apart.  Squares beyond fp32's range do no harm.
+ * n does, its norm_out apart.  Squares beyond fp32's range do no harm.  The order
+ * of a row's sum, and so the last bits of n, may differ with T.
  */
 #define FP8MOE_NORM_BF16  0
 #define FP8MOE_NORM_FP8   1
