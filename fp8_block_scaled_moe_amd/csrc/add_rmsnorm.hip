@@ -156,7 +156,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(
   }
   ss = row_reduce<TPR, RowSum>(ss, red[0]);
   bool bad = false;
-  if (!(ss <= 3.4028234e38f)) {   // the same in every thread of the row
+  float rinv;
+  if (ss <= 3.4028234e38f) {   // the same in every thread of the row
+    rinv = 1.0f / sqrtf(ss / (float)H + eps);
+  } else {
     // squares beyond fp32: once more on values scaled by 2^-80 (eps vanishes
     // beside them); still no number: the row holds an infinity or NaN
     ss = 0.f;
@@ -164,14 +167,20 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(
     for (int j = 0; j < V; ++j)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        v[j][k] *= 0x1p-80f;
-        ss = fmaf(v[j][k], v[j][k], ss);
+        const float u = v[j][k] * 0x1p-80f;
+        ss = fmaf(u, u, ss);
       }
     ss = row_reduce<TPR, RowSum>(ss, red[1]);
     bad = !(ss <= 3.4028234e38f);
-    eps = 0.f;
+    const float r = bad ? __uint_as_float(0x7fc00000u) : 1.0f / sqrtf(ss / (float)H);
+    // the scale goes on the quotients, which it leaves exact: on small values it
+    // would cost bits
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[j][k] = v[j][k] * r * 0x1p-80f;
+    rinv = bad ? r : 1.0f;
   }
-  const float rinv = bad ? __uint_as_float(0x7fc00000u) : 1.0f / sqrtf(ss / (float)H + eps);
 
   float rowmax = 0.f;
 #pragma unroll

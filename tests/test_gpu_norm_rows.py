@@ -52,7 +52,7 @@ def check(x, r, w, eps, fmt, out):
     ok = np.isfinite(vr).all(1)
     n, bad = n[ok], torch.from_numpy(~ok)
     assert torch.isnan(norm[bad]).all()
-    assert np.all(np.abs(f64(norm)[ok] - n) <= np.abs(n) * (2.0 ** -8 + 2 * DELTA) + 1e-38)
+    assert np.all(np.abs(f64(norm)[ok] - n) <= np.abs(n) * (2.0 ** -8 + 2 * DELTA) + 2.0 ** -133)
     if fmt == "bf16":
         assert q is None and scale is None
         return
@@ -137,3 +137,18 @@ def test_ties_of_int8_codes_go_to_even():
     v[0, :9] = torch.tensor([127.0, 0.5, 1.5, 2.5, -0.5, -1.5, -2.5, 63.5, -62.5])
     q, s = fm.quant_rows_int8(v.cuda())
     assert s.item() == 1.0 and q[0, :9].tolist() == [127, 0, 2, 2, 0, -2, -2, 64, -62]
+
+
+@pytest.mark.parametrize("T", [1, 600])
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+def test_small_values_beside_squares_that_overflow(T, fmt):
+    """One value of 2^66 in a row of 16384, whose root mean square is 2^59: values of 2^-66 still have their bits."""
+    H = 16384
+    say("norm wide range", T, fmt)
+    g = torch.Generator().manual_seed(T)
+    x = torch.zeros(T, H).bfloat16()
+    x[:, 100] = 2.0 ** 66
+    r = (1 + torch.rand(T, H, generator=g)) * 2.0 ** -66
+    r[:, 100] = 0
+    w = 1 + 0.3 * torch.rand(H, generator=g)
+    check(x, r, w, 1e-6, fmt, run(x, r, w, 1e-6, fmt))
