@@ -160,8 +160,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(
   if (ss <= 3.4028234e38f) {   // the same in every thread of the row
     rinv = 1.0f / sqrtf(ss / (float)H + eps);
   } else {
-    // squares beyond fp32: once more on values scaled by 2^-80 (eps vanishes
-    // beside them); still no number: the row holds an infinity or NaN
+    // squares beyond fp32: once more on values scaled by 2^-80, and eps by its
+    // square; still no number: the row holds an infinity or NaN
     ss = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j)
@@ -172,7 +172,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_rmsnorm_kernel(
       }
     ss = row_reduce<TPR, RowSum>(ss, red[1]);
     bad = !(ss <= 3.4028234e38f);
-    const float r = bad ? __uint_as_float(0x7fc00000u) : 1.0f / sqrtf(ss / (float)H);
+    const float r = bad ? __uint_as_float(0x7fc00000u) : 1.0f / sqrtf(ss / (float)H + eps * 0x1p-80f * 0x1p-80f);
     // the scale goes on the quotients, which it leaves exact: on small values it
     // would cost bits
 #pragma unroll

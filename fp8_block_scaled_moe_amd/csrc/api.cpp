@@ -910,7 +910,8 @@ int add_rmsnorm_quant(const void* x, const void* residual, int32_t residual_f32,
   if (H % step) return fail(FP8MOE_ERR_ALIGN, "H=%d must be a multiple of %d in this format", H, step);
   if (H > FP8MOE_MAX_DIM || T >= ((int64_t)1 << 24))
     return fail(FP8MOE_ERR_LIMIT, "H=%d must be at most %d and T=%lld below 2^24", H, FP8MOE_MAX_DIM, (long long)T);
-  if (!(eps > 0.f) || !isfinite(eps)) return fail(FP8MOE_ERR_ARG, "eps must be finite and positive");
+  // fp32 holds squares beside a subnormal eps badly, and the sum of a mean square and a larger eps may overflow
+  if (!(eps >= 0x1p-126f && eps <= 0x1p126f)) return fail(FP8MOE_ERR_ARG, "eps must lie in [2^-126, 2^126]");
   if (!residual != !residual_out) return fail(FP8MOE_ERR_NULL, "residual and residual_out go together");
   if (T == 0) return ok();
   const bool codes = format != FP8MOE_NORM_BF16;

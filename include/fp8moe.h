@@ -384,7 +384,7 @@ int moe_gemm2_weighted_bf16(const void* q, const void* w2,
  *   residual     bf16 or fp32 (residual_f32 != 0) [T, H], or NULL: then
  *                residual_out is NULL too
  *   weight       bf16 or fp32 (weight_f32 != 0) [H]
- *   eps          finite and > 0
+ *   eps          in [2^-126, 2^126]   (FP8MOE_ERR_ARG)
  *   residual_out [T, H] of the residual's type; may be `residual` itself
  *   norm_out     bf16 [T, H] or NULL
  *   q            fp8 / int8 [T, H]

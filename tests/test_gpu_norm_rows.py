@@ -152,3 +152,27 @@ def test_small_values_beside_squares_that_overflow(T, fmt):
     r[:, 100] = 0
     w = 1 + 0.3 * torch.rand(H, generator=g)
     check(x, r, w, 1e-6, fmt, run(x, r, w, 1e-6, fmt))
+
+
+@pytest.mark.parametrize("H", [256, 16384])
+def test_eps_beside_squares_that_overflow(H):
+    """A mean square of about 2^128 / H, and an eps as large."""
+    g = torch.Generator().manual_seed(H)
+    x = torch.zeros(5, H).bfloat16()
+    x[:, 7] = 1.5 * 2.0 ** 64
+    r = torch.randn(5, H, generator=g) * 2.0 ** 50
+    w = 1 + 0.3 * torch.randn(H, generator=g)
+    for eps in (2.0 ** 128 / H, 2.0 ** 126, 1.0):
+        for fmt in FORMATS:
+            check(x, r, w, eps, fmt, run(x, r, w, eps, fmt))
+
+
+def test_smallest_eps():
+    """Squares that fp32 holds as subnormals, or not at all, beside the smallest eps."""
+    x = (torch.randn(6, 512, generator=torch.Generator().manual_seed(1)) * 2.0 ** -64).bfloat16()
+    x[3] = (x[3].float() * 2.0 ** -8).bfloat16()
+    w = torch.ones(512)
+    for fmt in FORMATS:
+        check(x, None, w, 2.0 ** -126, fmt, run(x, None, w, 2.0 ** -126, fmt))
+    with pytest.raises(fm.Fp8MoeError, match="eps"):
+        run(x, None, w, 2.0 ** -127, "fp8")
