@@ -330,6 +330,22 @@ __global__ __launch_bounds__(64 * kDirectMaxSlots) void gemm2_direct_int8_kernel
   }
 }
 
+// Tiles of at most tm rows times N tiles, in whole rounds of the XCDs (as the
+// other formats' launches count them); those past the actual ones exit at once.
+static dim3 stream_grid(const GroupedRows& g, int tm, int NT) {
+  const int64_t by_rows = g.cap / 16, by_experts = g.cap / tm + g.E;
+  const int64_t items = (by_rows < by_experts ? by_rows : by_experts) * NT;
+  return wide_grid(items > 0 ? (items + kNumXcd - 1) / kNumXcd * kNumXcd : kNumXcd);
+}
+
+template <int TMAX>
+__device__ __forceinline__ bool stream_coord(const int32_t* __restrict__ padded,
+                                             const int32_t* __restrict__ sorted_src, int E, int NT, TileCoord& tc) {
+  ChunkTiles<TMAX> ch;
+  const int items = tile_items<TMAX>(padded, E, NT, ch);
+  return tile_coord_from<TMAX>(padded, sorted_src, E, NT, items, wide_block(), ch, tc);
+}
+
 // one uniform branch per workgroup on its tile height
 #define FP8MOE_STREAM_BODIES(BODY)                            \
   switch (tc.tm) {                                            \
@@ -346,7 +362,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void gemm1_stream_int8_kernel(
     int E, int K, int H, int I, uint16_t* __restrict__ act) {
   __shared__ i32x4 red[kStreamWaves * (TMAX / 16) * 2 * 64];
   TileCoord tc;
-  if (!tile_coord<TMAX>(padded, sorted_src, E, I / 16, tc)) return;
+  if (!stream_coord<TMAX>(padded, sorted_src, E, I / 16, tc)) return;
 #define FP8MOE_BODY(TS) stream_gemm1<TS, PACKED>(red, tc, x, x_scale, w13, w13_scale, sorted_src, K, H, I, act)
   FP8MOE_STREAM_BODIES(FP8MOE_BODY)
 #undef FP8MOE_BODY
@@ -359,7 +375,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void gemm2_stream_int8_kernel(
     const int32_t* __restrict__ sorted_src, int E, int H, int I, YT* __restrict__ Y) {
   __shared__ i32x4 red[kStreamWaves * (TMAX / 16) * 2 * 64];
   TileCoord tc;
-  if (!tile_coord<TMAX>(padded, sorted_src, E, H / 32, tc)) return;
+  if (!stream_coord<TMAX>(padded, sorted_src, E, H / 32, tc)) return;
 #define FP8MOE_BODY(TS) \
   stream_gemm2<TS, PACKED, YT>(red, tc, q, q_scale, w2, w2_scale, topk_weights, sorted_src, H, I, Y)
   FP8MOE_STREAM_BODIES(FP8MOE_BODY)
@@ -383,7 +399,7 @@ hipError_t launch_gemm1_int8(const uint8_t* x, const float* x_scale, const uint8
       return launch_gemm1_int8_tile(x, x_scale, w13, w13_scale, g, H, I, act, packed, stream);
     tile_m = 64;   // the tile kernel's token offsets are 32-bit
   }
-  const dim3 grid(grid_for(g, tile_m, I / 16)), block(64 * kStreamWaves);
+  const dim3 grid = stream_grid(g, tile_m, I / 16), block(64 * kStreamWaves);
 #define FP8MOE_LAUNCH(TM)                                                                                            \
   if (packed)                                                                                                        \
     hipLaunchKernelGGL((gemm1_stream_int8_kernel<TM, true>), grid, block, 0, stream, x, x_scale, w13, w13_scale,     \
@@ -401,7 +417,7 @@ hipError_t launch_gemm2_int8(const uint8_t* q, const float* q_scale, const uint8
                              bool packed, hipStream_t stream) {
   if (tile_m == kTileMaxInt8)
     return launch_gemm2_int8_tile(q, q_scale, w2, w2_scale, topk_weights, g, H, I, Y, packed, stream);
-  const dim3 grid(grid_for(g, tile_m, H / 32)), block(64 * kStreamWaves);
+  const dim3 grid = stream_grid(g, tile_m, H / 32), block(64 * kStreamWaves);
 #define FP8MOE_LAUNCH(TM)                                                                                         \
   if (packed)                                                                                                     \
     hipLaunchKernelGGL((gemm2_stream_int8_kernel<TM, true, YT>), grid, block, 0, stream, q, q_scale, w2, w2_scale, \

@@ -509,8 +509,8 @@ __global__ __launch_bounds__(kThreads) void gemm1_tile_int8_kernel(
   const TokenBuffers tb{{tb0, tb1, tb2, tb3}};
   const int NT = I / 128;
   TileCoord tc;
-  if (!tile_item(padded, sorted_src, E, tmax, lone, (NT + NB - 1) / NB, blockIdx.x % kNumXcd, blockIdx.x / kNumXcd,
-                 tc))
+  if (!tile_item(padded, sorted_src, E, tmax, lone, (NT + NB - 1) / NB, wide_block() % kNumXcd,
+                 wide_block() / kNumXcd, tc))
     return;
 #define FP8MOE_BODY(TM, WM) \
   tile_gemm1<TM, WM, PACKED>(tb, ri, tc, x, x_scale, w13, w13_scale, sorted_src, K, H, I, NB, x_bytes, act)
@@ -529,8 +529,8 @@ __global__ __launch_bounds__(kThreads) void gemm2_tile_int8_kernel(
   const TokenBuffers tb{{tb0, tb1, tb2, tb3}};
   const int NT = (H + kTN - 1) / kTN;
   TileCoord tc;
-  if (!tile_item(padded, sorted_src, E, tmax, lone, (NT + NB - 1) / NB, blockIdx.x % kNumXcd, blockIdx.x / kNumXcd,
-                 tc))
+  if (!tile_item(padded, sorted_src, E, tmax, lone, (NT + NB - 1) / NB, wide_block() % kNumXcd,
+                 wide_block() / kNumXcd, tc))
     return;
 #define FP8MOE_BODY(TM, WM) \
   tile_gemm2<TM, WM, PACKED, YT>(tb, ri, tc, q, q_scale, w2, w2_scale, topk_weights, sorted_src, H, I, NB, Y)
@@ -559,7 +559,7 @@ static int run_int8(const GroupedRows& g, int tmax, int NT, int KT) {
 // each; NB: N tiles of a run.
 struct TilePlan {
   int tmax, lone, NB;
-  unsigned grid;
+  int64_t workgroups;
 };
 
 static TilePlan tile_plan(const GroupedRows& g, int NT, int KT) {
@@ -593,7 +593,7 @@ static TilePlan tile_plan(const GroupedRows& g, int NT, int KT) {
   const int64_t class_size = (g.E + kNumXcd - 1) / kNumXcd, singles = (class_size < g.rows ? class_size : g.rows) * NG;
   const int64_t tiles = p.lone ? 2 * g.cap / p.tmax : g.cap / p.tmax + active;
   const int64_t many = (tiles * NG + kNumXcd - 1) / kNumXcd;
-  p.grid = (unsigned)(kNumXcd * ((p.lone ? singles : 0) + many));
+  p.workgroups = kNumXcd * ((p.lone ? singles : 0) + many);
   return p;
 }
 
@@ -603,7 +603,7 @@ hipError_t launch_gemm1_int8_tile(const uint8_t* x, const float* x_scale, const 
   if (g.rows / g.K * H >= (int64_t)1 << 32) return hipErrorInvalidValue;   // x: 32-bit offsets of its rows
   const uint32_t x_bytes = (uint32_t)(g.rows / g.K * H);
   const TilePlan p = tile_plan(g, I / 128, H / kKB);
-  const dim3 grid(p.grid), block(kThreads);
+  const dim3 grid = wide_grid(p.workgroups), block(kThreads);
   if (packed)
     hipLaunchKernelGGL((gemm1_tile_int8_kernel<true>), grid, block, 0, stream, x, x_scale, w13, w13_scale,
                        g.padded_indptr, g.sorted_src, g.E, g.K, H, I, p.tmax, p.lone, p.NB, x_bytes, act);
@@ -618,7 +618,7 @@ hipError_t launch_gemm2_int8_tile(const uint8_t* q, const float* q_scale, const 
                                   const float* topk_weights, const GroupedRows& g, int H, int I, YT* Y,
                                   bool packed, hipStream_t stream) {
   const TilePlan p = tile_plan(g, (H + kTN - 1) / kTN, I / kKB);
-  const dim3 grid(p.grid), block(kThreads);
+  const dim3 grid = wide_grid(p.workgroups), block(kThreads);
   if (packed)
     hipLaunchKernelGGL((gemm2_tile_int8_kernel<true, YT>), grid, block, 0, stream, q, q_scale, w2, w2_scale,
                        topk_weights, g.padded_indptr, g.sorted_src, g.E, H, I, p.tmax, p.lone, p.NB, Y);

@@ -9,6 +9,15 @@ namespace fp8moe {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
+// Workgroups of a launch, over x and y: the runtime takes the threads of one
+// dimension modulo 2^32, without an error.  Whole rounds of the XCDs in x.
+constexpr int kGridShift = 22;
+inline dim3 wide_grid(int64_t workgroups) {
+  const int64_t row = (int64_t)1 << kGridShift;
+  return workgroups <= row ? dim3((unsigned)workgroups) : dim3((unsigned)row, (unsigned)((workgroups + row - 1) / row));
+}
+__device__ __forceinline__ int wide_block() { return (int)(blockIdx.y << kGridShift | blockIdx.x); }
+
 // One 16x16x64 int8 MFMA on 16 bytes of each lane; both operands take the
 // same bytes of a K step, so the order of K within it is immaterial.
 __device__ __forceinline__ i32x4 mfma16x16x64_i8(const v4i& a, const v4i& b, const i32x4& c) {
