@@ -24,9 +24,17 @@ hipError_t launch_combine(const uint16_t* Y, const int32_t* topk_ids, int T, int
                           uint16_t* out, hipStream_t stream) {
   if (T == 0) return hipSuccess;
   const int chunks = H / 8;
-  const dim3 grid((unsigned)T, (unsigned)((chunks + 255) / 256));
-  hipLaunchKernelGGL(combine_kernel, grid, dim3(256), 0, stream, Y, topk_ids, T, H, E, K, out);
-  return hipGetLastError();
+  // a launch's threads along x are taken modulo 2^32, without an error
+  constexpr int kMaxTokens = 1 << 23;
+  for (int t0 = 0; t0 < T; t0 += kMaxTokens) {
+    const int n = T - t0 < kMaxTokens ? T - t0 : kMaxTokens;
+    const dim3 grid((unsigned)n, (unsigned)((chunks + 255) / 256));
+    hipLaunchKernelGGL(combine_kernel, grid, dim3(256), 0, stream, Y + (size_t)t0 * K * H, topk_ids + (size_t)t0 * K,
+                       n, H, E, K, out + (size_t)t0 * H);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess || T - t0 <= kMaxTokens) return err;   // t0 would pass 2^31
+  }
+  return hipSuccess;
 }
 
 // Y rows in fp32 (the int8 layer's, where they are few): a thread sums 4

@@ -1,5 +1,5 @@
-"""Int8 stages whose launches have more workgroups than one grid dimension takes (2^32 threads): the same bits as with
-tall tiles, which need few workgroups."""
+"""Int8 stages and the combine where a launch has more workgroups than one grid dimension takes (2^32 threads).  The
+GEMMs give the same bits as with tall tiles, which need few workgroups."""
 
 import pytest
 import torch
@@ -44,3 +44,19 @@ def test_streaming_gemm2_of_many_workgroups():
     torch.cuda.synchronize()
     for a in range(0, T, 1 << 16):
         assert torch.equal(short[a:a + (1 << 16)], tall[a:a + (1 << 16)])
+
+
+def test_combine_of_many_tokens():
+    """2^24 + 5 tokens, of 256 threads each."""
+    T, H = (1 << 24) + 5, 128
+    say("combine tokens", T, H)
+    Y = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    for a in range(0, T, 1 << 20):
+        Y[a:a + (1 << 20)] = (torch.arange(a, min(a + (1 << 20), T), device="cuda") % 251)[:, None] + 1
+    ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    ids[::3] = -1
+    out = fm.combine(Y, ids, 1)
+    torch.cuda.synchronize()
+    Y[::3] = 0
+    for a in range(0, T, 1 << 20):
+        assert torch.equal(out[a:a + (1 << 20)], Y[a:a + (1 << 20)])
