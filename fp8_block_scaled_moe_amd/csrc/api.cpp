@@ -148,11 +148,20 @@ int auto_tile_m(int64_t T, int K, int n, int k, int E, int num_cu, bool gated) {
   return class_tile_m(cls, gated);
 }
 
+// A height of less than 128 rows, doubled until tiles of rows x 128 columns
+// (gated) or 256 fit one launch: the runtime takes its threads, 512 a tile,
+// modulo 2^32, without an error.  Every height gives the same results.
+int launchable_tile_m(int tm, int64_t rows, int n, int E, bool gated) {
+  const int64_t NT = gated ? n / 128 : (n + 255) / 256;
+  while (tm < 128 && ((rows + 127 * (int64_t)E) / tm + E) * NT >= (int64_t)1 << 23) tm *= 2;
+  return tm;
+}
+
 // Largest tile height a GEMM runs with: the requested one (GEMM1 at most
 // 128 rows), else the auto choice.
 int pick_tile_m(int requested, int64_t T, int K, int n, int k, int E, bool gated) {
   const int cap = gated ? kMaxTileGemm1 : kMaxTileGemm2;
-  if (requested != -1) return requested < cap ? requested : cap;
+  if (requested != -1) return launchable_tile_m(requested < cap ? requested : cap, T * K, n, E, gated);
   return auto_tile_m(T, K, n, k, E, device_num_cu(), gated);
 }
 
@@ -698,7 +707,7 @@ int moe_grouped_gemm_fp8(const void* a, const float* a_scale, const void* b, con
   if (rows == 0) return ok();
   if (!a || !a_scale || !b || !b_scale || !padded_indptr || !sorted_src || !out)
     return fail(FP8MOE_ERR_NULL, "null tensor argument");
-  const int tm = tile_m == -1 ? 128 : tile_m;
+  const int tm = tile_m == -1 ? 128 : launchable_tile_m(tile_m, rows, is_gated ? n / 2 : n, E, is_gated != 0);
   GroupedRows g{padded_indptr, sorted_src, rows, E, 1, rows, device_num_cu()};
   hipError_t err = launch_grouped_gemm_plain(static_cast<const uint8_t*>(a), a_scale, static_cast<const uint8_t*>(b),
                                              b_scale, g, n, k, is_gated != 0, out, tm,
