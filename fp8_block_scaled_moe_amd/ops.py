@@ -646,9 +646,12 @@ def moe_fused_int8(x, x_scale, w13, w13_scale, w2, w2_scale, topk_ids, topk_weig
     return out
 
 
-def _route_on(route, index, E=None):
-    """A routing result's arrays, checked (of E experts, if given); returns (padded_indptr, sorted_src, cap)."""
+def _route_on(route, index, E=None, rows=None):
+    """A routing result's arrays, checked (of E experts and T*K rows, if given: the kernels read the rows that
+    sorted_src names); returns (padded_indptr, sorted_src, cap)."""
     padded, src = route["padded_indptr"], route["sorted_src"]
+    if rows is not None and route["src_to_sorted"].numel() != rows:
+        raise ValueError(f"route is of {route['src_to_sorted'].numel()} rows, T*K is {rows}")
     _check(padded, torch.int32, (padded.numel() if E is None else E + 1,), index, "padded_indptr")
     _check(src, torch.int32, (src.numel(),), index, "sorted_src")
     return padded, src, src.numel()
@@ -667,7 +670,7 @@ def gemm1_swiglu_int8(x, x_scale, w13, w13_scale, route, T, K, align, tile_m=-1,
     _check(w13, torch.int8, (E, 2 * I, H), index, "w13")
     _check(x_scale, torch.float32, (T,), index, "x_scale")
     _check(w13_scale, torch.float32, (E, I2), index, "w13_scale")
-    padded, src, cap = _route_on(route, index, E)
+    padded, src, cap = _route_on(route, index, E, T * K)
     act = torch.zeros((cap, I), dtype=torch.bfloat16, device=x.device) if act is None else act
     _check(act, torch.bfloat16, (cap, I), index, "act")
     _launch(index, lib().moe_gemm1_swiglu_int8, _ptr(x), _ptr(x_scale), _ptr(w13), _ptr(w13_scale), _ptr(padded),
@@ -702,7 +705,7 @@ def gemm2_weighted_int8(q, q_scale, w2, w2_scale, route, topk_weights, T, K, ali
     _need(w2, torch.int8, "w2", 3)
     E, H, I = w2.shape
     index = q.get_device()
-    padded, src, cap = _route_on(route, index, E)
+    padded, src, cap = _route_on(route, index, E, T * K)
     _check(q, torch.int8, (cap, I), index, "q")
     _check(w2, torch.int8, (E, H, I), index, "w2")
     _check(q_scale, torch.float32, (cap,), index, "q_scale")

@@ -125,7 +125,7 @@ int moe_route_permute(const int32_t* topk_ids, int64_t T, int32_t K, int32_t E, 
  *            pads each expert to 16 rows only, and the GEMMs cut each expert
  *            into ceil(rows / tile_m) tiles of equal height (a multiple of
  *            16, at most tile_m; where so many tiles would not fit one
- *            launch, a given height is doubled (up to 128)
+ *            launch, a given height is doubled, up to 128)
  *   tile_n   -1 (auto) or 256: GEMM2 output columns per tile (GEMM1 always
  *            covers 128 columns of I, one requantisation block, per tile)
  *   weight_layout  FP8MOE_WEIGHTS_ROW_MAJOR (w13, w2 as above) or
