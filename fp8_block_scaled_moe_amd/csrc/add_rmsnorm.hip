@@ -15,9 +15,10 @@
 // so block maxima are xor-shuffles inside a wave.
 //
 // Measured in a graph, with residual, bf16 norm and e4m3 codes: 8192 rows of
-// 7168 102 us, 5.2 TB/s (a large copy: 4.8); 8192 of 2048 26.5 us, 5.7 TB/s;
+// 7168 102-104 us, 5.1 TB/s (a large copy: 4.8); 8192 of 2048 26.2 us, 5.8 TB/s;
 // 1024 of 7168 14.9 us; 64 of 7168 4.4 us; one 3.9 us, an empty launch's time
-// and one trip to memory and back.
+// and one trip to memory and back.  8192 rows of 7168 in the other formats:
+// MXFP8 101 us (5.2 TB/s), int8 100 (5.3), no codes 87 (5.4).
 #include "device_common.h"
 #include "fp8moe.h"
 #include "launch_ops.h"

@@ -24,7 +24,8 @@
 // four waves take every fourth 128-byte K step, load both operands straight
 // into registers in MFMA order, and add their int32 sums in LDS.  It is bound
 // by the weights' bytes: H=7168, I=2048, E=256, top-8, T=64 reads 6.5 GB in
-// 1.03 ms in GEMM1 (6.3 TB/s) and 3.3 GB in 0.50 ms in GEMM2 (6.6 TB/s).
+// 1.03 ms in GEMM1 (6.3 TB/s) and 3.3 GB in 0.50 ms in GEMM2 (6.6 TB/s);
+// row-major 1.06 and 0.61 ms.
 //
 // A handful of rows (launch_moe_direct_int8) take two launches without routing:
 // H=2048, I=768, E=128, top-8, T=1: 5.3 + 7.5 us, the call 12.4, against 28.8

@@ -28,6 +28,9 @@
 // From 64-row tiles up (layer, T=8192): streaming kernel 13.2 ms; tiles of 256
 // rows in runs of 16 N tiles 5.30, of 2 4.08; 288 rows 3.89; 16-byte stores of
 // the results 3.48; loads spread over the sub-tiles 3.43-3.46.
+// Row-major weights, GEMM1 and GEMM2 against packed ones (us): T=8192 2921 and
+// 1524 (2107 and 1182 packed), T=4096, Zipf 1.2 218 and 158 (157 and 131): a load
+// then touches 64 bytes of each of 16 rows instead of 1 KB in a run.
 // No gain: weights prefetched to L2 (GEMM1 2064 -> 2447 us), nontemporal weight
 // loads (2354), one barrier per two K steps (2091), nontemporal result stores
 // (layer at T=4096, Zipf 1.2: 343.5 -> 346), raised wave priority.

@@ -23,7 +23,7 @@ hipError_t launch_gemm2_int8(const uint8_t* q, const float* q_scale, const uint8
                              bool packed, hipStream_t stream);
 
 // The whole layer without routing for at most kDirectMaxRows routed rows of at
-// most kDirectMaxSlots slots; act [T*K][I].
+// most kDirectMaxSlots slots a token; act [T*K][I].
 constexpr int kDirectMaxRows = 16, kDirectMaxSlots = 8;
 hipError_t launch_moe_direct_int8(const uint8_t* x, const float* x_scale, const uint8_t* w13, const float* w13_scale,
                                   const uint8_t* w2, const float* w2_scale, const int32_t* topk_ids,

@@ -37,10 +37,10 @@
 //     are ranked by fp64 totals of their best choices;
 //   * what is left for the exact path: more close candidates than lanes, and
 //     chosen experts or close groups whose scores are next to fp32's smallest.
-// In a graph, us for 8192 tokens of 256 experts, top-8: softmax 6.6 (bf16 logits
-// 5.3), sigmoid with bias 8.2, softmax with bias 12.1, groups by their maximum
+// In a graph, us for 8192 tokens of 256 experts, top-8: softmax 6.4 (bf16 logits
+// 5.3), sigmoid with bias 8.2, softmax with bias 12.7, groups by their maximum
 // 7.3, by the sum of two 9.8 (14 while close ones went the exact way); 65537
-// tokens of 128: 15.8, 2.4 TB/s; one token of 256: 3.7; 64: 4.0.
+// tokens of 128: 15.2, 2.5 TB/s; one token of 256: 3.4; 64: 3.7.
 // Bound by the K rounds of maximum and removal and their shuffles, at few tokens
 // by the launch and one trip to memory.
 #include "device_common.h"
