@@ -648,10 +648,11 @@ def moe_fused_int8(x, x_scale, w13, w13_scale, w2, w2_scale, topk_ids, topk_weig
 
 def _route_on(route, index, E=None, rows=None):
     """A routing result's arrays, checked (of E experts and T*K rows, if given: the kernels read the rows that
-    sorted_src names); returns (padded_indptr, sorted_src, cap)."""
-    padded, src = route["padded_indptr"], route["sorted_src"]
-    if rows is not None and route["src_to_sorted"].numel() != rows:
-        raise ValueError(f"route is of {route['src_to_sorted'].numel()} rows, T*K is {rows}")
+    sorted_src names; src_to_sorted, which no stage reads, tells how many there are and may be left out);
+    returns (padded_indptr, sorted_src, cap)."""
+    padded, src, back = route["padded_indptr"], route["sorted_src"], route.get("src_to_sorted")
+    if rows is not None and back is not None and back.numel() != rows:
+        raise ValueError(f"route is of {back.numel()} rows, T*K is {rows}")
     _check(padded, torch.int32, (padded.numel() if E is None else E + 1,), index, "padded_indptr")
     _check(src, torch.int32, (src.numel(),), index, "sorted_src")
     return padded, src, src.numel()

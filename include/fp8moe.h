@@ -456,9 +456,10 @@ int moe_router_topk(const void* logits, int32_t logits_bf16, const float* bias, 
  *   w2   int8 [E, H, I]      w2_scale  fp32 [E, H]
  * Products are summed exactly in int32 and scaled once, in fp32.  GEMM1 stores
  * the SwiGLU output rounded to bf16 (act), which moe_quant_rows_int8 quantises
- * per row: s = amax / 127, q = round(act * (127 / amax)), ties to even (s = 1
- * and q = 0 where amax is below 2^-120); GEMM2 takes q and s.  A row of act that
- * holds an infinity or NaN gets codes 0 and scale NaN.
+ * per row: s = amax / 127, q = round(act * r), ties to even, with the fp32
+ * quotient r = 127 / amax (s = 1 and q = 0 where amax is below 2^-120); GEMM2
+ * takes q and s.  A row of act that holds an infinity or NaN gets codes 0 and
+ * scale NaN.
  *
  * moe_fused_int8 takes and does what moe_fused_fp8 does, with a workspace of
  * moe_fused_int8_workspace_size bytes; up to 2^22 values of Y (T * K * H) are

@@ -19,3 +19,15 @@ def test_routing_of_other_rows(T, K):
     cap = r["sorted_src"].numel()
     with pytest.raises(ValueError, match="route"):
         fm.gemm2_weighted_int8(z(cap, I, dtype=torch.int8), z(cap), w2, z(E, H), r, z(T, K), T, K, 16)
+
+
+def test_routing_of_the_two_arrays_that_the_stages_read():
+    E, H, I, T, K = 4, 256, 128, 8, 2
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ri = lambda *s: torch.randint(-127, 128, s, generator=g, device="cuda", dtype=torch.int8)
+    x, w13, xs, ws = ri(T, H), ri(E, 2 * I, H), torch.full((T,), 0.01, device="cuda"), torch.full((E, 2 * I), 0.01,
+                                                                                                device="cuda")
+    r = fm.route_permute(torch.randint(0, E, (T, K), generator=g, device="cuda", dtype=torch.int32), E, 16)
+    part = {k: r[k] for k in ("padded_indptr", "sorted_src")}
+    assert torch.equal(fm.gemm1_swiglu_int8(x, xs, w13, ws, part, T, K, 16),
+                       fm.gemm1_swiglu_int8(x, xs, w13, ws, r, T, K, 16))
