@@ -70,7 +70,17 @@ enum Fmt { kFmtFp8 = 0, kFmtMx8 = 1, kFmtMx4 = 2, kFmtBf16 = 3, kFmtInt8 = 4 };
 // (H=2048, I=768, E=128, top-8: T=33 57.1 us with fp32 rows, 59.2 with bf16;
 // T=256 153.7 and 150.0; T=512 170 and 162; T=4096 414 and 354.  H=7168,
 // I=2048, E=256: T=64 1551 and 1545; T=256 1964 and 1939).
-bool int8_y_f32(int64_t R, int H) { return R * H <= (int64_t)1 << 22; }
+constexpr int64_t kInt8YF32 = (int64_t)1 << 22;
+bool int8_y_f32(int64_t R, int H) { return R * H <= kInt8YF32; }
+
+// Bytes of Y.  The int8 layer's never less than its fp32 rows take, so that a
+// workspace made for the largest batch serves the smaller ones.
+size_t y_bytes(int64_t R, int H, int fmt) {
+  const size_t n = (size_t)(R > 0 ? R : 1) * H, bf16 = sizeof(uint16_t) * n;
+  if (fmt != kFmtInt8) return bf16;
+  const size_t f32 = sizeof(float) * (n < (size_t)kInt8YF32 ? n : (size_t)kInt8YF32);
+  return f32 > bf16 ? f32 : bf16;
+}
 
 // MX: q_scale holds one E8M0 byte per 32 columns instead of a float per 128;
 // MXFP4: q holds two e2m1 codes per byte; bf16: q holds 2 bytes per element
@@ -92,7 +102,7 @@ WsLayout ws_layout(int64_t T, int H, int I, int E, int K, int fmt) {
                    : fmt == kFmtInt8 ? sizeof(float) * (size_t)cap
                    : fmt != kFmtFp8 ? (size_t)cap * (I / 32)
                                     : sizeof(float) * (size_t)cap * (I / 128));
-  w.Y = take((fmt == kFmtInt8 && int8_y_f32(R, H) ? sizeof(float) : sizeof(uint16_t)) * (size_t)(R > 0 ? R : 1) * H);
+  w.Y = take(y_bytes(R, H, fmt));
   w.act = take(fmt == kFmtInt8 ? sizeof(uint16_t) * (size_t)cap * I : 0);
   w.total = off;
   return w;

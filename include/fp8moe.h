@@ -464,7 +464,8 @@ int moe_router_topk(const void* logits, int32_t logits_bf16, const float* bias, 
  * moe_fused_int8 takes and does what moe_fused_fp8 does, with a workspace of
  * moe_fused_int8_workspace_size bytes; up to 2^22 values of Y (T * K * H) are
  * kept in fp32 there, more in bf16, so a token's output may differ by a bf16
- * rounding of each slot with T.  The stages follow those of the bf16
+ * rounding of each slot with T.  The bytes never fall as T grows: a workspace
+ * for the largest batch serves every smaller one.  The stages follow those of the bf16
  * layer: act bf16 [cap, I], q int8 [cap, I], q_scale fp32 [cap]; rows of
  * padding (sorted_src < 0) are not written by any of them.
  * moe_quant_rows_int8 also serves rows of any bf16 matrix: `in` bf16 [rows, N]
