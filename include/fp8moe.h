@@ -421,8 +421,9 @@ int add_rmsnorm_quant(const void* x, const void* residual, int32_t residual_f32,
  *                equal ones in ascending index
  *   topk_weights score_e (without the bias), divided by the chosen ones' sum if
  *                renormalize != 0 (0 where that sum is 0), times scale
- * Which experts are chosen is decided as if in 64 bits; weights are computed in
- * fp32, or in 64 bits and rounded once where a chosen score is below 2^-100, so
+ * Which experts are chosen is decided as if in 64 bits (choices, or groups, of
+ * different scores that 64-bit sums round together may go either way); weights
+ * are computed in fp32, or in 64 bits and rounded once where a chosen score is below 2^-100, so
  * that scores that fp32 cannot hold keep their shares of the sum.  A weight's
  * last bits may differ with T.
  *
@@ -465,8 +466,8 @@ int moe_router_topk(const void* logits, int32_t logits_bf16, const float* bias, 
  * moe_fused_int8_workspace_size bytes; up to 2^22 values of Y (T * K * H) are
  * kept in fp32 there, more in bf16, so a token's output may differ by a bf16
  * rounding of each slot with T.  The bytes never fall as T grows: a workspace
- * for the largest batch serves every smaller one.  The stages follow those of the bf16
- * layer: act bf16 [cap, I], q int8 [cap, I], q_scale fp32 [cap]; rows of
+ * for the largest batch serves every smaller one.
+ * The stages follow those of the bf16 layer: act bf16 [cap, I], q int8 [cap, I], q_scale fp32 [cap]; rows of
  * padding (sorted_src < 0) are not written by any of them.
  * moe_quant_rows_int8 also serves rows of any bf16 matrix: `in` bf16 [rows, N]
  * -> q int8 [rows, N], scale fp32 [rows], N a multiple of 8, sorted_src NULL;
