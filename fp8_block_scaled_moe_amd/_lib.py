@@ -91,6 +91,16 @@ SIGNATURES = {
     # layout, stream
     "moe_gemm2_weighted_int8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32,
                                                _i32, _vp, _i64, _i32, _i32, _vp]),
+    "gemm_fp8_blocks_workspace_size": (ctypes.c_int, [_i64, _i32, _i32, _psz]),
+    # a, a_scale, b, b_scale, addend, M, N, K, out, out_f32, workspace, bytes, layout, stream
+    "gemm_fp8_blocks": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _i32, _vp, _sz, _i32, _vp]),
+    # a, a_scale, b, b_scale, m_indptr, rows, N, K, E, out, out_f32, layout, stream
+    "moe_grouped_gemm_fp8_ragged": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _i32, _i32,
+                                                   _vp]),
+    # a, b, m_indptr, rows, N, K, E, out, out_f32, layout, stream
+    "moe_grouped_gemm_bf16_ragged": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _i32, _i32, _vp]),
+    # in, in_f32, M, N, gated, q, scale, stream
+    "quant_fp8_blocks": (ctypes.c_int, [_vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp]),
     "moe_select_tile": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, _pi32, _pi32]),
     "moe_auto_tiles": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, _pi32, _pi32]),
     "moe_select_tile_classes": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _pi32]),

@@ -12,9 +12,11 @@
 #include <initializer_list>
 #include <string>
 #include <type_traits>
+#include <utility>
 
 #include "fp8moe.h"
 #include "launch_ops.h"
+#include "launch_products.h"
 #include "tile_select.h"
 
 using namespace fp8moe;
@@ -1113,6 +1115,133 @@ int moe_gemm2_weighted_int8(const void* q, const float* q_scale, const void* w2,
                                      weight_layout == FP8MOE_WEIGHTS_MFMA_TILED,
                                      (hipStream_t)stream);
   if (err != hipSuccess) return hip_fail(err, "gemm2 launch");
+  return ok();
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kProductRows = (int64_t)1 << 30;   // tiles x weight tiles stay below 2^31
+
+bool overlap_any(const void* out, int64_t n, std::initializer_list<std::pair<const void*, int64_t>> others) {
+  for (const auto& o : others)
+    if (overlap(out, n, o.first, o.second)) return true;
+  return false;
+}
+
+// Sizes of a product of `esize`-byte operands, E groups (1: dense).
+int check_product(int64_t rows, int32_t N, int32_t K, int32_t E, int esize, int32_t weight_layout) {
+  if (rows < 0 || N <= 0 || K <= 0 || E < 1)
+    return fail(FP8MOE_ERR_SHAPE, "invalid rows=%lld N=%d K=%d E=%d", (long long)rows, N, K, E);
+  if (rows >= kProductRows || N > FP8MOE_MAX_PRODUCT_DIM || K > FP8MOE_MAX_PRODUCT_DIM || E > FP8MOE_MAX_EXPERTS)
+    return fail(FP8MOE_ERR_LIMIT, "rows=%lld must be below 2^30, N=%d and K=%d at most %d, E=%d at most %d",
+                (long long)rows, N, K, FP8MOE_MAX_PRODUCT_DIM, E, FP8MOE_MAX_EXPERTS);
+  if (!valid_layout(weight_layout)) return fail(FP8MOE_ERR_SHAPE, "weight_layout %d not 0 or 1", weight_layout);
+  const int kb = K * esize;
+  if (kb % 16) return fail(FP8MOE_ERR_ALIGN, "K=%d must be a multiple of %d", K, 16 / esize);
+  if (weight_layout == FP8MOE_WEIGHTS_MFMA_TILED && (N % 16 || kb % 128))
+    return fail(FP8MOE_ERR_ALIGN, "MFMA-tiled weights need N=%d a multiple of 16 and K=%d of %d", N, K, 128 / esize);
+  return FP8MOE_OK;
+}
+
+// Runs a product whose sizes check_product took; null, alignment and overlap
+// checks first.
+int run_product(const void* a, const float* a_scale, const void* b, const float* b_scale, const void* addend,
+                const int32_t* indptr, int64_t rows, int32_t N, int32_t K, int32_t E, bool bf16, void* out,
+                int32_t out_f32, int32_t weight_layout, void* stream) {
+  if (rows == 0) return ok();
+  if (!a || !b || !out || (!bf16 && (!a_scale || !b_scale))) return fail(FP8MOE_ERR_NULL, "null tensor argument");
+  if (!aligned16(a) || !aligned16(b)) return fail(FP8MOE_ERR_ALIGN, "a and b must be 16-byte aligned");
+  const uintptr_t out_size = out_f32 ? 4 : 2;
+  if ((uintptr_t)out % out_size || (uintptr_t)addend % 2 || (uintptr_t)a_scale % 4 || (uintptr_t)b_scale % 4 ||
+      (uintptr_t)indptr % 4)
+    return fail(FP8MOE_ERR_ALIGN, "a tensor is not aligned to its elements");
+  const int kb = K * (bf16 ? 2 : 1), KT = (kb + 127) / 128;
+  const int64_t on = rows * N * (int64_t)out_size, sb = (int64_t)E * ((N + 127) / 128) * KT * 4;
+  if (overlap_any(out, on, {{a, rows * kb}, {b, (int64_t)E * N * kb}, {a_scale, rows * KT * 4}, {b_scale, sb},
+                            {indptr, ((int64_t)E + 1) * 4}}) ||
+      (overlap(out, on, addend, rows * N * 2) && !(addend == out && !out_f32)))
+    return fail(FP8MOE_ERR_SHAPE, "out overlaps an input");
+  ProductArgs P{};
+  P.a = static_cast<const uint8_t*>(a);
+  P.a_scale = a_scale;
+  P.b = static_cast<const uint8_t*>(b);
+  P.b_scale = b_scale;
+  P.addend = static_cast<const uint16_t*>(addend);
+  P.out = out;
+  P.indptr = indptr;
+  P.rows = rows;
+  P.N = N;
+  P.E = E;
+  P.kbytes = kb;
+  P.num_cu = device_num_cu();
+  P.bf16 = bf16;
+  P.packed = weight_layout == FP8MOE_WEIGHTS_MFMA_TILED;
+  P.out_f32 = out_f32 != 0;
+  P.vec = N % 8 == 0 && aligned16(out) && aligned16(addend);
+  const hipError_t err = launch_product(P, (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "product launch");
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_fp8_blocks_workspace_size(int64_t M, int32_t N, int32_t K, size_t* bytes) {
+  const int st = check_product(M, N, K, 1, 1, FP8MOE_WEIGHTS_ROW_MAJOR);
+  if (st) return st;
+  if (!bytes) return fail(FP8MOE_ERR_NULL, "bytes is null");
+  *bytes = 0;
+  return ok();
+}
+
+int gemm_fp8_blocks(const void* a, const float* a_scale, const void* b, const float* b_scale, const void* addend,
+                    int64_t M, int32_t N, int32_t K, void* out, int32_t out_f32, void* workspace,
+                    size_t workspace_bytes, int32_t weight_layout, void* stream) {
+  const int st = check_product(M, N, K, 1, 1, weight_layout);
+  if (st) return st;
+  return run_product(a, a_scale, b, b_scale, addend, nullptr, M, N, K, 1, false, out, out_f32, weight_layout, stream);
+}
+
+int moe_grouped_gemm_fp8_ragged(const void* a, const float* a_scale, const void* b, const float* b_scale,
+                                const int32_t* m_indptr, int64_t rows, int32_t N, int32_t K, int32_t E, void* out,
+                                int32_t out_f32, int32_t weight_layout, void* stream) {
+  const int st = check_product(rows, N, K, E, 1, weight_layout);
+  if (st) return st;
+  if (rows > 0 && !m_indptr) return fail(FP8MOE_ERR_NULL, "null tensor argument");
+  return run_product(a, a_scale, b, b_scale, nullptr, m_indptr, rows, N, K, E, false, out, out_f32, weight_layout,
+                     stream);
+}
+
+int moe_grouped_gemm_bf16_ragged(const void* a, const void* b, const int32_t* m_indptr, int64_t rows, int32_t N,
+                                 int32_t K, int32_t E, void* out, int32_t out_f32, int32_t weight_layout,
+                                 void* stream) {
+  const int st = check_product(rows, N, K, E, 2, weight_layout);
+  if (st) return st;
+  if (rows > 0 && !m_indptr) return fail(FP8MOE_ERR_NULL, "null tensor argument");
+  return run_product(a, nullptr, b, nullptr, nullptr, m_indptr, rows, N, K, E, true, out, out_f32, weight_layout,
+                     stream);
+}
+
+int quant_fp8_blocks(const void* in, int32_t in_f32, int64_t M, int32_t N, int32_t gated, void* q, float* scale,
+                     void* stream) {
+  if (M < 0 || N <= 0) return fail(FP8MOE_ERR_SHAPE, "invalid M=%lld N=%d", (long long)M, N);
+  if (N % 16) return fail(FP8MOE_ERR_ALIGN, "N=%d must be a multiple of 16", N);
+  if (M >= kProductRows || N > FP8MOE_MAX_PRODUCT_DIM)
+    return fail(FP8MOE_ERR_LIMIT, "M=%lld must be below 2^30 and N=%d at most %d", (long long)M, N,
+                FP8MOE_MAX_PRODUCT_DIM);
+  if (M == 0) return ok();
+  if (!in || !q || !scale) return fail(FP8MOE_ERR_NULL, "null tensor argument");
+  if (!aligned16(in) || !aligned16(q) || (uintptr_t)scale % 4)
+    return fail(FP8MOE_ERR_ALIGN, "in and q must be 16-byte aligned, scale 4-byte");
+  const int64_t ni = M * N * (in_f32 ? 4 : 2) * (gated ? 2 : 1), nq = M * N, ns = M * ((N + 127) / 128) * 4;
+  if (overlap(q, nq, in, ni) || overlap(scale, ns, in, ni) || overlap(q, nq, scale, ns))
+    return fail(FP8MOE_ERR_SHAPE, "in, q and scale overlap");
+  const hipError_t err = launch_quant_blocks(in, in_f32 != 0, M, N, gated != 0, static_cast<uint8_t*>(q), scale,
+                                             (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "quant_blocks launch");
   return ok();
 }
 

@@ -1,0 +1,33 @@
+// Launchers of the dense and the ragged grouped products and of the FP8 block
+// quantiser.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fp8moe {
+
+// One product.  Dense: indptr == nullptr, E == 1, every row in the one group.
+struct ProductArgs {
+  const uint8_t* a;        // [rows][kbytes]
+  const float* a_scale;    // [rows][KT]  (FP8)
+  const uint8_t* b;        // [E][N][kbytes], row-major or MFMA-tiled
+  const float* b_scale;    // [E][ceil(N / 128)][KT]  (FP8)
+  const uint16_t* addend;  // bf16 [rows][N] or nullptr; may be out
+  void* out;               // bf16 or fp32 [rows][N]
+  const int32_t* indptr;   // [E + 1]
+  int64_t rows;
+  int N, E;
+  int kbytes;              // bytes of a row of a or b, a multiple of 16; KT = ceil(kbytes / 128) steps
+  int num_cu;
+  bool bf16, packed, out_f32, vec;
+};
+
+hipError_t launch_product(const ProductArgs& P, hipStream_t stream);
+
+// v = in, or silu(gate) * up of in's two halves; per row and 128 columns
+// scale = amax / 448, q = e4m3(v / scale).
+hipError_t launch_quant_blocks(const void* in, bool f32, int64_t M, int N, bool gated, uint8_t* q, float* scale,
+                               hipStream_t stream);
+
+}  // namespace fp8moe

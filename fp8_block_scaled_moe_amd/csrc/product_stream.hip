@@ -1,0 +1,155 @@
+// Streaming kernel of the products: few rows, bound by the bytes of b.
+//
+// A workgroup owns 16 B weight rows and an M tile of up to 16 TS rows; its NW
+// waves take every NW-th 128-byte step of K, load both operands straight into
+// registers in MFMA order, U steps at a time, and add their fp32 sums in LDS in
+// the order of the waves, so results do not depend on timing.
+#include "int8_common.h"
+#include "products.h"
+
+namespace fp8moe {
+
+template <int TS, int B, int NW, int U, bool BF, bool PACKED>
+__global__ __launch_bounds__(64 * NW) void product_stream_kernel(const ProductArgs P) {
+  constexpr int TM = 16 * TS, TN = 16 * B;
+  constexpr int kHalf = PACKED ? 1024 : 64, kStep = PACKED ? 2048 : kKB;
+  __shared__ v4f red[NW][TS][B][64];
+  RaggedTile t;
+  if (!ragged_tile(P, TM, (P.N + TN - 1) / TN, (unsigned)wide_block(), t)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, l16 = lane & 15, n0 = TN * t.nt, kb = P.kbytes;
+  const int KF = kb / kKB, KT = (kb + kKB - 1) / kKB;   // whole steps, and all
+
+  // bands of weight rows; the last tile's rows past N read its last row
+  const uint8_t* wbase = P.b + ((size_t)t.e * P.N + n0) * kb;
+  const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)wbase, (short)0, min(TN, P.N - n0) * kb, kWeightRsrcFlags);
+  int woff[B];
+#pragma unroll
+  for (int b = 0; b < B; ++b)
+    woff[b] = PACKED ? min(16 * b, P.N - n0 - 16) * kb + 16 * lane : min(16 * b + l16, P.N - n0 - 1) * kb + 16 * g;
+  // rows past the tile's last read its last; never stored
+  const __amdgpu_buffer_rsrc_t ar = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(P.a + (size_t)t.row0 * kb), (short)0, t.h * kb, kWeightRsrcFlags);
+  int aoff[TS];
+  const float* sa[TS];
+#pragma unroll
+  for (int ts = 0; ts < TS; ++ts) {
+    const int r = min(16 * ts + l16, t.h - 1);
+    aoff[ts] = r * kb + 16 * g;
+    sa[ts] = BF ? nullptr : P.a_scale + (size_t)(t.row0 + r) * KT;
+  }
+  const float* sb = BF ? nullptr : P.b_scale + ((size_t)t.e * ((P.N + 127) / 128) + n0 / 128) * KT;
+
+  v4f acc[TS][B];
+#pragma unroll
+  for (int ts = 0; ts < TS; ++ts)
+#pragma unroll
+    for (int b = 0; b < B; ++b) acc[ts][b] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  auto product = [&](const v8i (&w)[B], const v8i (&x)[TS], const float (&s)[TS]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int ts = 0; ts < TS; ++ts)
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        if constexpr (BF) {
+          acc[ts][b] = mfma16x16x32_bf16_half(w[b], x[ts], acc[ts][b], 0);
+          acc[ts][b] = mfma16x16x32_bf16_half(w[b], x[ts], acc[ts][b], 1);
+        } else {
+          const v4f p = mfma16x16x128_fp8(w[b], x[ts], v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[ts][b][i] = fmaf(p[i], s[ts], acc[ts][b][i]);
+        }
+      }
+  };
+
+  for (int k0 = wave; k0 < KF; k0 += NW * U) {
+    v8i w[U][B], x[U][TS];
+    float s[U][TS];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * NW;
+      if (k < KF) {
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+          w[u][b] = join(__builtin_amdgcn_raw_buffer_load_b128(wr, woff[b], k * kStep, 0),
+                         __builtin_amdgcn_raw_buffer_load_b128(wr, woff[b] + kHalf, k * kStep, 0));
+#pragma unroll
+        for (int ts = 0; ts < TS; ++ts) {
+          x[u][ts] = join(__builtin_amdgcn_raw_buffer_load_b128(ar, aoff[ts], k * kKB, 0),
+                          __builtin_amdgcn_raw_buffer_load_b128(ar, aoff[ts] + 64, k * kKB, 0));
+          s[u][ts] = BF ? 0.f : sa[ts][k] * sb[k];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + u * NW < KF) product(w[u], x[u], s[u]);
+  }
+  // the last step, where it is short: a lane whose 16 bytes lie past the end
+  // reads the row's first and takes zeros on both sides (row-major only)
+  if (!PACKED && KF < KT && wave == KF % NW) {
+    const v4i zero = {0, 0, 0, 0};
+    const int rem = kb - KF * kKB;
+    const bool lo = 16 * g < rem, hi = 64 + 16 * g < rem;
+    v8i w[B], x[TS];
+    float s[TS];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const v4i l = __builtin_amdgcn_raw_buffer_load_b128(wr, lo ? woff[b] + KF * kKB : 0, 0, 0);
+      const v4i h = __builtin_amdgcn_raw_buffer_load_b128(wr, hi ? woff[b] + KF * kKB + 64 : 0, 0, 0);
+      w[b] = join(lo ? l : zero, hi ? h : zero);
+    }
+#pragma unroll
+    for (int ts = 0; ts < TS; ++ts) {
+      const v4i l = __builtin_amdgcn_raw_buffer_load_b128(ar, lo ? aoff[ts] + KF * kKB : 0, 0, 0);
+      const v4i h = __builtin_amdgcn_raw_buffer_load_b128(ar, hi ? aoff[ts] + KF * kKB + 64 : 0, 0, 0);
+      x[ts] = join(lo ? l : zero, hi ? h : zero);
+      s[ts] = BF ? 0.f : sa[ts][KF] * sb[KF];
+    }
+    product(w, x, s);
+  }
+
+#pragma unroll
+  for (int ts = 0; ts < TS; ++ts)
+#pragma unroll
+    for (int b = 0; b < B; ++b) red[wave][ts][b][lane] = acc[ts][b];
+  __syncthreads();
+  for (int u = wave; u < TS * B; u += NW) {
+    const int ts = u / B, b = u % B;
+    v4f y = red[0][ts][b][lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) y += red[w][ts][b][lane];
+    const int r = 16 * ts + l16;
+    if (r < t.h) store_out4(P, (int64_t)t.row0 + r, n0 + 16 * b + 4 * g, y);
+  }
+}
+
+namespace {
+
+template <int TS, int B, int NW, int U, bool BF>
+hipError_t launch_stream(const ProductArgs& P, hipStream_t stream) {
+  const int64_t NT = (P.N + 16 * B - 1) / (16 * B);
+  const int64_t tiles = P.indptr ? P.rows / (16 * TS) + (P.rows < P.E ? P.rows : P.E) : (P.rows + 16 * TS - 1) / (16 * TS);
+  if (tiles * NT >= (int64_t)1 << 31) return hipErrorInvalidValue;
+  const dim3 grid = wide_grid((tiles * NT + kNumXcd - 1) / kNumXcd * kNumXcd), block(64 * NW);
+  if (P.packed) hipLaunchKernelGGL((product_stream_kernel<TS, B, NW, U, BF, true>), grid, block, 0, stream, P);
+  else hipLaunchKernelGGL((product_stream_kernel<TS, B, NW, U, BF, false>), grid, block, 0, stream, P);
+  return hipGetLastError();
+}
+
+template <bool BF>
+hipError_t launch_rows(const ProductArgs& P, hipStream_t stream) {
+  const int64_t groups = P.rows < P.E ? P.rows : P.E, share = (P.rows + groups - 1) / groups;
+  if (share <= 16) return launch_stream<1, 2, 4, 4, BF>(P, stream);
+  if (share <= 32) return launch_stream<2, 2, 4, 4, BF>(P, stream);
+  return launch_stream<4, 2, 4, 2, BF>(P, stream);
+}
+
+}  // namespace
+
+hipError_t launch_product(const ProductArgs& P, hipStream_t stream) {
+  return P.bf16 ? launch_rows<true>(P, stream) : launch_rows<false>(P, stream);
+}
+
+}  // namespace fp8moe

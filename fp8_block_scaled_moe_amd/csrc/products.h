@@ -1,0 +1,171 @@
+// Device-side pieces shared by the kernels of the products outside the routed
+// layer: the dense FP8 product with block scales and the products grouped by
+// expert over ragged rows (FP8 and bf16).
+//
+//   out[m][n] = sum_k a[m][k] b[e][n][k]   with e the group of row m
+//
+// In FP8 every 128 values of K are summed by one MFMA into a zero accumulator
+// and folded in fp32: acc += p * (a_scale[m][k/128] * b_scale[e][n/128][k/128]).
+// bf16 operands accumulate inside the MFMA.  Sums are fp32 throughout and are
+// rounded once, to bf16 or not at all, after an addend was added.
+#pragma once
+
+#include "gemm_kernels.h"
+#include "launch_products.h"
+
+namespace fp8moe {
+
+// Rows of one tile: group e's rows row0 .. row0 + h - 1, and the index of its
+// tile of weight rows.
+struct RaggedTile {
+  int e, row0, h, nt;
+};
+
+// Tiles of TM rows of four groups a lane, 256 groups a wave; indptr values
+// outside [0, rows] or descending leave groups empty instead of rows out of
+// range.
+struct GroupChunk {
+  int start[4], len[4], tiles[4], incl, total;
+  __device__ __forceinline__ void load(const int32_t* __restrict__ indptr, int E, int rows, int TM, int c, int lane) {
+    int s[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) s[k] = min(max(indptr[min(c + 4 * lane + k, E)], 0), rows);
+    int sum = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      start[k] = s[k];
+      len[k] = c + 4 * lane + k < E ? max(s[k + 1] - s[k], 0) : 0;
+      tiles[k] = (len[k] + TM - 1) / TM;
+      sum += tiles[k];
+    }
+    incl = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o);
+      if (lane >= o) incl += v;
+    }
+    total = __builtin_amdgcn_readlane(incl, 63);
+  }
+};
+
+// M tiles whose weight tiles are taken together: one XCD's workgroups then
+// share 8 row tiles and a few weight tiles in its L2.
+constexpr int kPanel = 8;
+
+// Item j of a group with nm row tiles: panels of kPanel row tiles, in a panel
+// the weight tiles, and the panel's row tiles innermost.
+__device__ __forceinline__ void panel_item(unsigned j, unsigned nm, unsigned NT, int& mt, int& nt) {
+  unsigned p = 0, rem = j, pm = nm;
+  if (nm > kPanel) {
+    p = j / (kPanel * NT);
+    rem = j - p * kPanel * NT;
+    pm = min(nm - kPanel * p, (unsigned)kPanel);
+  }
+  const unsigned n = rem / pm;
+  nt = (int)n;
+  mt = (int)(kPanel * p + rem - n * pm);
+}
+
+// The tile of this workgroup (false: none).  Workgroup b runs on XCD b % 8 and
+// takes item (b % 8) * ceil(items / 8) + b / 8, so each XCD works through a
+// contiguous range of items.  An M tile has at most TM rows; a group's rows
+// are cut into tiles of equal height, a multiple of 16.
+__device__ __forceinline__ bool ragged_tile(const ProductArgs& P, int TM, int NT, unsigned block, RaggedTile& t) {
+  const unsigned slot = block / kNumXcd, xcd = block % kNumXcd;
+  int start, len;
+  unsigned nm, j;
+  if (P.indptr == nullptr) {
+    start = 0;
+    len = (int)P.rows;
+    nm = (unsigned)((len + TM - 1) / TM);
+    const unsigned items = nm * NT, per = (items + kNumXcd - 1) / kNumXcd;
+    j = xcd * per + slot;
+    if (slot >= per || j >= items) return false;
+    t.e = 0;
+  } else {
+    const int lane = threadIdx.x & 63, rows = (int)P.rows;
+    GroupChunk ch;
+    ch.load(P.indptr, P.E, rows, TM, 0, lane);
+    unsigned tot = ch.total;
+    for (int c = 256; c < P.E; c += 256) {
+      GroupChunk more;
+      more.load(P.indptr, P.E, rows, TM, c, lane);
+      tot += more.total;
+    }
+    const unsigned items = __builtin_amdgcn_readfirstlane(tot) * NT, per = (items + kNumXcd - 1) / kNumXcd;
+    const unsigned L = xcd * per + slot;
+    if (slot >= per || L >= items) return false;
+    const int want = (int)(L / NT);      // the group that holds tile `want` holds item L
+    int base = 0, c = 0;
+    while (base + ch.total <= want) {    // want < tot: this stops at a chunk of the groups
+      base += ch.total;
+      c += 256;
+      ch.load(P.indptr, P.E, rows, TM, c, lane);
+    }
+    const int own = __builtin_amdgcn_readfirstlane(__popcll(__ballot(base + ch.incl <= want)));
+    int tl[4], st[4], ln[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      tl[i] = __builtin_amdgcn_readlane(ch.tiles[i], own);
+      st[i] = __builtin_amdgcn_readlane(ch.start[i], own);
+      ln[i] = __builtin_amdgcn_readlane(ch.len[i], own);
+    }
+    int first = __builtin_amdgcn_readfirstlane(base) + __builtin_amdgcn_readlane(ch.incl, own) -
+                (tl[0] + tl[1] + tl[2] + tl[3]);
+    int k = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (k == i && first + tl[i] <= want) {
+        first += tl[i];
+        k = i + 1;
+      }
+    start = st[0], len = ln[0];
+    nm = (unsigned)tl[0];
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+      if (k == i) {
+        start = st[i];
+        len = ln[i];
+        nm = (unsigned)tl[i];
+      }
+    t.e = c + 4 * own + k;
+    j = L - (unsigned)first * NT;
+  }
+  int mt;
+  panel_item(j, nm, (unsigned)NT, mt, t.nt);
+  const int tm = ((len + (int)nm - 1) / (int)nm + 15) / 16 * 16;
+  t.row0 = start + mt * tm;
+  t.h = min(tm, len - mt * tm);
+  return t.h > 0;
+}
+
+// Four consecutive columns n .. n + 3 of row `row`, the addend added first.
+// vec: N % 8 == 0 and aligned tensors, so that whole groups of four lie inside
+// a row on 8-byte (bf16) or 16-byte (fp32) boundaries.
+__device__ __forceinline__ void store_out4(const ProductArgs& P, int64_t row, int n, v4f v) {
+  const int64_t at = row * P.N + n;
+  if (P.vec) {
+    if (n >= P.N) return;
+    if (P.addend) {
+      const uint2 d = *reinterpret_cast<const uint2*>(P.addend + at);
+      v[0] += __uint_as_float(d.x << 16);
+      v[1] += __uint_as_float(d.x & 0xffff0000u);
+      v[2] += __uint_as_float(d.y << 16);
+      v[3] += __uint_as_float(d.y & 0xffff0000u);
+    }
+    if (P.out_f32) *reinterpret_cast<v4f*>(static_cast<float*>(P.out) + at) = v;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + at) =
+          uint2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < P.N) {
+      const float y = P.addend ? v[i] + bf16_to_f32(P.addend[at + i]) : v[i];
+      if (P.out_f32) static_cast<float*>(P.out)[at + i] = y;
+      else static_cast<uint16_t*>(P.out)[at + i] = (uint16_t)pack2_bf16(y, y);
+    }
+}
+
+}  // namespace fp8moe

@@ -812,6 +812,121 @@ def moe_router_topk(logits, K, score=SCORE_SOFTMAX, bias=None, n_group=1, topk_g
     return ids, weights
 
 
+# ---------------------------------------------------------------- dense and ragged grouped products
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def _fp8(t, name, ndim):
+    """An e4m3 tensor (float8_e4m3fn or uint8 codes) of this many dims."""
+    t = _u8(t) if isinstance(t, torch.Tensor) else t
+    _need(t, torch.uint8, name, ndim)
+    return t
+
+
+def _out_dtype(out, dtype):
+    dtype = dtype if out is None else getattr(out, "dtype", None)
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out must be bfloat16 or float32, got {dtype}")
+    return dtype
+
+
+def gemm_workspace_size(M, N, K):
+    n = ctypes.c_size_t(0)
+    check(lib().gemm_fp8_blocks_workspace_size(M, N, K, ctypes.byref(n)))
+    return int(n.value)
+
+
+def alloc_workspace_gemm(M, N, K, device):
+    """A device workspace for gemm_fp8_blocks."""
+    return torch.empty(gemm_workspace_size(M, N, K), dtype=torch.uint8, device=device)
+
+
+def gemm_fp8_blocks(a, a_scale, b, b_scale, addend=None, out=None, out_dtype=torch.bfloat16, workspace=None,
+                    weight_layout=WEIGHTS_ROW_MAJOR):
+    """Dense FP8 product with block scales, a [M, K] . b [N, K]^T (+ addend): a e4m3 with a_scale fp32
+    [M, ceil(K/128)], b e4m3 with b_scale fp32 [ceil(N/128), ceil(K/128)], addend bf16 [M, N] (may be out).
+    Returns out [M, N], bf16 or fp32 (out_dtype, or the type of a given out).  weight_layout 1: b packed by
+    pack_weights (as [1, N, K])."""
+    a, b = _fp8(a, "a", 2), _fp8(b, "b", 2)
+    M, K = a.shape
+    N = b.shape[0]
+    index = a.get_device()
+    _check(b, torch.uint8, (N, K), index, "b")
+    _check(a_scale, torch.float32, (M, _blocks(K)), index, "a_scale")
+    _check(b_scale, torch.float32, (_blocks(N), _blocks(K)), index, "b_scale")
+    if addend is not None:
+        _check(addend, torch.bfloat16, (M, N), index, "addend")
+    dtype = _out_dtype(out, out_dtype)
+    out = _out(out, dtype, (M, N), a, "out")
+    if workspace is None:
+        workspace = alloc_workspace_gemm(M, N, K, a.device)
+    else:
+        _check(workspace, workspace.dtype, workspace.shape, index, "workspace")
+    _launch(index, lib().gemm_fp8_blocks, a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(),
+            _ptr(addend), M, N, K, out.data_ptr(), dtype == torch.float32, workspace.data_ptr(), workspace.nbytes,
+            weight_layout)
+    return out
+
+
+def _ragged(a, b, m_indptr, out, out_dtype):
+    """Checks shared by the ragged products; returns (rows, N, K, E, device index, out, fp32?)."""
+    rows, K = a.shape
+    E, N, _ = b.shape
+    index = a.get_device()
+    _check(b, a.dtype, (E, N, K), index, "b")
+    _check(m_indptr, torch.int32, (E + 1,), index, "m_indptr")
+    dtype = _out_dtype(out, out_dtype)
+    if out is None:      # rows of no group are not written
+        out = torch.zeros((rows, N), dtype=dtype, device=a.device)
+    else:
+        _check(out, dtype, (rows, N), index, "out")
+    return rows, N, K, E, index, out, dtype == torch.float32
+
+
+def grouped_gemm_fp8_ragged(a, a_scale, b, b_scale, m_indptr, out=None, out_dtype=torch.bfloat16,
+                            weight_layout=WEIGHTS_ROW_MAJOR):
+    """FP8 products grouped by expert over rows without padding: rows m_indptr[e] .. m_indptr[e+1]-1 of a
+    e4m3 [rows, K] (a_scale fp32 [rows, ceil(K/128)]) times b[e]^T, b e4m3 [E, N, K] with b_scale fp32
+    [E, ceil(N/128), ceil(K/128)], m_indptr int32 [E+1].  Returns out [rows, N], bf16 or fp32; rows of no
+    group are not written (zero when out is allocated here).  weight_layout 1: b packed by pack_weights."""
+    a, b = _fp8(a, "a", 2), _fp8(b, "b", 3)
+    rows, N, K, E, index, out, f32 = _ragged(a, b, m_indptr, out, out_dtype)
+    _check(a_scale, torch.float32, (rows, _blocks(K)), index, "a_scale")
+    _check(b_scale, torch.float32, (E, _blocks(N), _blocks(K)), index, "b_scale")
+    _launch(index, lib().moe_grouped_gemm_fp8_ragged, a.data_ptr(), a_scale.data_ptr(), b.data_ptr(),
+            b_scale.data_ptr(), m_indptr.data_ptr(), rows, N, K, E, out.data_ptr(), f32, weight_layout)
+    return out
+
+
+def grouped_gemm_bf16_ragged(a, b, m_indptr, out=None, out_dtype=torch.bfloat16, weight_layout=WEIGHTS_ROW_MAJOR):
+    """grouped_gemm_fp8_ragged with unquantised operands: a bf16 [rows, K], b bf16 [E, N, K]."""
+    _need(a, torch.bfloat16, "a", 2)
+    _need(b, torch.bfloat16, "b", 3)
+    rows, N, K, E, index, out, f32 = _ragged(a, b, m_indptr, out, out_dtype)
+    _launch(index, lib().moe_grouped_gemm_bf16_ragged, a.data_ptr(), b.data_ptr(), m_indptr.data_ptr(), rows, N, K, E,
+            out.data_ptr(), f32, weight_layout)
+    return out
+
+
+def quant_fp8_blocks(x, gated=False, q=None, scale=None):
+    """bf16 or fp32 x [M, N] -> (e4m3 codes uint8 [M, N], fp32 scales [M, ceil(N/128)], one per row and 128
+    columns).  gated: x is [M, 2N], gate and up halves, and silu(gate) * up is quantised."""
+    f32 = getattr(x, "dtype", None) == torch.float32
+    _need(x, torch.float32 if f32 else torch.bfloat16, "x", 2)
+    M, N = x.shape
+    if gated:
+        if N % 2:
+            raise ValueError("gated x must have an even number of columns")
+        N //= 2
+    q = _out(q, torch.uint8, (M, N), x, "q")
+    scale = _out(scale, torch.float32, (M, _blocks(N)), x, "scale")
+    _launch(x.get_device(), lib().quant_fp8_blocks, x.data_ptr(), f32, M, N, bool(gated), q.data_ptr(),
+            scale.data_ptr())
+    return q, scale
+
+
 # ---------------------------------------------------------------- cost model (host only)
 
 def select_tile(total_rows, n, k, E, num_cu=256, gated=False):

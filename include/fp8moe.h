@@ -495,6 +495,78 @@ int moe_gemm2_weighted_int8(const void* q, const float* q_scale, const void* w2,
                             int64_t T, int32_t H, int32_t I, int32_t E, int32_t K, int32_t align, void* Y,
                             int64_t cap, int32_t tile_m, int32_t weight_layout, void* stream);
 
+/* ---------------------------------------------------------------- dense FP8 product with block scales
+ * gemm_fp8_blocks: the layer's dense neighbours (projections, a shared expert,
+ * a dense FFN) in the layer's own format:
+ *   out[m, n] = sum_k a[m, k] a_scale[m, k/128] b[n, k] b_scale[n/128, k/128] (+ addend[m, n])
+ *   a       fp8  [M, K]
+ *   a_scale fp32 [M, ceil(K/128)]               one per row and 128 columns
+ *   b       fp8  [N, K], or packed by moe_pack_weights (E = 1)
+ *   b_scale fp32 [ceil(N/128), ceil(K/128)]     one per 128 x 128
+ *   addend  bf16 [M, N] or NULL; may be out itself when out is bf16
+ *   out     bf16, or fp32 (out_f32 != 0) [M, N]
+ * Each block of 128 values of K is summed by one MFMA and folded with its
+ * scales in fp32; out is rounded once.  (The fp8 MFMA's own sum of 128 products
+ * carries up to 5e-5 of the sum of their magnitudes; typically 1e-6.)  NaN codes and infinite or NaN scales
+ * give NaN or infinities in the rows and columns that they belong to.
+ * K is a multiple of 16 and N any (MFMA_TILED: of 128 and 16; FP8MOE_ERR_ALIGN),
+ * both at most FP8MOE_MAX_PRODUCT_DIM, M < 2^30 (FP8MOE_ERR_LIMIT).  a and b are
+ * 16-byte aligned, the others to their elements (FP8MOE_ERR_ALIGN); out overlaps
+ * no other tensor but addend as said (FP8MOE_ERR_SHAPE).  M == 0 launches nothing.
+ * The workspace is gemm_fp8_blocks_workspace_size bytes (0 for many sizes: then it may be
+ * NULL), 256-byte aligned; it holds nothing between calls.
+ * Deterministic; an output's last bits may differ with M, N and the layout.
+ */
+#define FP8MOE_MAX_PRODUCT_DIM 65536
+int gemm_fp8_blocks_workspace_size(int64_t M, int32_t N, int32_t K, size_t* bytes);
+int gemm_fp8_blocks(const void* a, const float* a_scale, const void* b, const float* b_scale, const void* addend,
+                    int64_t M, int32_t N, int32_t K, void* out, int32_t out_f32, void* workspace,
+                    size_t workspace_bytes, int32_t weight_layout, void* stream);
+
+/* ---------------------------------------------------------------- products grouped by expert, ragged rows
+ * For rows that are sorted by expert already and packed without padding (rows
+ * received from other ranks, or of a router of the caller's own):
+ *   out[m, :] = a[m, :] . b[e]^T   for m_indptr[e] <= m < m_indptr[e+1]
+ *   moe_grouped_gemm_fp8_ragged   a fp8 [rows, K], a_scale fp32 [rows, ceil(K/128)],
+ *                                 b fp8 [E, N, K], b_scale fp32 [E, ceil(N/128), ceil(K/128)]
+ *   moe_grouped_gemm_bf16_ragged  a bf16 [rows, K], b bf16 [E, N, K], fp32 sums
+ *   m_indptr int32 [E+1] (device), ascending, m_indptr[0] >= 0,
+ *            m_indptr[E] <= rows; groups may be empty.  moe_route_permute's
+ *            m_indptr is of this form.  Values outside [0, rows] are taken as
+ *            the nearer end and a group whose end lies ahead of its start as
+ *            empty, so no row outside the tensors is touched; where groups
+ *            overlap, their common rows hold either's result.
+ *   out      bf16, or fp32 (out_f32 != 0) [rows, N]; rows of no group are not
+ *            written
+ * Sums, types, sizes, alignment, overlap and errors as for gemm_fp8_blocks (in bf16 K is a
+ * multiple of 8, MFMA_TILED of 64: moe_pack_weights takes bytes, 2 K).
+ * 1 <= E <= FP8MOE_MAX_EXPERTS, rows < 2^30.  rows == 0 launches nothing.
+ */
+int moe_grouped_gemm_fp8_ragged(const void* a, const float* a_scale, const void* b, const float* b_scale,
+                                const int32_t* m_indptr, int64_t rows, int32_t N, int32_t K, int32_t E, void* out,
+                                int32_t out_f32, int32_t weight_layout, void* stream);
+int moe_grouped_gemm_bf16_ragged(const void* a, const void* b, const int32_t* m_indptr, int64_t rows, int32_t N,
+                                 int32_t K, int32_t E, void* out, int32_t out_f32, int32_t weight_layout,
+                                 void* stream);
+
+/* ---------------------------------------------------------------- FP8 activations with block scales
+ * quant_fp8_blocks: per row and 128 columns (the last block may be short)
+ *   s = amax / 448 in fp32 (1 where that is 0), q = e4m3(v / s), saturating,
+ * with v = in, or (gated != 0) v = silu(in[:, :N]) * in[:, N:] in fp32: what
+ * the products above take as a and a_scale.
+ *   in    bf16, or fp32 (in_f32 != 0) [M, N], gated [M, 2N]
+ *   q     fp8  [M, N]
+ *   scale fp32 [M, ceil(N/128)]
+ * A block whose v holds an infinity or NaN has codes 0x7F and scale NaN.  The
+ * quotient is taken as v * (448 / amax), so a code may differ from the
+ * correctly rounded quotient's by one step within 2^-23 of the middle of two.
+ * N is a multiple of 16 (FP8MOE_ERR_ALIGN), at most FP8MOE_MAX_PRODUCT_DIM;
+ * M < 2^30 (FP8MOE_ERR_LIMIT); in and q are 16-byte aligned; no overlap
+ * (FP8MOE_ERR_SHAPE).  M == 0 launches nothing.
+ */
+int quant_fp8_blocks(const void* in, int32_t in_f32, int64_t M, int32_t N, int32_t gated, void* q, float* scale,
+                     void* stream);
+
 /* ---------------------------------------------------------------- weight packing
  * moe_pack_weights: expert weights e4m3 [E, N, K] row-major (w13 with N = 2I,
  * K = H, or w2 with N = H, K = I) -> FP8MOE_WEIGHTS_MFMA_TILED, the layout
