@@ -7,6 +7,8 @@
 
 namespace fp8moe {
 
+constexpr int kMaxProductDim = 65536;   // largest N and K
+
 // One product.  Dense: indptr == nullptr, E == 1, every row in the one group.
 struct ProductArgs {
   const uint8_t* a;        // [rows][kbytes]
@@ -24,6 +26,8 @@ struct ProductArgs {
 };
 
 hipError_t launch_product(const ProductArgs& P, hipStream_t stream);
+// The tile kernel, of up to tile_m (128 or 256) rows a tile.
+hipError_t launch_product_tile(const ProductArgs& P, int tile_m, hipStream_t stream);
 
 // v = in, or silu(gate) * up of in's two halves; per row and 128 columns
 // scale = amax / 448, q = e4m3(v / scale).

@@ -13,7 +13,7 @@ template <int TS, int B, int NW, int U, bool BF, bool PACKED>
 __global__ __launch_bounds__(64 * NW) void product_stream_kernel(const ProductArgs P) {
   constexpr int TM = 16 * TS, TN = 16 * B;
   constexpr int kHalf = PACKED ? 1024 : 64, kStep = PACKED ? 2048 : kKB;
-  __shared__ v4f red[NW][TS][B][64];
+  __shared__ v4f red[NW][TM][4 * B];
   RaggedTile t;
   if (!ragged_tile(P, TM, (P.N + TN - 1) / TN, (unsigned)wide_block(), t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -110,18 +110,21 @@ __global__ __launch_bounds__(64 * NW) void product_stream_kernel(const ProductAr
     product(w, x, s);
   }
 
+  // the waves' sums, as [row][column]; a thread then adds up eight columns
 #pragma unroll
   for (int ts = 0; ts < TS; ++ts)
 #pragma unroll
-    for (int b = 0; b < B; ++b) red[wave][ts][b][lane] = acc[ts][b];
+    for (int b = 0; b < B; ++b) red[wave][16 * ts + l16][4 * b + g] = acc[ts][b];
   __syncthreads();
-  for (int u = wave; u < TS * B; u += NW) {
-    const int ts = u / B, b = u % B;
-    v4f y = red[0][ts][b][lane];
+  for (int u = threadIdx.x; u < TM * 2 * B; u += 64 * NW) {
+    const int r = u / (2 * B), c = u % (2 * B);
+    v4f lo = red[0][r][2 * c], hi = red[0][r][2 * c + 1];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) y += red[w][ts][b][lane];
-    const int r = 16 * ts + l16;
-    if (r < t.h) store_out4(P, (int64_t)t.row0 + r, n0 + 16 * b + 4 * g, y);
+    for (int w = 1; w < NW; ++w) {
+      lo += red[w][r][2 * c];
+      hi += red[w][r][2 * c + 1];
+    }
+    if (r < t.h) store_out8(P, (int64_t)t.row0 + r, n0 + 8 * c, lo, hi);
   }
 }
 
@@ -149,6 +152,8 @@ hipError_t launch_rows(const ProductArgs& P, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_product(const ProductArgs& P, hipStream_t stream) {
+  const int64_t groups = P.rows < P.E ? P.rows : P.E, share = (P.rows + groups - 1) / groups;
+  if (share > 16) return launch_product_tile(P, share > 128 ? 256 : 128, stream);
   return P.bf16 ? launch_rows<true>(P, stream) : launch_rows<false>(P, stream);
 }
 

@@ -139,33 +139,43 @@ __device__ __forceinline__ bool ragged_tile(const ProductArgs& P, int TM, int NT
   return t.h > 0;
 }
 
-// Four consecutive columns n .. n + 3 of row `row`, the addend added first.
-// vec: N % 8 == 0 and aligned tensors, so that whole groups of four lie inside
-// a row on 8-byte (bf16) or 16-byte (fp32) boundaries.
-__device__ __forceinline__ void store_out4(const ProductArgs& P, int64_t row, int n, v4f v) {
+// Eight consecutive columns n .. n + 7 of row `row`, the addend added first.
+// vec: N % 8 == 0 and aligned tensors, so that groups of eight columns lie
+// inside or outside a row as a whole, on 16-byte boundaries.
+__device__ __forceinline__ void store_out8(const ProductArgs& P, int64_t row, int n, v4f lo, v4f hi) {
+  if (n >= P.N) return;
   const int64_t at = row * P.N + n;
+  float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   if (P.vec) {
-    if (n >= P.N) return;
     if (P.addend) {
-      const uint2 d = *reinterpret_cast<const uint2*>(P.addend + at);
-      v[0] += __uint_as_float(d.x << 16);
-      v[1] += __uint_as_float(d.x & 0xffff0000u);
-      v[2] += __uint_as_float(d.y << 16);
-      v[3] += __uint_as_float(d.y & 0xffff0000u);
+      const uint4 d = *reinterpret_cast<const uint4*>(P.addend + at);
+      const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] += __uint_as_float(w[i] << 16);
+        v[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+      }
     }
-    if (P.out_f32) *reinterpret_cast<v4f*>(static_cast<float*>(P.out) + at) = v;
-    else
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + at) =
-          uint2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
+    if (P.out_f32) {
+      v4f* o = reinterpret_cast<v4f*>(static_cast<float*>(P.out) + at);
+      o[0] = v4f{v[0], v[1], v[2], v[3]};
+      o[1] = v4f{v[4], v[5], v[6], v[7]};
+    } else {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + at) =
+          uint4{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]), pack2_bf16(v[6], v[7])};
+    }
     return;
   }
+  const int live = min(8, P.N - n);
+#pragma unroll 1
+  for (int i = 0; i < live; ++i) {
+    float y = v[0];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (n + i < P.N) {
-      const float y = P.addend ? v[i] + bf16_to_f32(P.addend[at + i]) : v[i];
-      if (P.out_f32) static_cast<float*>(P.out)[at + i] = y;
-      else static_cast<uint16_t*>(P.out)[at + i] = (uint16_t)pack2_bf16(y, y);
-    }
+    for (int k = 1; k < 8; ++k) y = i == k ? v[k] : y;
+    if (P.addend) y += bf16_to_f32(P.addend[at + i]);
+    if (P.out_f32) static_cast<float*>(P.out)[at + i] = y;
+    else static_cast<uint16_t*>(P.out)[at + i] = (uint16_t)pack2_bf16(y, y);
+  }
 }
 
 }  // namespace fp8moe

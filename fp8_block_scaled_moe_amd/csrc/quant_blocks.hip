@@ -4,9 +4,11 @@
 //
 // 16 lanes hold a block, 8 values each, from the one read to the codes; the
 // maximum is taken over the values' bits (sign cleared), which order as
-// integers with infinity and NaN last.  v / scale is v * (448 / amax), one
-// division a block: two roundings of 2^-24 against one, which moves a code only
-// where v / scale lies that close to the middle of two.  SwiGLU uses the
+// integers with infinity and NaN last.  v / scale costs one division a block,
+// r = 1 / scale: q0 = v * r lies within an ulp of the quotient, and
+// q0 + r * (v - q0 * scale), with both products fused, is the correctly rounded
+// one (r is, too); bf16 values meet the middle of two codes often enough for the
+// last bit to matter.  SwiGLU uses the
 // transcendental units (silu_mul); a block whose maximum is below 2^-60, where
 // their flushed results could matter, is computed again in fp64.
 #include "device_common.h"
@@ -52,11 +54,14 @@ __device__ __forceinline__ uint2 encode8(const Eight& e, uint32_t m, float& scal
   const float amax = __uint_as_float(m);
   float q[8];
   if (amax >= 0x1p-100f) {
-    const float inv = kE4m3Max / amax;
     scale = amax / kE4m3Max;
+    const float r = 1.f / scale;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = e.v[i] * inv;
-  } else {                  // the quotient above would overflow, and the scale may underflow
+    for (int i = 0; i < 8; ++i) {
+      const float q0 = e.v[i] * r;
+      q[i] = fmaf(fmaf(-q0, scale, e.v[i]), r, q0);
+    }
+  } else {                  // the reciprocal would overflow, and the scale may underflow
     const float s = amax / kE4m3Max;
     scale = s > 0.f ? s : 1.f;
 #pragma unroll

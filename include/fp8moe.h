@@ -557,9 +557,7 @@ int moe_grouped_gemm_bf16_ragged(const void* a, const void* b, const int32_t* m_
  *   in    bf16, or fp32 (in_f32 != 0) [M, N], gated [M, 2N]
  *   q     fp8  [M, N]
  *   scale fp32 [M, ceil(N/128)]
- * A block whose v holds an infinity or NaN has codes 0x7F and scale NaN.  The
- * quotient is taken as v * (448 / amax), so a code may differ from the
- * correctly rounded quotient's by one step within 2^-23 of the middle of two.
+ * A block whose v holds an infinity or NaN has codes 0x7F and scale NaN.
  * N is a multiple of 16 (FP8MOE_ERR_ALIGN), at most FP8MOE_MAX_PRODUCT_DIM;
  * M < 2^30 (FP8MOE_ERR_LIMIT); in and q are 16-byte aligned; no overlap
  * (FP8MOE_ERR_SHAPE).  M == 0 launches nothing.
