@@ -35,7 +35,7 @@ struct ProductLds {
   uint8_t *s0, *s1, *s2;
   // s is a constant of the unrolled loops
   __device__ __forceinline__ uint8_t* stage(int s) const { return s == 0 ? s0 : s == 1 ? s1 : s2; }
-  float* scale;    // [2][kPScaleSteps][2 blocks of 128 weight rows][rows]
+  float* scale;    // [2][kPScaleSteps][2 blocks of 128 weight rows][SROW]
   float* bscale;   // [2 blocks][KT]
 };
 
@@ -47,6 +47,13 @@ struct ProductTile {
   static constexpr int WPW = WBLK / kPWaves, APW = (ABLK + kPWaves - 1) / kPWaves;   // of them by each wave
   static constexpr int LPW = WPW + APW;
   static constexpr int kStep = PACKED ? 2048 : kKB;
+
+  // scales of a step and block of weight rows: quads of a lane's sub-tiles,
+  // [wm][quad][l16][4], so that a lane reads four with one load
+  static constexpr int SQ = (TS + 3) / 4, SROW = kPWM * SQ * 64;
+  __device__ static __forceinline__ int scale_at(int wm, int ts, int l16) {
+    return ((wm * SQ + (ts >> 2)) * 16 + l16) * 4 + (ts & 3);
+  }
 
   const ProductArgs& P;
   const ProductLds L;
@@ -100,12 +107,12 @@ struct ProductTile {
 #pragma unroll
       for (int i = 0; i < WPW; ++i)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            wr, (__attribute__((address_space(3))) void*)(L.stage(s) + (wave * WPW + i) * 1024), 16, woff[i],
+            wr, (__attribute__((address_space(3))) void*)(L.stage(s) + ((wave * WPW + i) * 1024)), 16, woff[i],
             k * kStep, 0, 0);
 #pragma unroll
       for (int i = 0; i < APW; ++i)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            ar, (__attribute__((address_space(3))) void*)(L.stage(s) + kPTN * kKB + ablock(wave, i) * 1024), 16,
+            ar, (__attribute__((address_space(3))) void*)(L.stage(s) + (kPTN * kKB + ablock(wave, i) * 1024)), 16,
             aoff[i], k * kKB, 0, 0);
     } else {
       // the last step, where it is short: through registers, zeros past the end
@@ -116,14 +123,14 @@ struct ProductTile {
         const int blk = wave * WPW + i, c = (lane & 7) ^ swz_key(blk * 8 + (lane >> 3));
         const bool live = c * 16 < rem;
         const v4i v = __builtin_amdgcn_raw_buffer_load_b128(wr, live ? woff[i] + k * kKB : 0, 0, 0);
-        *reinterpret_cast<v4i*>(L.stage(s) + blk * 1024 + lane * 16) = live ? v : zero;
+        *reinterpret_cast<v4i*>(L.stage(s) + (blk * 1024 + lane * 16)) = live ? v : zero;
       }
 #pragma unroll
       for (int i = 0; i < APW; ++i) {
         const int blk = ablock(wave, i), c = (lane & 7) ^ swz_key(blk * 8 + (lane >> 3));
         const bool live = c * 16 < rem;
         const v4i v = __builtin_amdgcn_raw_buffer_load_b128(ar, live ? aoff[i] + k * kKB : 0, 0, 0);
-        *reinterpret_cast<v4i*>(L.stage(s) + kPTN * kKB + blk * 1024 + lane * 16) = live ? v : zero;
+        *reinterpret_cast<v4i*>(L.stage(s) + (kPTN * kKB + blk * 1024 + lane * 16)) = live ? v : zero;
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
@@ -141,28 +148,31 @@ struct ProductTile {
   __device__ __forceinline__ void write_scales(int k) {
     const int u = threadIdx.x, pair = u / TM, k0 = k + 2 * pair;
     if (u >= 2 * TM) return;
-    float* d = L.scale + ((k & kPScaleSteps) + 2 * pair) * 2 * TM + (u - pair * TM);
+    const int r = u - pair * TM;
+    float* d = L.scale + ((k & kPScaleSteps) + 2 * pair) * 2 * SROW + scale_at(r / (16 * TS), r / 16 % TS, r & 15);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int blk = 0; blk < 2; ++blk) d[(2 * i + blk) * TM] = sreg[i] * L.bscale[blk * KT + min(k0 + i, KT - 1)];
+      for (int blk = 0; blk < 2; ++blk) d[(2 * i + blk) * SROW] = sreg[i] * L.bscale[blk * KT + min(k0 + i, KT - 1)];
   }
 
   __device__ __forceinline__ void run(const RaggedTile& t) {
     const int g = lane >> 4, l16 = lane & 15, wn = wave % kPWN, wm = wave / kPWN;
     const int wbase = wn * 64 * kKB, abase = kPTN * kKB + wm * TS * 16 * kKB;
-    const int lo = swz(l16, g), hi = swz(l16, g + 4);
+    const int wlo = wbase + (PACKED ? lane * 16 : swz(l16, g));
+    const int whi = wbase + (PACKED ? lane * 16 + 1024 : swz(l16, g + 4));
+    const int alo = abase + swz(l16, g), ahi = abase + swz(l16, g + 4);
     auto wfrag = [&](int s, int b) __attribute__((always_inline)) -> v8i {
-      const uint8_t* p = L.stage(s) + wbase + b * 2048;
-      if constexpr (PACKED)
-        return join(*reinterpret_cast<const v4i*>(p + lane * 16), *reinterpret_cast<const v4i*>(p + 1024 + lane * 16));
-      else return join(*reinterpret_cast<const v4i*>(p + lo), *reinterpret_cast<const v4i*>(p + hi));
+      return join(*reinterpret_cast<const v4i*>(L.stage(s) + (wlo + b * 2048)),
+                  *reinterpret_cast<const v4i*>(L.stage(s) + (whi + b * 2048)));
     };
     auto afrag = [&](int s, int ts) __attribute__((always_inline)) -> v8i {
-      const uint8_t* p = L.stage(s) + abase + ts * 2048;
-      return join(*reinterpret_cast<const v4i*>(p + lo), *reinterpret_cast<const v4i*>(p + hi));
+      return join(*reinterpret_cast<const v4i*>(L.stage(s) + (alo + ts * 2048)),
+                  *reinterpret_cast<const v4i*>(L.stage(s) + (ahi + ts * 2048)));
     };
-    const float* sbase = L.scale + (wn >> 1) * TM + wm * TS * 16 + l16;
+    // offsets are summed up ahead of one addition to the object's address: the
+    // compiler keeps track of which object is read through short chains only
+    const int sbase = (wn >> 1) * SROW + scale_at(wm, 0, l16);
 
     v4f acc[TS][4];
 #pragma unroll
@@ -181,14 +191,14 @@ struct ProductTile {
       }
       if (k + NST - 1 < KT) dma((s + NST - 1) % NST, k + NST - 1);
       v8i w[4], x[2];
-      float sc[TS];
+      v4f sc[SQ];
 #pragma unroll
       for (int b = 0; b < 4; ++b) w[b] = wfrag(s, b);
       x[0] = afrag(s, 0);
       if constexpr (!BF) {
-        const float* sp = sbase + (k & 7) * 2 * TM;
 #pragma unroll
-        for (int ts = 0; ts < TS; ++ts) sc[ts] = sp[ts * 16];
+        for (int q = 0; q < SQ; ++q)
+          sc[q] = *reinterpret_cast<const v4f*>(L.scale + (sbase + (k & 7) * 2 * SROW + q * 64));
       }
       v4f p[2][4];
 #pragma unroll
@@ -209,7 +219,7 @@ struct ProductTile {
             for (int b = 0; b < 4; ++b)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                acc[ts - 1][b][i] = fmaf(p[(ts - 1) & 1][b][i], sc[ts - 1], acc[ts - 1][b][i]);
+                acc[ts - 1][b][i] = fmaf(p[(ts - 1) & 1][b][i], sc[(ts - 1) / 4][(ts - 1) % 4], acc[ts - 1][b][i]);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -219,7 +229,7 @@ struct ProductTile {
         for (int b = 0; b < 4; ++b)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            acc[TS - 1][b][i] = fmaf(p[(TS - 1) & 1][b][i], sc[TS - 1], acc[TS - 1][b][i]);
+            acc[TS - 1][b][i] = fmaf(p[(TS - 1) & 1][b][i], sc[(TS - 1) / 4][(TS - 1) % 4], acc[TS - 1][b][i]);
       }
     };
 
