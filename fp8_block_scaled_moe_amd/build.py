@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libfp8moe.so")
 SOURCES = ["api.cpp", "tile_select.cpp", "route.hip", "gemm1.hip", "gemm2.hip", "gemm1_mx.hip", "gemm2_mx.hip", "gemm1_mxfp4.hip",
            "gemm2_mxfp4.hip", "gemm1_bf16.hip", "gemm2_bf16.hip", "gemm_plain.hip", "fused_small.hip",
            "combine.hip", "gated_act.hip", "pack.hip", "noalloc.hip", "add_rmsnorm.hip", "router.hip", "experts_int8.hip",
-           "experts_int8_tile.hip", "product_stream.hip", "product_tile.hip", "quant_blocks.hip"]
+           "experts_int8_tile.hip", "product_plan.cpp", "product_stream.hip", "product_tile.hip", "quant_blocks.hip"]
 
 ARCH = "gfx950"
 COMMON_FLAGS = [

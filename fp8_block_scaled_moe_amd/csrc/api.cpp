@@ -1149,7 +1149,7 @@ int check_product(int64_t rows, int32_t N, int32_t K, int32_t E, int esize, int3
 // checks first.
 int run_product(const void* a, const float* a_scale, const void* b, const float* b_scale, const void* addend,
                 const int32_t* indptr, int64_t rows, int32_t N, int32_t K, int32_t E, bool bf16, void* out,
-                int32_t out_f32, int32_t weight_layout, void* stream) {
+                int32_t out_f32, void* workspace, size_t workspace_bytes, int32_t weight_layout, void* stream) {
   if (rows == 0) return ok();
   if (!a || !b || !out || (!bf16 && (!a_scale || !b_scale))) return fail(FP8MOE_ERR_NULL, "null tensor argument");
   if (!aligned16(a) || !aligned16(b)) return fail(FP8MOE_ERR_ALIGN, "a and b must be 16-byte aligned");
@@ -1163,6 +1163,12 @@ int run_product(const void* a, const float* a_scale, const void* b, const float*
                             {indptr, ((int64_t)E + 1) * 4}}) ||
       (overlap(out, on, addend, rows * N * 2) && !(addend == out && !out_f32)))
     return fail(FP8MOE_ERR_SHAPE, "out overlaps an input");
+  const size_t need = indptr ? 0 : partial_bytes(rows, N, KT);
+  if (need && (!workspace || workspace_bytes < need || (uintptr_t)workspace % kAlignWs))
+    return fail(FP8MOE_ERR_WORKSPACE, "workspace NULL, not %zu-byte aligned or below %zu bytes", kAlignWs, need);
+  if (need && overlap_any(workspace, (int64_t)need, {{a, rows * kb}, {b, (int64_t)E * N * kb}, {a_scale, rows * KT * 4},
+                                                     {b_scale, sb}, {addend, rows * N * 2}, {out, on}}))
+    return fail(FP8MOE_ERR_SHAPE, "the workspace overlaps a tensor");
   ProductArgs P{};
   P.a = static_cast<const uint8_t*>(a);
   P.a_scale = a_scale;
@@ -1175,12 +1181,14 @@ int run_product(const void* a, const float* a_scale, const void* b, const float*
   P.N = N;
   P.E = E;
   P.kbytes = kb;
-  P.num_cu = device_num_cu();
+  const ProductPlan plan = plan_product(rows, N, KT, indptr ? E : 0, device_num_cu());
+  P.splits = plan.splits;
+  P.partial = static_cast<float*>(workspace);
   P.bf16 = bf16;
   P.packed = weight_layout == FP8MOE_WEIGHTS_MFMA_TILED;
   P.out_f32 = out_f32 != 0;
   P.vec = N % 8 == 0 && aligned16(out) && aligned16(addend);
-  const hipError_t err = launch_product(P, (hipStream_t)stream);
+  const hipError_t err = launch_product(P, plan, (hipStream_t)stream);
   if (err != hipSuccess) return hip_fail(err, "product launch");
   return ok();
 }
@@ -1193,7 +1201,7 @@ int gemm_fp8_blocks_workspace_size(int64_t M, int32_t N, int32_t K, size_t* byte
   const int st = check_product(M, N, K, 1, 1, FP8MOE_WEIGHTS_ROW_MAJOR);
   if (st) return st;
   if (!bytes) return fail(FP8MOE_ERR_NULL, "bytes is null");
-  *bytes = 0;
+  *bytes = partial_bytes(M, N, (K + 127) / 128);
   return ok();
 }
 
@@ -1202,7 +1210,8 @@ int gemm_fp8_blocks(const void* a, const float* a_scale, const void* b, const fl
                     size_t workspace_bytes, int32_t weight_layout, void* stream) {
   const int st = check_product(M, N, K, 1, 1, weight_layout);
   if (st) return st;
-  return run_product(a, a_scale, b, b_scale, addend, nullptr, M, N, K, 1, false, out, out_f32, weight_layout, stream);
+  return run_product(a, a_scale, b, b_scale, addend, nullptr, M, N, K, 1, false, out, out_f32, workspace, workspace_bytes,
+                     weight_layout, stream);
 }
 
 int moe_grouped_gemm_fp8_ragged(const void* a, const float* a_scale, const void* b, const float* b_scale,
@@ -1211,8 +1220,8 @@ int moe_grouped_gemm_fp8_ragged(const void* a, const float* a_scale, const void*
   const int st = check_product(rows, N, K, E, 1, weight_layout);
   if (st) return st;
   if (rows > 0 && !m_indptr) return fail(FP8MOE_ERR_NULL, "null tensor argument");
-  return run_product(a, a_scale, b, b_scale, nullptr, m_indptr, rows, N, K, E, false, out, out_f32, weight_layout,
-                     stream);
+  return run_product(a, a_scale, b, b_scale, nullptr, m_indptr, rows, N, K, E, false, out, out_f32, nullptr, 0,
+                     weight_layout, stream);
 }
 
 int moe_grouped_gemm_bf16_ragged(const void* a, const void* b, const int32_t* m_indptr, int64_t rows, int32_t N,
@@ -1221,8 +1230,8 @@ int moe_grouped_gemm_bf16_ragged(const void* a, const void* b, const int32_t* m_
   const int st = check_product(rows, N, K, E, 2, weight_layout);
   if (st) return st;
   if (rows > 0 && !m_indptr) return fail(FP8MOE_ERR_NULL, "null tensor argument");
-  return run_product(a, nullptr, b, nullptr, nullptr, m_indptr, rows, N, K, E, true, out, out_f32, weight_layout,
-                     stream);
+  return run_product(a, nullptr, b, nullptr, nullptr, m_indptr, rows, N, K, E, true, out, out_f32, nullptr, 0,
+                     weight_layout, stream);
 }
 
 int quant_fp8_blocks(const void* in, int32_t in_f32, int64_t M, int32_t N, int32_t gated, void* q, float* scale,

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 namespace fp8moe {
@@ -21,13 +22,29 @@ struct ProductArgs {
   int64_t rows;
   int N, E;
   int kbytes;              // bytes of a row of a or b, a multiple of 16; KT = ceil(kbytes / 128) steps
-  int num_cu;
+  int splits;              // parts of K whose sums go to `partial` [splits][rows][N]; 1: straight to out
+  float* partial;
   bool bf16, packed, out_f32, vec;
 };
 
-hipError_t launch_product(const ProductArgs& P, hipStream_t stream);
-// The tile kernel, of up to tile_m (128 or 256) rows a tile.
-hipError_t launch_product_tile(const ProductArgs& P, int tile_m, hipStream_t stream);
+// How a product is run: the streaming kernel with 16 sub_tiles rows a tile, or
+// a tile kernel (weight rows x rows of a), in `splits` parts of K.
+enum ProductShape { kStream, kTile256x256, kTile256x128, kTile128x128, kTile128x64 };
+struct ProductPlan {
+  ProductShape shape;
+  int sub_tiles, splits;
+};
+// E == 0: dense.  rows, N, K steps of 128 bytes.
+ProductPlan plan_product(int64_t rows, int N, int steps, int E, int num_cu);
+// Bytes of the parts' sums, never fewer for more rows.
+size_t partial_bytes(int64_t rows, int N, int steps);
+
+// Runs P (splits and partial as the plan says).
+hipError_t launch_product(const ProductArgs& P, const ProductPlan& plan, hipStream_t stream);
+
+hipError_t launch_product_stream(const ProductArgs& P, int sub_tiles, hipStream_t stream);
+hipError_t launch_product_tile(const ProductArgs& P, ProductShape shape, hipStream_t stream);
+hipError_t launch_product_join(const ProductArgs& P, hipStream_t stream);
 
 // v = in, or silu(gate) * up of in's two halves; per row and 128 columns
 // scale = amax / 448, q = e4m3(v / scale).

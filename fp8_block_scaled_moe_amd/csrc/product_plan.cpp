@@ -1,0 +1,112 @@
+// Which kernel runs a product, and in how many parts of K: a model of the
+// kernels' times, fitted to sweeps on one MI355X.  It compares kernels with one
+// another; what it leaves out (the rate of memory) is alike for all of them.
+#include <math.h>
+
+#include "launch_products.h"
+
+namespace fp8moe {
+
+namespace {
+
+constexpr int kMaxSplits = 8;
+constexpr size_t kMaxPartial = (size_t)16 << 20;   // the parts' sums stay in the last-level cache
+
+// us of a K step of one workgroup with TS sub-tiles a wave (base + per * TS), of
+// a round's start and end, and how many workgroups share a CU, each then taking
+// `shared` times as long.  Dense products, row-major, us (model | 256 x 256, 256 x
+// 128, 128 x 128, 128 x 64 measured):
+//   8192 x 4096 x 7168: 250, 287, 321, 437 | 253, 285, 290, 351
+//   2048 x 4096 x 7168: 127, 75, 83, 110 | 110, 77, 77, 95
+//   1111 x 4096 x 7168: 110, 75, 72, 64 | 104, 63, 65, 73
+//   4096 x 7168 x 2048: 81, 92, 88, 114 | 81, 92, 90, 108
+//   512 x 7168 x 2048:  43, 26, 23, 20 | 37, 23, 20, 18.5
+//   512 x 1500 x 7168:  127, 75, 65, 41 | 129, 77, 65, 38
+struct TileCost {
+  ProductShape shape;
+  int tn, tm, wm, per_cu;
+  float base, per, shared, ends;
+};
+constexpr TileCost kTiles[] = {
+    {kTile128x64, 128, 64, 2, 2, 0.43f, 0.10f, 1.5f, 1.0f},
+    {kTile128x128, 128, 128, 2, 2, 0.72f, 0.085f, 1.3f, 2.0f},
+    {kTile256x128, 256, 128, 2, 1, 0.62f, 0.15f, 1.0f, 2.5f},
+    {kTile256x256, 256, 256, 2, 1, 0.75f, 0.17f, 1.0f, 5.0f},
+};
+constexpr float kLaunch = 4.f;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// `groups` groups of `share` rows each
+float tile_us(const TileCost& c, int64_t groups, int64_t share, int N, int steps, int splits, int num_cu) {
+  const int64_t cut = ceil_div(share, c.tm), ts = ceil_div(ceil_div(share, cut), 16 * c.wm);
+  const float tiles = (float)(groups * cut * ceil_div(N, c.tn) * splits), cus = (float)num_cu;
+  float step = c.base + c.per * ts, rounds;
+  if (c.per_cu == 1) {
+    rounds = ceilf(tiles / cus);
+  } else {
+    step *= 1.f + (c.shared - 1.f) * fminf(1.f, fmaxf(0.f, tiles / cus - 1.f));
+    rounds = fmaxf(1.f, tiles / (2 * cus));
+  }
+  return kLaunch + rounds * (ceil_div(steps, splits) * step + c.ends);
+}
+
+// writing the parts' sums, reading them, and the launch between
+float join_us(int64_t rows, int N, int splits) { return splits > 1 ? 3.f + 2e-6f * splits * rows * N : 0.f; }
+
+}  // namespace
+
+size_t partial_bytes(int64_t rows, int N, int steps) {
+  if (steps < 8 || rows == 0) return 0;
+  const size_t n = (size_t)(rows < (int64_t)kMaxPartial ? rows : (int64_t)kMaxPartial) * ((N + 7) & ~7) * sizeof(float) *
+                   kMaxSplits;
+  return n < kMaxPartial ? (n + 255) / 256 * 256 : kMaxPartial;
+}
+
+ProductPlan plan_product(int64_t rows, int N, int steps, int E, int num_cu) {
+  const bool grouped = E > 0;
+  const int64_t groups = grouped ? (rows < E ? rows : E) : 1;
+  int64_t share = ceil_div(rows, groups);
+  const int64_t small = groups * ceil_div(N, 128);   // workgroups of 128 x 64 tiles where each group is one
+  // Groups of a few rows: streaming where weights are read once for them, or
+  // tiles would be few.  128 groups, 1536 x 2048, tiled, us, streaming | 128 x 64:
+  // 4 rows 69, 71, 12 rows 77, 74, 24 rows 106, 78; 2 rows in bf16 67, 79; 8
+  // groups of 4 rows, 4096 x 4096: 27, 28.
+  if (grouped && (share <= 4 || (share <= 16 && small < num_cu))) return {kStream, 1, 1};
+  if (grouped) share += (int64_t)sqrt((double)share);   // rows that chance puts on some of the groups
+  auto fits = [&](int s) {
+    return s == 1 || (!grouped && steps >= 8 * s && (size_t)rows * ((N + 7) & ~7) * s * sizeof(float) <= kMaxPartial);
+  };
+  ProductPlan best{kTile256x256, 0, 1};
+  float us = 1e30f;
+  for (const TileCost& c : kTiles) {
+    // tiles are numbered in 31 bits (256 x 256 ones of 2^30 rows and 2^16 columns fit)
+    if ((rows / c.tm + groups + 1) * ceil_div(N, c.tn) >= (int64_t)1 << 31) continue;
+    for (int s = 1; s <= (c.shape == kTile128x64 ? kMaxSplits : 1); s *= 2) {
+      if (!fits(s)) continue;
+      const float t = tile_us(c, groups, share, N, steps, s, num_cu) + join_us(rows, N, s);
+      if (t < us) us = t, best = {c.shape, 0, s};
+    }
+  }
+  if (grouped || rows > 1024) return best;
+  // Streaming: a step of 32 weight rows by 16 TS takes a CU 0.09 + 0.09 TS us, and
+  // a workgroup alone on its CU no less than half that a step of its eight waves.
+  const int64_t cut = ceil_div(rows, 64);
+  const int ts = (int)ceil_div(ceil_div(rows, cut), 16);
+  for (int s = 1; s <= kMaxSplits; s *= 2) {
+    if (!fits(s)) continue;
+    const float wgs = (float)(cut * ceil_div(N, 32) * s), work = ceil_div(steps, s) * (0.09f + 0.09f * ts);
+    const float t = kLaunch + fmaxf(1.f, wgs / num_cu) * work + join_us(rows, N, s);
+    if (t < us) us = t, best = {kStream, ts, s};
+  }
+  return best;
+}
+
+hipError_t launch_product(const ProductArgs& P, const ProductPlan& plan, hipStream_t stream) {
+  const hipError_t err = plan.shape == kStream ? launch_product_stream(P, plan.sub_tiles, stream)
+                                               : launch_product_tile(P, plan.shape, stream);
+  if (err != hipSuccess || P.splits == 1) return err;
+  return launch_product_join(P, stream);
+}
+
+}  // namespace fp8moe

@@ -63,12 +63,14 @@ __global__ __launch_bounds__(64 * NW) void product_stream_kernel(const ProductAr
       }
   };
 
-  for (int k0 = wave; k0 < KF; k0 += NW * U) {
+  // this split's steps: every NW * splits-th from the wave's own on
+  const int stride = NW * P.splits, mine = NW * (int)blockIdx.z + wave;
+  for (int k0 = mine; k0 < KF; k0 += stride * U) {
     v8i w[U][B], x[U][TS];
     float s[U][TS];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = k0 + u * NW;
+      const int k = k0 + u * stride;
       if (k < KF) {
 #pragma unroll
         for (int b = 0; b < B; ++b)
@@ -84,11 +86,11 @@ __global__ __launch_bounds__(64 * NW) void product_stream_kernel(const ProductAr
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (k0 + u * NW < KF) product(w[u], x[u], s[u]);
+      if (k0 + u * stride < KF) product(w[u], x[u], s[u]);
   }
   // the last step, where it is short: a lane whose 16 bytes lie past the end
   // reads the row's first and takes zeros on both sides (row-major only)
-  if (!PACKED && KF < KT && wave == KF % NW) {
+  if (!PACKED && KF < KT && mine == KF % stride) {
     const v4i zero = {0, 0, 0, 0};
     const int rem = kb - KF * kKB;
     const bool lo = 16 * g < rem, hi = 64 + 16 * g < rem;
@@ -117,44 +119,88 @@ __global__ __launch_bounds__(64 * NW) void product_stream_kernel(const ProductAr
     for (int b = 0; b < B; ++b) red[wave][16 * ts + l16][4 * b + g] = acc[ts][b];
   __syncthreads();
   for (int u = threadIdx.x; u < TM * 2 * B; u += 64 * NW) {
-    const int r = u / (2 * B), c = u % (2 * B);
+    const int r = u / (2 * B), c = u % (2 * B), n = n0 + 8 * c;
+    uint4 add = {};
+    if (P.splits == 1 && P.addend && P.vec && r < t.h && n < P.N)
+      add = *reinterpret_cast<const uint4*>(P.addend + ((int64_t)t.row0 + r) * P.N + n);
     v4f lo = red[0][r][2 * c], hi = red[0][r][2 * c + 1];
 #pragma unroll
     for (int w = 1; w < NW; ++w) {
       lo += red[w][r][2 * c];
       hi += red[w][r][2 * c + 1];
     }
-    if (r < t.h) store_out8(P, (int64_t)t.row0 + r, n0 + 8 * c, lo, hi);
+    if (r >= t.h) continue;
+    if (P.splits == 1) store_out8(P, (int64_t)t.row0 + r, n, lo, hi, add);
+    else store_partial8(P, t.row0 + r, n, lo, hi);
   }
+}
+
+// out = the splits' sums in ascending order (+ addend), eight columns a thread.
+constexpr int kJoinThreads = 256;
+__global__ __launch_bounds__(kJoinThreads) void product_join_kernel(const ProductArgs P) {
+  const int NP = (P.N + 7) & ~7, per = NP / 8;
+  const int u = (int)blockIdx.x * kJoinThreads + (int)threadIdx.x;
+  if (u >= (int)P.rows * per) return;
+  const int row = u / per, n = 8 * (u - row * per);
+  uint4 add = {};
+  if (P.addend && P.vec) add = *reinterpret_cast<const uint4*>(P.addend + (int64_t)row * P.N + n);
+  const float* p = P.partial + (int64_t)row * NP + n;   // rows padded to whole groups of eight columns
+  const int64_t next = P.rows * NP;
+  v4f lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+#pragma unroll 4
+  for (int s = 0; s < P.splits; ++s) {
+    lo += *reinterpret_cast<const v4f*>(p + s * next);
+    hi += *reinterpret_cast<const v4f*>(p + s * next + 4);
+  }
+  store_out8(P, row, n, lo, hi, add);
 }
 
 namespace {
 
-template <int TS, int B, int NW, int U, bool BF>
+// Weight rows, waves and steps in flight of a workgroup.  Dense, few rows, us,
+// MFMA-tiled unless said (16 rows x 4 waves, 16 x 8, 16 x 16, 32 x 4, 32 x 8;
+// with S parts of K), N x K:
+//   7168 x 2048:   M=1: 6.0, 5.7, 7.3, 6.2, 5.8   M=64: 15.3, 16.2, 20.5, 11.2, 10.7 (S=2: 15.3)
+//   4096 x 7168:   M=16: 12.5, 10.4, 10.7, 13.4, 12.1 (S=2: 11.8)   M=64: 24, 24, 28, 28, 26 (S=2: 20.6)
+//   1500 x 7168, row-major:  M=1: 12.5, 8.7, 8.8, 15.5, 11.9 (S=4: 8.4)   M=33: 18, 18, 18, 22, 22 (S=4: 12.2)
+//   512 x 7168:    M=33: 14, 14, 15, 15, 15 (S=8: 8.2)
+//   7168 x 16384:  M=1: 31.8, 26.0, 25.9, 31.5, 23.4   M=64: 94, 95, 111, 59, 55
+// Grouped, where weights of many groups stream by (256 groups of 2 rows, 4096 x
+// 7168): 32 x 4 1052, 32 x 8 1036; with more rows four waves are ahead (12 rows
+// of each of 128 groups, 1536 x 2048: 77 and 98).
+template <int TS, int NW, bool BF>
 hipError_t launch_stream(const ProductArgs& P, hipStream_t stream) {
+  constexpr int B = 2, U = TS <= 2 ? 4 : 2;
   const int64_t NT = (P.N + 16 * B - 1) / (16 * B);
   const int64_t tiles = P.indptr ? P.rows / (16 * TS) + (P.rows < P.E ? P.rows : P.E) : (P.rows + 16 * TS - 1) / (16 * TS);
   if (tiles * NT >= (int64_t)1 << 31) return hipErrorInvalidValue;
-  const dim3 grid = wide_grid((tiles * NT + kNumXcd - 1) / kNumXcd * kNumXcd), block(64 * NW);
+  dim3 grid = wide_grid((tiles * NT + kNumXcd - 1) / kNumXcd * kNumXcd);
+  const dim3 block(64 * NW);
+  grid.z = P.splits;
   if (P.packed) hipLaunchKernelGGL((product_stream_kernel<TS, B, NW, U, BF, true>), grid, block, 0, stream, P);
   else hipLaunchKernelGGL((product_stream_kernel<TS, B, NW, U, BF, false>), grid, block, 0, stream, P);
   return hipGetLastError();
 }
 
-template <bool BF>
-hipError_t launch_rows(const ProductArgs& P, hipStream_t stream) {
-  const int64_t groups = P.rows < P.E ? P.rows : P.E, share = (P.rows + groups - 1) / groups;
-  if (share <= 16) return launch_stream<1, 2, 4, 4, BF>(P, stream);
-  if (share <= 32) return launch_stream<2, 2, 4, 4, BF>(P, stream);
-  return launch_stream<4, 2, 4, 2, BF>(P, stream);
-}
-
 }  // namespace
 
-hipError_t launch_product(const ProductArgs& P, hipStream_t stream) {
-  const int64_t groups = P.rows < P.E ? P.rows : P.E, share = (P.rows + groups - 1) / groups;
-  if (share > 16) return launch_product_tile(P, share > 128 ? 256 : 128, stream);
-  return P.bf16 ? launch_rows<true>(P, stream) : launch_rows<false>(P, stream);
+hipError_t launch_product_stream(const ProductArgs& P, int sub_tiles, hipStream_t stream) {
+  if (P.bf16)
+    return sub_tiles == 1 ? launch_stream<1, 4, true>(P, stream) : hipErrorInvalidValue;
+  if (P.indptr) return sub_tiles == 1 ? launch_stream<1, 4, false>(P, stream) : hipErrorInvalidValue;
+  switch (sub_tiles) {
+    case 1: return launch_stream<1, 8, false>(P, stream);
+    case 2: return launch_stream<2, 8, false>(P, stream);
+    case 3: return launch_stream<3, 8, false>(P, stream);
+    default: return launch_stream<4, 8, false>(P, stream);
+  }
+}
+
+hipError_t launch_product_join(const ProductArgs& P, hipStream_t stream) {
+  const int64_t u = P.rows * ((P.N + 7) / 8);
+  hipLaunchKernelGGL(product_join_kernel, dim3((unsigned)((u + kJoinThreads - 1) / kJoinThreads)), dim3(kJoinThreads), 0,
+                     stream, P);
+  return hipGetLastError();
 }
 
 }  // namespace fp8moe

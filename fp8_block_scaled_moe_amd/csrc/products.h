@@ -141,14 +141,14 @@ __device__ __forceinline__ bool ragged_tile(const ProductArgs& P, int TM, int NT
 
 // Eight consecutive columns n .. n + 7 of row `row`, the addend added first.
 // vec: N % 8 == 0 and aligned tensors, so that groups of eight columns lie
-// inside or outside a row as a whole, on 16-byte boundaries.
-__device__ __forceinline__ void store_out8(const ProductArgs& P, int64_t row, int n, v4f lo, v4f hi) {
+// inside or outside a row as a whole, on 16-byte boundaries; the caller has
+// then read the addend's, which may be out's own.
+__device__ __forceinline__ void store_out8(const ProductArgs& P, int64_t row, int n, v4f lo, v4f hi, const uint4& d) {
   if (n >= P.N) return;
   const int64_t at = row * P.N + n;
   float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   if (P.vec) {
     if (P.addend) {
-      const uint4 d = *reinterpret_cast<const uint4*>(P.addend + at);
       const uint32_t w[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -176,6 +176,15 @@ __device__ __forceinline__ void store_out8(const ProductArgs& P, int64_t row, in
     if (P.out_f32) static_cast<float*>(P.out)[at + i] = y;
     else static_cast<uint16_t*>(P.out)[at + i] = (uint16_t)pack2_bf16(y, y);
   }
+}
+
+// The same eight columns of this part of K's sums, for the join; rows there
+// are padded to whole groups of eight columns.
+__device__ __forceinline__ void store_partial8(const ProductArgs& P, int row, int n, v4f lo, v4f hi) {
+  if (n >= P.N) return;
+  v4f* o = reinterpret_cast<v4f*>(P.partial + (((int64_t)blockIdx.z * P.rows + row) * ((P.N + 7) & ~7) + n));
+  o[0] = lo;
+  o[1] = hi;
 }
 
 }  // namespace fp8moe
