@@ -22,6 +22,11 @@ constexpr size_t kMaxPartial = (size_t)16 << 20;   // the parts' sums stay in th
 //   4096 x 7168 x 2048: 81, 92, 88, 114 | 81, 92, 90, 108
 //   512 x 7168 x 2048:  43, 26, 23, 20 | 37, 23, 20, 18.5
 //   512 x 1500 x 7168:  127, 75, 65, 41 | 129, 77, 65, 38
+// grouped, MFMA-tiled:
+//   256 groups of 256 rows, 7168 x 2048: 1403, 1545, 1686, 2000 | 1430, 1599, 1637, 1956
+//   128 of 256, 1536 x 2048: 170, 180, 184, 236 | 174, 188, 181, 218
+//   128 of 100, 1536 x 2048: 88, 70, 76, 101 | 99, 98, 97, 111 (its weights alone take 75)
+//   8 of 160, 4096 x 4096:   60, 41, 46, 51 | 60, 47, 47, 55
 struct TileCost {
   ProductShape shape;
   int tn, tm, wm, per_cu;
@@ -37,16 +42,20 @@ constexpr float kLaunch = 4.f;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// `groups` groups of `share` rows each
+// `groups` groups of about `share` rows each.  Chance gives some of them more
+// rows than the average: where the average comes near a tile's height they need
+// one tile more, on average a half.
 float tile_us(const TileCost& c, int64_t groups, int64_t share, int N, int steps, int splits, int num_cu) {
-  const int64_t cut = ceil_div(share, c.tm), ts = ceil_div(ceil_div(share, cut), 16 * c.wm);
-  const float tiles = (float)(groups * cut * ceil_div(N, c.tn) * splits), cus = (float)num_cu;
+  float cut = (float)ceil_div(share, c.tm);
+  if (groups > 1 && share + 2 * sqrtf((float)share) > c.tm) cut = fmaxf(1.f, (float)share / c.tm + 0.5f);
+  const float ts = fminf((float)(c.tm / (16 * c.wm)), ceilf(share / cut / (16 * c.wm)));
+  const float tiles = groups * cut * ceil_div(N, c.tn) * splits, cus = (float)num_cu;
   float step = c.base + c.per * ts, rounds;
   if (c.per_cu == 1) {
     rounds = ceilf(tiles / cus);
   } else {
     step *= 1.f + (c.shared - 1.f) * fminf(1.f, fmaxf(0.f, tiles / cus - 1.f));
-    rounds = fmaxf(1.f, tiles / (2 * cus));
+    rounds = fmaxf(1.f, ceilf(tiles / cus) / 2);
   }
   return kLaunch + rounds * (ceil_div(steps, splits) * step + c.ends);
 }
@@ -66,14 +75,13 @@ size_t partial_bytes(int64_t rows, int N, int steps) {
 ProductPlan plan_product(int64_t rows, int N, int steps, int E, int num_cu) {
   const bool grouped = E > 0;
   const int64_t groups = grouped ? (rows < E ? rows : E) : 1;
-  int64_t share = ceil_div(rows, groups);
+  const int64_t share = ceil_div(rows, groups);
   const int64_t small = groups * ceil_div(N, 128);   // workgroups of 128 x 64 tiles where each group is one
   // Groups of a few rows: streaming where weights are read once for them, or
   // tiles would be few.  128 groups, 1536 x 2048, tiled, us, streaming | 128 x 64:
   // 4 rows 69, 71, 12 rows 77, 74, 24 rows 106, 78; 2 rows in bf16 67, 79; 8
   // groups of 4 rows, 4096 x 4096: 27, 28.
   if (grouped && (share <= 4 || (share <= 16 && small < num_cu))) return {kStream, 1, 1};
-  if (grouped) share += (int64_t)sqrt((double)share);   // rows that chance puts on some of the groups
   auto fits = [&](int s) {
     return s == 1 || (!grouped && steps >= 8 * s && (size_t)rows * ((N + 7) & ~7) * s * sizeof(float) <= kMaxPartial);
   };

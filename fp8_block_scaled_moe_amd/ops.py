@@ -819,10 +819,13 @@ def _blocks(n):
 
 
 def _fp8(t, name, ndim):
-    """An e4m3 tensor (float8_e4m3fn or uint8 codes) of this many dims."""
-    t = _u8(t) if isinstance(t, torch.Tensor) else t
-    _need(t, torch.uint8, name, ndim)
-    return t
+    """t is a contiguous device tensor of e4m3 codes (float8_e4m3fn or uint8) of this many dims."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.float8_e4m3fn:
+        _need(t, torch.uint8, name, ndim)
+    elif not (t.is_cuda and t.is_contiguous() and t.dim() == ndim):
+        _need(t, t.dtype, name, ndim)
 
 
 def _out_dtype(out, dtype):
@@ -849,11 +852,12 @@ def gemm_fp8_blocks(a, a_scale, b, b_scale, addend=None, out=None, out_dtype=tor
     [M, ceil(K/128)], b e4m3 with b_scale fp32 [ceil(N/128), ceil(K/128)], addend bf16 [M, N] (may be out).
     Returns out [M, N], bf16 or fp32 (out_dtype, or the type of a given out).  weight_layout 1: b packed by
     pack_weights (as [1, N, K])."""
-    a, b = _fp8(a, "a", 2), _fp8(b, "b", 2)
+    _fp8(a, "a", 2)
+    _fp8(b, "b", 2)
     M, K = a.shape
     N = b.shape[0]
     index = a.get_device()
-    _check(b, torch.uint8, (N, K), index, "b")
+    _check(b, b.dtype, (N, K), index, "b")
     _check(a_scale, torch.float32, (M, _blocks(K)), index, "a_scale")
     _check(b_scale, torch.float32, (_blocks(N), _blocks(K)), index, "b_scale")
     if addend is not None:
@@ -875,7 +879,7 @@ def _ragged(a, b, m_indptr, out, out_dtype):
     rows, K = a.shape
     E, N, _ = b.shape
     index = a.get_device()
-    _check(b, a.dtype, (E, N, K), index, "b")
+    _check(b, b.dtype, (E, N, K), index, "b")
     _check(m_indptr, torch.int32, (E + 1,), index, "m_indptr")
     dtype = _out_dtype(out, out_dtype)
     if out is None:      # rows of no group are not written
@@ -891,7 +895,8 @@ def grouped_gemm_fp8_ragged(a, a_scale, b, b_scale, m_indptr, out=None, out_dtyp
     e4m3 [rows, K] (a_scale fp32 [rows, ceil(K/128)]) times b[e]^T, b e4m3 [E, N, K] with b_scale fp32
     [E, ceil(N/128), ceil(K/128)], m_indptr int32 [E+1].  Returns out [rows, N], bf16 or fp32; rows of no
     group are not written (zero when out is allocated here).  weight_layout 1: b packed by pack_weights."""
-    a, b = _fp8(a, "a", 2), _fp8(b, "b", 3)
+    _fp8(a, "a", 2)
+    _fp8(b, "b", 3)
     rows, N, K, E, index, out, f32 = _ragged(a, b, m_indptr, out, out_dtype)
     _check(a_scale, torch.float32, (rows, _blocks(K)), index, "a_scale")
     _check(b_scale, torch.float32, (E, _blocks(N), _blocks(K)), index, "b_scale")
