@@ -106,3 +106,14 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         fm.quant_fp8_blocks(torch.zeros(4, 128))
     with pytest.raises(TypeError):
         fm.quant_fp8_blocks(torch.zeros(4, 128, dtype=torch.float16))
+
+
+def test_gemm_workspace_serves_smaller_batches():
+    """The size never falls as M grows and stays bounded; calls refuse a smaller, missing or unaligned one."""
+    for N, K in ((576, 7168), (7168, 2048), (1, 65536), (65536, 128)):
+        sizes = [fm.gemm_workspace_size(M, N, K) for M in (0, 1, 2, 16, 33, 64, 200, 1000, 5000, 100000, (1 << 30) - 1)]
+        assert sizes == sorted(sizes) and sizes[-1] <= 16 << 20
+    need = fm.gemm_workspace_size(4, 24, 2048)
+    assert need > 0 and need % 256 == 0
+    assert gemm(K=2048, ws=NULL) == E_WS and gemm(K=2048, wsb=need - 1) == E_WS and gemm(K=2048, ws=P(5, 128)) == E_WS
+    assert gemm(K=2048, ws=P(0)) == E_SHAPE and gemm(K=2048, ws=P(4)) == E_SHAPE and gemm(K=2048, add=P(5)) == E_SHAPE
