@@ -29,7 +29,8 @@ struct ProductArgs {
 
 // How a product is run: the streaming kernel with 16 sub_tiles rows a tile, or
 // a tile kernel (weight rows x rows of a), in `splits` parts of K.
-enum ProductShape { kStream, kTile256x256, kTile256x128, kTile128x128, kTile128x64 };
+// (kTile128x128x8: with eight waves, alone on its CU.)
+enum ProductShape { kStream, kTile256x256, kTile256x128, kTile128x128, kTile128x128x8, kTile128x64 };
 struct ProductPlan {
   ProductShape shape;
   int sub_tiles, splits;

@@ -15,13 +15,15 @@ constexpr size_t kMaxPartial = (size_t)16 << 20;   // the parts' sums stay in th
 // us of a K step of one workgroup with TS sub-tiles a wave (base + per * TS), of
 // a round's start and end, and how many workgroups share a CU, each then taking
 // `shared` times as long.  Dense products, row-major, us (model | 256 x 256, 256 x
-// 128, 128 x 128, 128 x 64 measured):
+// 128, 128 x 128, 128 x 64 measured; then 128 x 128 of eight waves):
 //   8192 x 4096 x 7168: 250, 287, 321, 437 | 253, 285, 290, 351
 //   2048 x 4096 x 7168: 127, 75, 83, 110 | 110, 77, 77, 95
 //   1111 x 4096 x 7168: 110, 75, 72, 64 | 104, 63, 65, 73
 //   4096 x 7168 x 2048: 81, 92, 88, 114 | 81, 92, 90, 108
-//   512 x 7168 x 2048:  43, 26, 23, 20 | 37, 23, 20, 18.5
+//   512 x 7168 x 2048:  43, 26, 23, 20 | 37, 23, 20, 18.5; 17.5 | 16.9
 //   512 x 1500 x 7168:  127, 75, 65, 41 | 129, 77, 65, 38
+//   2048 x 1500 x 7168: 127, 75, 67, 52 | 130, 76, 65, 52; 46 | 49
+//   1111 x 2000 x 1936: 43, 26, 23, 19 | 36, 24, 20, 18; 17.5 | 16.2
 // grouped, MFMA-tiled:
 //   256 groups of 256 rows, 7168 x 2048: 1403, 1545, 1686, 2000 | 1430, 1599, 1637, 1956
 //   128 of 256, 1536 x 2048: 170, 180, 184, 236 | 174, 188, 181, 218
@@ -34,6 +36,7 @@ struct TileCost {
 };
 constexpr TileCost kTiles[] = {
     {kTile128x64, 128, 64, 2, 2, 0.43f, 0.10f, 1.5f, 1.0f},
+    {kTile128x128x8, 128, 128, 4, 1, 0.44f, 0.14f, 1.0f, 2.0f},
     {kTile128x128, 128, 128, 2, 2, 0.72f, 0.085f, 1.3f, 2.0f},
     {kTile256x128, 256, 128, 2, 1, 0.62f, 0.15f, 1.0f, 2.5f},
     {kTile256x256, 256, 256, 2, 1, 0.75f, 0.17f, 1.0f, 5.0f},
@@ -54,7 +57,7 @@ float tile_us(const TileCost& c, int64_t groups, int64_t share, int N, int steps
   if (c.per_cu == 1) {
     rounds = ceilf(tiles / cus);
   } else {
-    step *= 1.f + (c.shared - 1.f) * fminf(1.f, fmaxf(0.f, tiles / cus - 1.f));
+    if (tiles > cus) step *= 1.f + (c.shared - 1.f) * (0.5f + 0.5f * fminf(1.f, tiles / cus - 1.f));
     rounds = fmaxf(1.f, ceilf(tiles / cus) / 2);
   }
   return kLaunch + rounds * (ceil_div(steps, splits) * step + c.ends);
@@ -90,7 +93,7 @@ ProductPlan plan_product(int64_t rows, int N, int steps, int E, int num_cu) {
   for (const TileCost& c : kTiles) {
     // tiles are numbered in 31 bits (256 x 256 ones of 2^30 rows and 2^16 columns fit)
     if ((rows / c.tm + groups + 1) * ceil_div(N, c.tn) >= (int64_t)1 << 31) continue;
-    for (int s = 1; s <= (c.shape == kTile128x64 ? kMaxSplits : 1); s *= 2) {
+    for (int s = 1; s <= (c.shape == kTile128x64 || c.shape == kTile128x128x8 ? kMaxSplits : 1); s *= 2) {
       if (!fits(s)) continue;
       const float t = tile_us(c, groups, share, N, steps, s, num_cu) + join_us(rows, N, s);
       if (t < us) us = t, best = {c.shape, 0, s};
@@ -104,7 +107,7 @@ ProductPlan plan_product(int64_t rows, int N, int steps, int E, int num_cu) {
   for (int s = 1; s <= kMaxSplits; s *= 2) {
     if (!fits(s)) continue;
     const float wgs = (float)(cut * ceil_div(N, 32) * s), work = ceil_div(steps, s) * (0.09f + 0.09f * ts);
-    const float t = kLaunch + fmaxf(1.f, wgs / num_cu) * work + join_us(rows, N, s);
+    const float t = kLaunch + ceilf(wgs / num_cu) * work + join_us(rows, N, s);
     if (t < us) us = t, best = {kStream, ts, s};
   }
   return best;

@@ -20,7 +20,6 @@ struct ProductTile {
   static constexpr int WPW = WBLK / S::Waves, APW = (ABLK + S::Waves - 1) / S::Waves;   // of them by each wave
   static constexpr int LPW = WPW + APW;
   static constexpr int XN = 3;   // fragments of rows held
-  static_assert(S::OutBytes <= S::Stage, "the sums of 16 rows fit a buffer");
   static_assert((NST - 2) * LPW < 64, "vmcnt is a 6-bit counter");
 
   const ProductArgs& P;
@@ -200,7 +199,8 @@ struct ProductTile {
 
 template <typename S, bool BF, bool PACKED>
 __global__ __launch_bounds__(S::Threads) void product_tile_kernel(const ProductArgs P) {
-  __shared__ __attribute__((aligned(16))) uint8_t s0[S::Stage], s1[S::Stage];
+  __shared__ __attribute__((aligned(16))) uint8_t s0[S::OutBytes > S::Stage ? S::OutBytes : S::Stage];
+  __shared__ __attribute__((aligned(16))) uint8_t s1[S::Stage];
   __shared__ __attribute__((aligned(16))) uint8_t s2[S::NST > 2 ? S::Stage : 16], s3[S::NST > 3 ? S::Stage : 16];
   __shared__ __attribute__((aligned(16))) float sc[BF ? 4 : S::ScaleFloats];
   __shared__ float sb[BF ? 4 : S::BScaleFloats];
@@ -235,6 +235,7 @@ hipError_t launch_product_tile(const ProductArgs& P, ProductShape shape, hipStre
     case kTile256x256: return run(TileShape<4, 2, 8, 2>{});
     case kTile256x128: return run(TileShape<4, 2, 4, 3>{});
     case kTile128x128: return run(TileShape<2, 2, 4, 2>{});
+    case kTile128x128x8: return run(TileShape<2, 4, 2, 3>{});
     default: return run(TileShape<2, 2, 2, 3>{});
   }
 }
