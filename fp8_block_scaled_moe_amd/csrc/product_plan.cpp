@@ -9,7 +9,7 @@ namespace fp8moe {
 
 namespace {
 
-constexpr int kMaxSplits = 8;
+constexpr int kMaxSplits = 8, kPartSteps = 8;      // parts of K, and the fewest steps of one
 constexpr size_t kMaxPartial = (size_t)16 << 20;   // the parts' sums stay in the last-level cache
 
 // us of a K step of one workgroup with TS sub-tiles a wave (base + per * TS), of
@@ -69,7 +69,7 @@ float join_us(int64_t rows, int N, int splits) { return splits > 1 ? 3.f + 2e-6f
 }  // namespace
 
 size_t partial_bytes(int64_t rows, int N, int steps) {
-  if (steps < 8 || rows == 0) return 0;
+  if (steps < 2 * kPartSteps || rows == 0) return 0;
   const size_t n = (size_t)(rows < (int64_t)kMaxPartial ? rows : (int64_t)kMaxPartial) * ((N + 7) & ~7) * sizeof(float) *
                    kMaxSplits;
   return n < kMaxPartial ? (n + 255) / 256 * 256 : kMaxPartial;
@@ -86,7 +86,7 @@ ProductPlan plan_product(int64_t rows, int N, int steps, int E, int num_cu) {
   // groups of 4 rows, 4096 x 4096: 27, 28.
   if (grouped && (share <= 4 || (share <= 16 && small < num_cu))) return {kStream, 1, 1};
   auto fits = [&](int s) {
-    return s == 1 || (!grouped && steps >= 8 * s && (size_t)rows * ((N + 7) & ~7) * s * sizeof(float) <= kMaxPartial);
+    return s == 1 || (!grouped && steps >= kPartSteps * s && (size_t)rows * ((N + 7) & ~7) * s * sizeof(float) <= kMaxPartial);
   };
   ProductPlan best{kTile256x256, 0, 1};
   float us = 1e30f;

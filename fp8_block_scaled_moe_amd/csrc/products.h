@@ -97,9 +97,12 @@ __device__ __forceinline__ bool ragged_tile(const ProductArgs& P, int TM, int NT
     if (slot >= per || L >= items) return false;
     const int want = (int)(L / NT);      // the group that holds tile `want` holds item L
     int base = 0, c = 0;
-    while (base + ch.total <= want) {    // want < tot: this stops at a chunk of the groups
+    // want < tot, so this stops at a chunk of the groups by itself, unless
+    // overlapping groups have more tiles than an int counts
+    while (base + ch.total <= want) {
       base += ch.total;
       c += 256;
+      if (c >= P.E) return false;
       ch.load(P.indptr, P.E, rows, TM, c, lane);
     }
     const int own = __builtin_amdgcn_readfirstlane(__popcll(__ballot(base + ch.incl <= want)));
@@ -130,6 +133,7 @@ __device__ __forceinline__ bool ragged_tile(const ProductArgs& P, int TM, int NT
       }
     t.e = c + 4 * own + k;
     j = L - (unsigned)first * NT;
+    if (j >= nm * NT) return false;      // (then, too)
   }
   int mt;
   panel_item(j, nm, (unsigned)NT, mt, t.nt);

@@ -505,16 +505,20 @@ int moe_gemm2_weighted_int8(const void* q, const float* q_scale, const void* w2,
  *   b_scale fp32 [ceil(N/128), ceil(K/128)]     one per 128 x 128
  *   addend  bf16 [M, N] or NULL; may be out itself when out is bf16
  *   out     bf16, or fp32 (out_f32 != 0) [M, N]
- * Each block of 128 values of K is summed by one MFMA and folded with its
- * scales in fp32; out is rounded once.  (The fp8 MFMA's own sum of 128 products
- * carries up to 5e-5 of the sum of their magnitudes; typically 1e-6.)  NaN codes and infinite or NaN scales
- * give NaN or infinities in the rows and columns that they belong to.
+ * Each block of 128 values of K is summed by one MFMA and folded with the
+ * product of its two scales in fp32; out is rounded once.  (The fp8 MFMA's own
+ * sum of 128 products carries up to 5e-5 of the sum of their magnitudes;
+ * typically 1e-6.)  NaN codes, infinite or NaN scales and products of scales
+ * beyond fp32 give NaN or infinities in the rows and columns that they belong to.
  * K is a multiple of 16 and N any (MFMA_TILED: of 128 and 16; FP8MOE_ERR_ALIGN),
  * both at most FP8MOE_MAX_PRODUCT_DIM, M < 2^30 (FP8MOE_ERR_LIMIT).  a and b are
  * 16-byte aligned, the others to their elements (FP8MOE_ERR_ALIGN); out overlaps
  * no other tensor but addend as said (FP8MOE_ERR_SHAPE).  M == 0 launches nothing.
- * The workspace is gemm_fp8_blocks_workspace_size bytes (0 for many sizes: then it may be
- * NULL), 256-byte aligned; it holds nothing between calls.
+ * The workspace is gemm_fp8_blocks_workspace_size bytes: at most 16 MiB, never
+ * fewer for more rows, and 0 for K <= 1920 (then it may be NULL).  It is 256-byte
+ * aligned (FP8MOE_ERR_WORKSPACE), overlaps no tensor (FP8MOE_ERR_SHAPE) and holds
+ * nothing between calls; calls, captured ones too, that share it must not run at
+ * the same time.
  * Deterministic; an output's last bits may differ with M, N and the layout.
  */
 #define FP8MOE_MAX_PRODUCT_DIM 65536
@@ -534,8 +538,9 @@ int gemm_fp8_blocks(const void* a, const float* a_scale, const void* b, const fl
  *            m_indptr[E] <= rows; groups may be empty.  moe_route_permute's
  *            m_indptr is of this form.  Values outside [0, rows] are taken as
  *            the nearer end and a group whose end lies ahead of its start as
- *            empty, so no row outside the tensors is touched; where groups
- *            overlap, their common rows hold either's result.
+ *            empty, so no row outside the tensors is touched; rows of out that
+ *            lie in several groups, and others where groups overlap, may be
+ *            left as they were or hold any of those groups' results.
  *   out      bf16, or fp32 (out_f32 != 0) [rows, N]; rows of no group are not
  *            written
  * Sums, types, sizes, alignment, overlap and errors as for gemm_fp8_blocks (in bf16 K is a

@@ -272,6 +272,7 @@ def test_ragged_every_height(fmt, tiled, lo, hi, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(4096, 2000, 2048), (2500, 4100, 1040), (2048, 4096, 1936), (1111, 3900, 2064),
+                                   (1111, 2000, 1936), (700, 516, 16384), (4100, 520, 4240),
                                    (512, 1500, 7168), (300, 500, 7184), (130, 260, 16384), (64, 500, 7168),
                                    (48, 4096, 2000), (30, 130, 4096), (5, 7168, 2048), (1, 33, 16384)])
 @pytest.mark.parametrize("addend", [False, True])
@@ -286,6 +287,18 @@ def test_gemm_every_kernel(M, N, K, addend):
         want += add.double()
     assert torch.equal(fm.gemm_fp8_blocks(*ops, addend=add, out_dtype=torch.float32).double(), want)
     assert torch.equal(fm.gemm_fp8_blocks(*ops, addend=add), want.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("M,N,K", [(4096, 2000, 2048), (2500, 4112, 1152), (8200, 4096, 2048), (1111, 2000, 1920),
+                                   (300, 7168, 2048), (700, 528, 8192), (300, 512, 7168), (130, 272, 16384),
+                                   (33, 4096, 2048)])
+def test_gemm_every_kernel_tiled(M, N, K):
+    g = gen(M + K)
+    a, sa, b, sb = gemm_operands(g, M, N, K)
+    say("every kernel tiled", M, N, K)
+    out = fm.gemm_fp8_blocks(a, sa, fm.pack_weights(b[None]).view(E4M3)[0], sb, out_dtype=torch.float32,
+                             weight_layout=fm.WEIGHTS_MFMA_TILED)
+    assert torch.equal(out.double(), product64(a, sa, b, sb))
 
 
 @pytest.mark.parametrize("M,N,K", [(3, 70, 65536), (100, 300, 65536), (3, 65536, 128), (200, 65536, 48), (1, 65536, 2048)])
@@ -331,6 +344,27 @@ def test_ragged_far_groups():
         for r in (1, rows - 2):
             s = slice(max(r, 1), r + 2)
             assert torch.equal(out[s].double(), product64(a[s], sa[s], b[-1].view(E4M3), sb[-1])), (rows, r)
+
+
+@pytest.mark.parametrize("rows", [1, 50, 4000, 2 ** 29 - 2 ** 21])
+def test_ragged_overlapping_groups(rows):
+    """512 groups of every row: more tiles than distinct groups could have, and with the most rows more than 2^31.
+    What is written is a group's result (the groups are equal here), nothing behind the rows is."""
+    E, N, K, mark = 1024, 16, 16, 99.0
+    g = gen(rows)
+    few = min(rows, 4096)
+    a, sa = whole(g, few, K).repeat(rows // few, 1), powers(g, few, 1).repeat(rows // few, 1)
+    b, sb = whole(g, 1, N, K).expand(E, N, K).contiguous(), powers(g, 1, 1, 1).expand(E, 1, 1).contiguous()
+    ptr = torch.tensor([0, rows] * (E // 2) + [0], dtype=torch.int32, device="cuda")
+    out = torch.full((rows + 64, N), mark, dtype=torch.bfloat16, device="cuda")
+    say("overlapping groups", rows)
+    fm.grouped_gemm_fp8_ragged(a, sa, b, sb, ptr, out=out[:rows])
+    torch.cuda.synchronize()
+    assert torch.all(out[rows:] == mark)
+    want = product64(a[:few], sa[:few], b[0], sb[0]).to(torch.bfloat16)
+    for r in range(0, rows, max(few, rows // 64 // few * few)):
+        got = out[r:r + few]
+        assert torch.all((got == want) | (got == mark))
 
 
 def test_quant_far_rows():
