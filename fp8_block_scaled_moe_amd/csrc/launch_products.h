@@ -27,13 +27,13 @@ struct ProductArgs {
   bool bf16, packed, out_f32, vec;
 };
 
-// How a product is run: the streaming kernel with 16 sub_tiles rows a tile, or
-// a tile kernel (weight rows x rows of a), in `splits` parts of K.
-// (kTile128x128x8: with eight waves, alone on its CU.)
+// How a product is run: the streaming kernel with tiles of 16 bands weight rows
+// and 16 sub_tiles rows, or a tile kernel (weight rows x rows of a;
+// kTile128x128x8: with eight waves, alone on its CU), in `splits` parts of K.
 enum ProductShape { kStream, kTile256x256, kTile256x128, kTile128x128, kTile128x128x8, kTile128x64 };
 struct ProductPlan {
   ProductShape shape;
-  int sub_tiles, splits;
+  int bands, sub_tiles, splits;
 };
 // E == 0: dense.  rows, N, K steps of 128 bytes.
 ProductPlan plan_product(int64_t rows, int N, int steps, int E, int num_cu);
@@ -43,7 +43,7 @@ size_t partial_bytes(int64_t rows, int N, int steps);
 // Runs P (splits and partial as the plan says).
 hipError_t launch_product(const ProductArgs& P, const ProductPlan& plan, hipStream_t stream);
 
-hipError_t launch_product_stream(const ProductArgs& P, int sub_tiles, hipStream_t stream);
+hipError_t launch_product_stream(const ProductArgs& P, int bands, int sub_tiles, hipStream_t stream);
 hipError_t launch_product_tile(const ProductArgs& P, ProductShape shape, hipStream_t stream);
 hipError_t launch_product_join(const ProductArgs& P, hipStream_t stream);
 

@@ -84,11 +84,11 @@ ProductPlan plan_product(int64_t rows, int N, int steps, int E, int num_cu) {
   // tiles would be few.  128 groups, 1536 x 2048, tiled, us, streaming | 128 x 64:
   // 4 rows 69, 71, 12 rows 77, 74, 24 rows 106, 78; 2 rows in bf16 67, 79; 8
   // groups of 4 rows, 4096 x 4096: 27, 28.
-  if (grouped && (share <= 4 || (share <= 16 && small < num_cu))) return {kStream, 1, 1};
+  if (grouped && (share <= 4 || (share <= 16 && small < num_cu))) return {kStream, 2, 1, 1};
   auto fits = [&](int s) {
     return s == 1 || (!grouped && steps >= kPartSteps * s && (size_t)rows * ((N + 7) & ~7) * s * sizeof(float) <= kMaxPartial);
   };
-  ProductPlan best{kTile256x256, 0, 1};
+  ProductPlan best{kTile256x256, 0, 0, 1};
   float us = 1e30f;
   for (const TileCost& c : kTiles) {
     // tiles are numbered in 31 bits (256 x 256 ones of 2^30 rows and 2^16 columns fit)
@@ -96,25 +96,27 @@ ProductPlan plan_product(int64_t rows, int N, int steps, int E, int num_cu) {
     for (int s = 1; s <= (c.shape == kTile128x64 || c.shape == kTile128x128x8 ? kMaxSplits : 1); s *= 2) {
       if (!fits(s)) continue;
       const float t = tile_us(c, groups, share, N, steps, s, num_cu) + join_us(rows, N, s);
-      if (t < us) us = t, best = {c.shape, 0, s};
+      if (t < us) us = t, best = {c.shape, 0, 0, s};
     }
   }
   if (grouped || rows > 1024) return best;
-  // Streaming: a step of 32 weight rows by 16 TS takes a CU 0.09 + 0.09 TS us, and
-  // a workgroup alone on its CU no less than half that a step of its eight waves.
+  // Streaming: what a step of 16 or 32 weight rows by 16 ts rows takes a CU.
   const int64_t cut = ceil_div(rows, 64);
   const int ts = (int)ceil_div(ceil_div(rows, cut), 16);
-  for (int s = 1; s <= kMaxSplits; s *= 2) {
-    if (!fits(s)) continue;
-    const float wgs = (float)(cut * ceil_div(N, 32) * s), work = ceil_div(steps, s) * (0.09f + 0.09f * ts);
-    const float t = kLaunch + ceilf(wgs / num_cu) * work + join_us(rows, N, s);
-    if (t < us) us = t, best = {kStream, ts, s};
+  for (int bands = 1; bands <= 2; ++bands) {
+    const float step = bands == 1 ? 0.06f + 0.07f * ts : 0.09f + 0.09f * ts;
+    for (int s = 1; s <= kMaxSplits; s *= 2) {
+      if (!fits(s)) continue;
+      const float wgs = (float)(cut * ceil_div(N, 16 * bands) * s);
+      const float t = kLaunch + ceilf(wgs / num_cu) * ceil_div(steps, s) * step + join_us(rows, N, s);
+      if (t < us) us = t, best = {kStream, bands, ts, s};
+    }
   }
   return best;
 }
 
 hipError_t launch_product(const ProductArgs& P, const ProductPlan& plan, hipStream_t stream) {
-  const hipError_t err = plan.shape == kStream ? launch_product_stream(P, plan.sub_tiles, stream)
+  const hipError_t err = plan.shape == kStream ? launch_product_stream(P, plan.bands, plan.sub_tiles, stream)
                                                : launch_product_tile(P, plan.shape, stream);
   if (err != hipSuccess || P.splits == 1) return err;
   return launch_product_join(P, stream);

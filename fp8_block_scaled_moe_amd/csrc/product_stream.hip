@@ -157,20 +157,22 @@ __global__ __launch_bounds__(kJoinThreads) void product_join_kernel(const Produc
 
 namespace {
 
-// Weight rows, waves and steps in flight of a workgroup.  Dense, few rows, us,
-// MFMA-tiled unless said (16 rows x 4 waves, 16 x 8, 16 x 16, 32 x 4, 32 x 8;
-// with S parts of K), N x K:
-//   7168 x 2048:   M=1: 6.0, 5.7, 7.3, 6.2, 5.8   M=64: 15.3, 16.2, 20.5, 11.2, 10.7 (S=2: 15.3)
-//   4096 x 7168:   M=16: 12.5, 10.4, 10.7, 13.4, 12.1 (S=2: 11.8)   M=64: 24, 24, 28, 28, 26 (S=2: 20.6)
-//   1500 x 7168, row-major:  M=1: 12.5, 8.7, 8.8, 15.5, 11.9 (S=4: 8.4)   M=33: 18, 18, 18, 22, 22 (S=4: 12.2)
-//   512 x 7168:    M=33: 14, 14, 15, 15, 15 (S=8: 8.2)
-//   7168 x 16384:  M=1: 31.8, 26.0, 25.9, 31.5, 23.4   M=64: 94, 95, 111, 59, 55
+// Weight rows, waves and steps in flight of a workgroup.  Dense, eight waves, us
+// in a graph, 16 | 32 weight rows, each in 1, 2, 4 parts of K:
+//   7168 x 2048, MFMA-tiled: M=1: 5.7, 9.2 | 5.8, 8.0   M=33: 12.0, 18.3 | 8.0, 12.6
+//   4096 x 7168, MFMA-tiled: M=1: 8.4, 10.4, 11.1 | 9.2, 10.4, 10.2   M=16: 10.3, 13.0, 14.1 | 12.1, 11.8, 11.7
+//                            M=33: 16.1, 20.5, 23.8 | 17.9, 15.6, 17.0
+//   1500 x 7168, row-major:  M=1: 8.8, 8.9, 8.5 | 11.7, 10.9, 8.4   M=33: 18.2, 14.8, 16.2 | 21.8, 17.0, 12.2
+//   512 x 7168, MFMA-tiled:  M=1: 5.4, 6.3, 5.6 | 6.2, 6.8, 5.8   M=33: 14.3, 11.8, 8.7 | 15.3, 12.9, 9.4
+//   2000 x 1936, row-major:  M=1: 4.0, 5.8 | 4.5, 6.0   M=33: 5.7, 6.9 | 6.7, 7.6
+// Sixteen waves: 5.9 to 7.2, 8.4 to 9.5 and 8.6 to 11.8 for the first, second
+// and third M=1; eight steps in flight instead of four: no change.
 // Grouped, where weights of many groups stream by (256 groups of 2 rows, 4096 x
 // 7168): 32 x 4 1052, 32 x 8 1036; with more rows four waves are ahead (12 rows
 // of each of 128 groups, 1536 x 2048: 77 and 98).
-template <int TS, int NW, bool BF>
+template <int B, int TS, int NW, bool BF>
 hipError_t launch_stream(const ProductArgs& P, hipStream_t stream) {
-  constexpr int B = 2, U = TS <= 2 ? 4 : 2;
+  constexpr int U = B == 1 || TS <= 2 ? 4 : 2;
   const int64_t NT = (P.N + 16 * B - 1) / (16 * B);
   const int64_t tiles = P.indptr ? P.rows / (16 * TS) + (P.rows < P.E ? P.rows : P.E) : (P.rows + 16 * TS - 1) / (16 * TS);
   if (tiles * NT >= (int64_t)1 << 31) return hipErrorInvalidValue;
@@ -184,15 +186,22 @@ hipError_t launch_stream(const ProductArgs& P, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_product_stream(const ProductArgs& P, int sub_tiles, hipStream_t stream) {
-  if (P.bf16)
-    return sub_tiles == 1 ? launch_stream<1, 4, true>(P, stream) : hipErrorInvalidValue;
-  if (P.indptr) return sub_tiles == 1 ? launch_stream<1, 4, false>(P, stream) : hipErrorInvalidValue;
-  switch (sub_tiles) {
-    case 1: return launch_stream<1, 8, false>(P, stream);
-    case 2: return launch_stream<2, 8, false>(P, stream);
-    case 3: return launch_stream<3, 8, false>(P, stream);
-    default: return launch_stream<4, 8, false>(P, stream);
+hipError_t launch_product_stream(const ProductArgs& P, int bands, int sub_tiles, hipStream_t stream) {
+  if (P.indptr) {
+    if (bands != 2 || sub_tiles != 1) return hipErrorInvalidValue;
+    return P.bf16 ? launch_stream<2, 1, 4, true>(P, stream) : launch_stream<2, 1, 4, false>(P, stream);
+  }
+  if (P.bf16) return hipErrorInvalidValue;   // bf16 products are grouped ones
+  switch (4 * bands + sub_tiles) {
+    case 5: return launch_stream<1, 1, 8, false>(P, stream);
+    case 6: return launch_stream<1, 2, 8, false>(P, stream);
+    case 7: return launch_stream<1, 3, 8, false>(P, stream);
+    case 8: return launch_stream<1, 4, 8, false>(P, stream);
+    case 9: return launch_stream<2, 1, 8, false>(P, stream);
+    case 10: return launch_stream<2, 2, 8, false>(P, stream);
+    case 11: return launch_stream<2, 3, 8, false>(P, stream);
+    case 12: return launch_stream<2, 4, 8, false>(P, stream);
+    default: return hipErrorInvalidValue;
   }
 }
 

@@ -274,7 +274,8 @@ def test_ragged_every_height(fmt, tiled, lo, hi, N, K):
 @pytest.mark.parametrize("M,N,K", [(4096, 2000, 2048), (2500, 4100, 1040), (2048, 4096, 1936), (1111, 3900, 2064),
                                    (1111, 2000, 1936), (700, 516, 16384), (4100, 520, 4240),
                                    (512, 1500, 7168), (300, 500, 7184), (130, 260, 16384), (64, 500, 7168),
-                                   (48, 4096, 2000), (30, 130, 4096), (5, 7168, 2048), (1, 33, 16384)])
+                                   (48, 4096, 2000), (30, 130, 4096), (20, 7170, 2064), (60, 7168, 2048), (5, 7168, 2048),
+                                   (1, 33, 16384)])
 @pytest.mark.parametrize("addend", [False, True])
 def test_gemm_every_kernel(M, N, K, addend):
     """Sizes at which the cost model takes each of the kernels, in one part of K and in several."""
