@@ -41,18 +41,15 @@ __device__ __forceinline__ void wave_lds_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// LDS of a workgroup: its buffers as objects of their
-// own, so that the compiler does not wait for loads into one buffer where
-// another one is read.
+// LDS of a workgroup: its buffers as objects of their own, so that the compiler
+// does not wait for loads into one buffer where another one is read.
 struct ProductLds {
-  uint8_t *s0, *s1, *s2, *s3;
+  uint8_t *s0, *s1, *s2;
   // s is a constant of the unrolled loops
-  __device__ __forceinline__ uint8_t* stage(int s) const { return s == 0 ? s0 : s == 1 ? s1 : s == 2 ? s2 : s3; }
-  float* scale;    // [2][kPScaleSteps][2 blocks of 128 weight rows][SROW]
-  float* bscale;   // [2 blocks][KT]
+  __device__ __forceinline__ uint8_t* stage(int s) const { return s == 0 ? s0 : s == 1 ? s1 : s2; }
+  float* scale;    // [2][kPScaleSteps][blocks of 128 weight rows][SROW]
+  float* bscale;   // [blocks][KT]
 };
-
-
 
 // The K steps of this part of the product (blockIdx.z of splits): steps first
 // .. first + KT - 1, KF of them whole.

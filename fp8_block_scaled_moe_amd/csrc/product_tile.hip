@@ -9,6 +9,20 @@
 // sit on the MFMA's A side, rows of a on its B side: a lane then holds four
 // consecutive output columns of one row, and needs one scale a step and
 // sub-tile.
+//
+// What bounds it (one MI355X): 8192 x 4096 x 7168 in FP8 takes 230 us, 2.09
+// PFLOP/s, 1.9 us a step of a 256 x 256 tile.  The same step in a bare loop: its
+// products alone 1.43 us (a clock of 1.9 GHz, the card at its power limit), with
+// the folds 1.50, with the loads 1.49, with both 1.67 to 1.73: folds and loads
+// each hide under the products, not both.  Where groups have few rows the
+// weights' bytes are next: 256 groups of 256 rows, 7168 x 2048, 1.44 ms, 1.34
+// PFLOP/s; half of them need a second tile for a few rows over 256.  bf16 (no
+// folds): 8192 x 8192 x 8192 864 us, 1.27 PFLOP/s.
+//
+// Slower: weights of the packed layout straight into registers with rows in
+// four LDS buffers (273 us against 255 at the time); runs of N tiles in one
+// workgroup, the next one's loads under this one's epilogue (256 groups: 1540
+// and 1445); 128 x 320 tiles, which take those groups whole (1680 and 1500).
 #include "product_tile.h"
 
 namespace fp8moe {
@@ -20,7 +34,7 @@ struct ProductTile {
   static constexpr int WPW = WBLK / S::Waves, APW = (ABLK + S::Waves - 1) / S::Waves;   // of them by each wave
   static constexpr int LPW = WPW + APW;
   static constexpr int XN = 3;   // fragments of rows held
-  static_assert((NST - 2) * LPW < 64, "vmcnt is a 6-bit counter");
+  static_assert(NST == 2 || NST == 3, "a step waits for at most one other's loads");
 
   const ProductArgs& P;
   const ProductLds L;
@@ -49,16 +63,6 @@ struct ProductTile {
     // and odd number (the swizzle's key takes bit 3 of the row)
     rowoff0 = (lane >> 3) * kb + (((lane & 7) ^ swz_key(lane >> 3)) << 4);
     rowoff1 = (lane >> 3) * kb + (((lane & 7) ^ swz_key(8 + (lane >> 3))) << 4);
-  }
-
-  // Waits until at most j steps' loads of the wave are under way; j is a
-  // constant of the unrolled loop.
-  __device__ static __forceinline__ void wait_steps(int j) {
-    switch (j) {
-      case 0: return vmcnt_wait<0>();
-      case 1: return vmcnt_wait<(NST > 2 ? 1 : 0) * LPW>();
-      default: return vmcnt_wait<(NST > 3 ? 2 : 0) * LPW>();
-    }
   }
 
   // The lane's offset in block blk of weight rows or rows of a, ahead of the K
@@ -164,11 +168,10 @@ struct ProductTile {
       }
     };
     auto step = [&](int s, int k) __attribute__((always_inline)) {
-      // this step's loads have landed; those of the next NST - 2 may be under way
-      const int ahead = min(NST - 2, KF - 1 - k);
-#pragma unroll
-      for (int j = NST - 2; j >= 0; --j)
-        if (ahead == j) wait_steps(j);
+      // this step's loads have landed; with three buffers the next one's may be
+      // under way
+      if (NST > 2 && k + 1 < KF) vmcnt_wait<LPW>();
+      else vmcnt_wait<0>();
       step_barrier();
       if constexpr (!BF) sc.advance(k);
       if (k + NST - 1 < KF) dma((s + NST - 1) % NST, k + NST - 1);
@@ -201,12 +204,12 @@ template <typename S, bool BF, bool PACKED>
 __global__ __launch_bounds__(S::Threads) void product_tile_kernel(const ProductArgs P) {
   __shared__ __attribute__((aligned(16))) uint8_t s0[S::OutBytes > S::Stage ? S::OutBytes : S::Stage];
   __shared__ __attribute__((aligned(16))) uint8_t s1[S::Stage];
-  __shared__ __attribute__((aligned(16))) uint8_t s2[S::NST > 2 ? S::Stage : 16], s3[S::NST > 3 ? S::Stage : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t s2[S::NST > 2 ? S::Stage : 16];
   __shared__ __attribute__((aligned(16))) float sc[BF ? 4 : S::ScaleFloats];
   __shared__ float sb[BF ? 4 : S::BScaleFloats];
   RaggedTile t;
   if (!ragged_tile(P, S::TM, (P.N + S::TN - 1) / S::TN, (unsigned)wide_block(), t)) return;
-  const ProductLds L{s0, s1, s2, s3, sc, sb};
+  const ProductLds L{s0, s1, s2, sc, sb};
   const StepRange R(P);
   with_sub_tiles<S>(t.h, [&](auto ts) __attribute__((always_inline)) {
     ProductTile<S, decltype(ts)::value, BF, PACKED> tile(P, L, t, R);
