@@ -92,7 +92,7 @@ ProductPlan plan_product(int64_t rows, int N, int steps, int E, int num_cu) {
   float us = 1e30f;
   for (const TileCost& c : kTiles) {
     // tiles are numbered in 31 bits (256 x 256 ones of 2^30 rows and 2^16 columns fit)
-    if ((rows / c.tm + groups + 1) * ceil_div(N, c.tn) >= (int64_t)1 << 31) continue;
+    if ((rows / c.tm + groups + 64) * ceil_div(N, c.tn) >= (int64_t)1 << 31) continue;
     for (int s = 1; s <= (c.shape == kTile128x64 || c.shape == kTile128x128x8 ? kMaxSplits : 1); s *= 2) {
       if (!fits(s)) continue;
       const float t = tile_us(c, groups, share, N, steps, s, num_cu) + join_us(rows, N, s);

@@ -24,7 +24,7 @@ __global__ __launch_bounds__(64 * NW) void product_stream_kernel(const ProductAr
   constexpr int kHalf = PACKED ? 1024 : 64, kStep = PACKED ? 2048 : kKB;
   __shared__ v4f red[NW][TM][4 * B];
   RaggedTile t;
-  if (!ragged_tile(P, TM, (P.N + TN - 1) / TN, (unsigned)wide_block(), t)) return;
+  if (!ragged_tile<false>(P, TM, (P.N + TN - 1) / TN, (unsigned)wide_block(), t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, l16 = lane & 15, n0 = TN * t.nt, kb = P.kbytes;
   const int KF = kb / kKB, KT = (kb + kKB - 1) / kKB;   // whole steps, and all

@@ -19,6 +19,7 @@ struct TileShape {
   static constexpr int WN = WN_, WM = WM_, TSMAX = TSMAX_, NST = NST_;
   static constexpr int Waves = WN * WM, Threads = 64 * Waves;
   static constexpr int TN = 64 * WN, TM = 16 * TSMAX * WM;
+  static constexpr bool DEAL = TM >= 256;
   static constexpr int NBlk = TN / 128;                        // blocks of 128 weight rows
   static constexpr int Stage = (TN + TM) * kKB;                // bytes of a buffer
   static constexpr int SRow = WM * ((TSMAX + 3) / 4) * 64;     // scales of a step and block of weight rows
@@ -234,7 +235,8 @@ __device__ __forceinline__ void with_sub_tiles(int h, Body body) {
 template <typename S>
 dim3 tile_grid(const ProductArgs& P) {
   const int64_t NT = (P.N + S::TN - 1) / S::TN;
-  const int64_t tiles = P.indptr ? P.rows / S::TM + (P.rows < P.E ? P.rows : P.E) : (P.rows + S::TM - 1) / S::TM;
+  const int64_t most = P.rows / S::TM + (P.rows < P.E ? P.rows : P.E);
+  const int64_t tiles = P.indptr == nullptr ? (P.rows + S::TM - 1) / S::TM : S::DEAL ? dealt_tiles(most) : most;
   dim3 grid = wide_grid((tiles * NT + kNumXcd - 1) / kNumXcd * kNumXcd);
   grid.z = P.splits;
   return grid;

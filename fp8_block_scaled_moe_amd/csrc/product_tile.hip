@@ -208,7 +208,7 @@ __global__ __launch_bounds__(S::Threads) void product_tile_kernel(const ProductA
   __shared__ __attribute__((aligned(16))) float sc[BF ? 4 : S::ScaleFloats];
   __shared__ float sb[BF ? 4 : S::BScaleFloats];
   RaggedTile t;
-  if (!ragged_tile(P, S::TM, (P.N + S::TN - 1) / S::TN, (unsigned)wide_block(), t)) return;
+  if (!ragged_tile<S::DEAL>(P, S::TM, (P.N + S::TN - 1) / S::TN, (unsigned)wide_block(), t)) return;
   const ProductLds L{s0, s1, s2, sc, sb};
   const StepRange R(P);
   with_sub_tiles<S>(t.h, [&](auto ts) __attribute__((always_inline)) {

@@ -21,11 +21,16 @@ struct RaggedTile {
   int e, row0, h, nt;
 };
 
+// M tiles whose weight tiles are taken together: one XCD's workgroups then
+// share 8 row tiles and a few weight tiles in its L2.
+constexpr int kPanel = 8;
+
 // Tiles of TM rows of four groups a lane, 256 groups a wave; indptr values
 // outside [0, rows] or descending leave groups empty instead of rows out of
 // range.
 struct GroupChunk {
   int start[4], len[4], tiles[4], incl, total;
+  bool high;   // a group has more tiles than a panel
   __device__ __forceinline__ void load(const int32_t* __restrict__ indptr, int E, int rows, int TM, int c, int lane) {
     int s[5];
 #pragma unroll
@@ -45,12 +50,9 @@ struct GroupChunk {
       if (lane >= o) incl += v;
     }
     total = __builtin_amdgcn_readlane(incl, 63);
+    high = __ballot(max(max(tiles[0], tiles[1]), max(tiles[2], tiles[3])) > kPanel) != 0;
   }
 };
-
-// M tiles whose weight tiles are taken together: one XCD's workgroups then
-// share 8 row tiles and a few weight tiles in its L2.
-constexpr int kPanel = 8;
 
 // Item j of a group with nm row tiles: panels of kPanel row tiles, in a panel
 // the weight tiles, and the panel's row tiles innermost.
@@ -66,10 +68,30 @@ __device__ __forceinline__ void panel_item(unsigned j, unsigned nm, unsigned NT,
   mt = (int)(kPanel * p + rem - n * pm);
 }
 
-// The tile of this workgroup (false: none).  Workgroup b runs on XCD b % 8 and
-// takes item (b % 8) * ceil(items / 8) + b / 8, so each XCD works through a
-// contiguous range of items.  An M tile has at most TM rows; a group's rows
-// are cut into tiles of equal height, a multiple of 16.
+// M tiles of groups that an XCD is dealt at a time.
+constexpr int kDeals = 64;
+__device__ __forceinline__ unsigned deal_tiles(unsigned tiles) {
+  return min(max(tiles / kDeals, 1u), (unsigned)kPanel);
+}
+// M tiles for which the grid needs workgroups where up to `tiles` are dealt: the
+// last round's deals may be missing from any XCD but the first.
+inline int64_t dealt_tiles(int64_t tiles) {
+  return tiles < 2 * kDeals ? (tiles + kNumXcd - 1) / kNumXcd * kNumXcd : tiles + kNumXcd * kPanel;
+}
+
+// The tile of this workgroup (false: none).  Workgroup b runs on XCD b % 8.
+// Each XCD works through a contiguous range of items, which keeps what a
+// group's tiles share in its L2.  With groups of more than a panel, ranges of
+// as many items differ in work by the low tiles of small groups beside them:
+// DEAL then deals M tiles to the XCDs in turn.  us, contiguous | dealt, 256 x 256
+// tiles: 128 groups, 32768 rows, popularity 1 / rank^1.2, 1536 x 2048, 202 | 192;
+// 8 of 4096, 2048 x 7168, 571 | 541; without such groups, 256 of 256, 7168 x
+// 2048, 1487 | 1524.  Low tiles, whose weights come at the rate of memory, are not
+// dealt: 128 x 64 tiles, bf16, 256 groups, 16384 rows, 1 / rank^0.7, 7168 x 2048,
+// 1509 | 1546.
+// An M tile has at most TM rows; a group's rows are cut into tiles of equal
+// height, a multiple of 16.
+template <bool DEAL>
 __device__ __forceinline__ bool ragged_tile(const ProductArgs& P, int TM, int NT, unsigned block, RaggedTile& t) {
   const unsigned slot = block / kNumXcd, xcd = block % kNumXcd;
   int start, len;
@@ -87,14 +109,24 @@ __device__ __forceinline__ bool ragged_tile(const ProductArgs& P, int TM, int NT
     GroupChunk ch;
     ch.load(P.indptr, P.E, rows, TM, 0, lane);
     unsigned tot = ch.total;
+    bool high = ch.high;
     for (int c = 256; c < P.E; c += 256) {
       GroupChunk more;
       more.load(P.indptr, P.E, rows, TM, c, lane);
       tot += more.total;
+      high = high || more.high;
     }
-    const unsigned items = __builtin_amdgcn_readfirstlane(tot) * NT, per = (items + kNumXcd - 1) / kNumXcd;
-    const unsigned L = xcd * per + slot;
-    if (slot >= per || L >= items) return false;
+    tot = __builtin_amdgcn_readfirstlane(tot);
+    unsigned L;
+    if (DEAL && high) {
+      const unsigned deal = deal_tiles(tot) * NT, round = slot / deal;
+      L = (round * kNumXcd + xcd) * deal + (slot - round * deal);
+    } else {
+      const unsigned per = (tot * NT + kNumXcd - 1) / kNumXcd;
+      L = xcd * per + slot;
+      if (slot >= per) return false;
+    }
+    if (L >= tot * NT) return false;
     const int want = (int)(L / NT);      // the group that holds tile `want` holds item L
     int base = 0, c = 0;
     // want < tot, so this stops at a chunk of the groups by itself, unless

@@ -271,6 +271,33 @@ def test_ragged_every_height(fmt, tiled, lo, hi, N, K):
         assert torch.equal(out[r].double(), want), f"group {e} of {ends[e + 1] - ends[e]} rows"
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "bf16"])
+@pytest.mark.parametrize("sizes,N,K", [([9000, 3, 0, 7100, 300, 40, 3557], 1500, 528), ([20000], 1536, 512),
+                                       ([30, 60, 0, 90] * 75 + [22000, 2049], 1536, 512),
+                                       ([2304] * 8 + [1, 2305, 100], 2048, 384)])
+def test_ragged_high_and_low_groups(fmt, sizes, N, K):
+    """Groups of more than eight tiles beside low ones, whose tiles are dealt out: every row, and none behind."""
+    E, rows = len(sizes), sum(sizes)
+    g = gen(E + rows)
+    ptr = torch.tensor([0] + sizes, device="cuda").cumsum(0).to(torch.int32)
+    t = E4M3 if fmt == "fp8" else torch.bfloat16
+    a, b = whole(g, rows + 5, K, dtype=t), whole(g, E, N, K, dtype=t)
+    out = torch.full((rows + 5, N), 7.5, dtype=torch.float32, device="cuda")
+    say("high and low groups", fmt, E, rows)
+    sa = sb = None
+    if fmt == "fp8":
+        sa, sb = powers(g, rows + 5, nb(K)), powers(g, E, nb(N), nb(K))
+        fm.grouped_gemm_fp8_ragged(a, sa, b, sb, ptr, out=out)
+    else:
+        fm.grouped_gemm_bf16_ragged(a, b, ptr, out=out)
+    ends = ptr.tolist()
+    assert torch.all(out[rows:] == 7.5)
+    for e in range(E):
+        r = slice(ends[e], ends[e + 1])
+        want = product64(a[r], None if sa is None else sa[r], b[e], None if sb is None else sb[e])
+        assert torch.equal(out[r].double(), want), f"group {e} of {sizes[e]} rows"
+
+
 @pytest.mark.parametrize("M,N,K", [(4096, 2000, 2048), (2500, 4100, 1040), (2048, 4096, 1936), (1111, 3900, 2064),
                                    (1111, 2000, 1936), (700, 516, 16384), (4100, 520, 4240),
                                    (512, 1500, 7168), (300, 500, 7184), (130, 260, 16384), (64, 500, 7168),
