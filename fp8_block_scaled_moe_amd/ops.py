@@ -917,7 +917,8 @@ def grouped_gemm_bf16_ragged(a, b, m_indptr, out=None, out_dtype=torch.bfloat16,
 
 def quant_fp8_blocks(x, gated=False, q=None, scale=None):
     """bf16 or fp32 x [M, N] -> (e4m3 codes uint8 [M, N], fp32 scales [M, ceil(N/128)], one per row and 128
-    columns).  gated: x is [M, 2N], gate and up halves, and silu(gate) * up is quantised."""
+    columns).  gated: x is [M, 2N], gate and up halves, and silu(gate) * up is quantised.  A given q may be
+    uint8 or float8_e4m3fn and comes back as it is."""
     f32 = getattr(x, "dtype", None) == torch.float32
     _need(x, torch.float32 if f32 else torch.bfloat16, "x", 2)
     M, N = x.shape
@@ -925,7 +926,8 @@ def quant_fp8_blocks(x, gated=False, q=None, scale=None):
         if N % 2:
             raise ValueError("gated x must have an even number of columns")
         N //= 2
-    q = _out(q, torch.uint8, (M, N), x, "q")
+    codes = torch.float8_e4m3fn if getattr(q, "dtype", None) == torch.float8_e4m3fn else torch.uint8
+    q = _out(q, codes, (M, N), x, "q")
     scale = _out(scale, torch.float32, (M, _blocks(N)), x, "scale")
     _launch(x.get_device(), lib().quant_fp8_blocks, x.data_ptr(), f32, M, N, bool(gated), q.data_ptr(),
             scale.data_ptr())

@@ -73,3 +73,17 @@ def test_middles_of_codes(amax):
         rows[:, 127] = amax
         rows[:, :126] = torch.where(rows[:, :126].abs() <= amax, rows[:, :126], torch.zeros((), dtype=dtype))
         compare(rows)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_codes_into_a_float8_tensor(gated):
+    """q of the type that the products take as a: the same codes, into the caller's tensor."""
+    x = torch.randn(9, 288, generator=torch.Generator().manual_seed(6)).bfloat16().cuda()
+    want, scale = fm.quant_fp8_blocks(x, gated=gated)
+    q = torch.zeros(want.shape, dtype=torch.float8_e4m3fn, device="cuda")
+    got, s = fm.quant_fp8_blocks(x, gated=gated, q=q)
+    torch.cuda.synchronize()
+    assert got is q and torch.equal(q.view(torch.uint8), want) and torch.equal(s, scale)
+    for bad in (torch.int8, torch.float8_e5m2):
+        with pytest.raises(TypeError):
+            fm.quant_fp8_blocks(x, gated=gated, q=torch.zeros(want.shape, dtype=bad, device="cuda"))
