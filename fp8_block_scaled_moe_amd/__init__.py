@@ -19,5 +19,5 @@ from .ops import (  # noqa: F401
     fused_int8_workspace_size, alloc_workspace_int8, moe_fused_int8, gemm1_swiglu_int8, quant_rows_int8,
     gemm2_weighted_int8, add_rmsnorm_quant, NORM_BF16, NORM_FP8, NORM_MXFP8, NORM_INT8, moe_router_topk,
     SCORE_SOFTMAX, SCORE_SIGMOID, gemm_workspace_size, alloc_workspace_gemm, gemm_fp8_blocks,
-    grouped_gemm_fp8_ragged, grouped_gemm_bf16_ragged, quant_fp8_blocks,
+    grouped_gemm_fp8_ragged, grouped_gemm_bf16_ragged, quant_fp8_blocks, product_plan,
 )

@@ -1234,6 +1234,23 @@ int moe_grouped_gemm_bf16_ragged(const void* a, const void* b, const int32_t* m_
                      weight_layout, stream);
 }
 
+int moe_product_plan(int64_t rows, int32_t N, int32_t K, int32_t E, int32_t bf16, int32_t num_cu, int32_t* weight_rows,
+                     int32_t* tile_rows, int32_t* waves, int32_t* parts) {
+  const bool grouped = E != 0;
+  const int esize = bf16 ? 2 : 1;
+  const int st = check_product(rows, N, K, grouped ? E : 1, esize, FP8MOE_WEIGHTS_ROW_MAJOR);
+  if (st) return st;
+  if (rows == 0 || num_cu < 1 || (bf16 && !grouped)) return fail(FP8MOE_ERR_SHAPE, "invalid plan arguments");
+  if (!weight_rows || !tile_rows || !waves || !parts) return fail(FP8MOE_ERR_NULL, "null output");
+  const ProductPlan plan = plan_product(rows, N, (K * esize + 127) / 128, E, num_cu);
+  const ProductTileSize size = product_tile_size(plan, grouped);
+  *weight_rows = size.weight_rows;
+  *tile_rows = size.rows;
+  *waves = size.waves;
+  *parts = plan.splits;
+  return ok();
+}
+
 int quant_fp8_blocks(const void* in, int32_t in_f32, int64_t M, int32_t N, int32_t gated, void* q, float* scale,
                      void* stream) {
   if (M < 0 || N <= 0) return fail(FP8MOE_ERR_SHAPE, "invalid M=%lld N=%d", (long long)M, N);

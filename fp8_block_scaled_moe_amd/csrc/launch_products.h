@@ -37,6 +37,11 @@ struct ProductPlan {
 };
 // E == 0: dense.  rows, N, K steps of 128 bytes.
 ProductPlan plan_product(int64_t rows, int N, int steps, int E, int num_cu);
+// Weight rows, rows of a and waves of a workgroup of the planned kernel.
+struct ProductTileSize {
+  int weight_rows, rows, waves;
+};
+ProductTileSize product_tile_size(const ProductPlan& plan, bool grouped);
 // Bytes of the parts' sums, never fewer for more rows.
 size_t partial_bytes(int64_t rows, int N, int steps);
 

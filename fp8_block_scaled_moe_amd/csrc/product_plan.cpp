@@ -115,6 +115,12 @@ ProductPlan plan_product(int64_t rows, int N, int steps, int E, int num_cu) {
   return best;
 }
 
+ProductTileSize product_tile_size(const ProductPlan& plan, bool grouped) {
+  for (const TileCost& c : kTiles)
+    if (c.shape == plan.shape) return {c.tn, c.tm, c.tn / 64 * c.wm};
+  return {16 * plan.bands, 16 * plan.sub_tiles, grouped ? 4 : 8};
+}
+
 hipError_t launch_product(const ProductArgs& P, const ProductPlan& plan, hipStream_t stream) {
   const hipError_t err = plan.shape == kStream ? launch_product_stream(P, plan.bands, plan.sub_tiles, stream)
                                                : launch_product_tile(P, plan.shape, stream);

@@ -949,6 +949,14 @@ def auto_tiles(T, K, H, I, E, num_cu=256):
     return t1.value, t2.value
 
 
+def product_plan(rows, N, K, E=0, bf16=False, num_cu=256):
+    """(weight rows, rows, waves, parts of K) of the kernel that gemm_fp8_blocks (E = 0) or the ragged products of E
+    groups take."""
+    v = [ctypes.c_int32(0) for _ in range(4)]
+    check(lib().moe_product_plan(rows, N, K, E, bool(bf16), num_cu, *map(ctypes.byref, v)))
+    return tuple(n.value for n in v)
+
+
 def select_tile_classes(total_rows, n, k, E, num_cu, narrow, tile_n):
     """tile_n: dict class -> width for the classes (narrow, 32, 64, 128)."""
     tm = ctypes.c_int32(0)

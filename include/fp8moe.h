@@ -652,6 +652,15 @@ int moe_select_tile(int64_t total_rows, int32_t n, int32_t k, int32_t E, int32_t
 int moe_auto_tiles(int64_t T, int32_t K, int32_t H, int32_t I, int32_t E, int32_t num_cu, int32_t* tile_m1,
                    int32_t* tile_m2);
 
+/* moe_product_plan: the kernel that gemm_fp8_blocks (E == 0) and the ragged
+ * products (E groups; bf16 != 0: moe_grouped_gemm_bf16_ragged) take for `rows` >= 1
+ * rows, N columns, K and num_cu compute units: weight rows (16 and 32: the
+ * streaming kernel), the most rows of a and waves of a workgroup's tile, and the
+ * parts that K is split into.  An MI355X choice from measured times, and no part of
+ * the results' contract.  Pure host code; sizes and errors as for the products. */
+int moe_product_plan(int64_t rows, int32_t N, int32_t K, int32_t E, int32_t bf16, int32_t num_cu,
+                     int32_t* weight_rows, int32_t* tile_rows, int32_t* waves, int32_t* parts);
+
 /* The same ladder with the tile classes given explicitly: the narrow
  * (swap-AB) class height and the tile width of each class (narrow, 32, 64,
  * 128).  Lets the ladder be checked against the outcomes the SM120 page
