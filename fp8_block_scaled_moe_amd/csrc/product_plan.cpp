@@ -1,6 +1,6 @@
 // Which kernel runs a product, and in how many parts of K: a model of the
 // kernels' times, fitted to sweeps on one MI355X.  It compares kernels with one
-// another; what it leaves out (the rate of memory) is alike for all of them.
+// another; the rate of memory and the host's share are left out.
 #include <math.h>
 
 #include "launch_products.h"
@@ -14,21 +14,33 @@ constexpr size_t kMaxPartial = (size_t)16 << 20;   // the parts' sums stay in th
 
 // us of a K step of one workgroup with TS sub-tiles a wave (base + per * TS), of
 // a round's start and end, and how many workgroups share a CU, each then taking
-// `shared` times as long.  Dense products, row-major, us (model | 256 x 256, 256 x
-// 128, 128 x 128, 128 x 64 measured; then 128 x 128 of eight waves):
-//   8192 x 4096 x 7168: 250, 287, 321, 437 | 253, 285, 290, 351
-//   2048 x 4096 x 7168: 127, 75, 83, 110 | 110, 77, 77, 95
-//   1111 x 4096 x 7168: 110, 75, 72, 64 | 104, 63, 65, 73
-//   4096 x 7168 x 2048: 81, 92, 88, 114 | 81, 92, 90, 108
-//   512 x 7168 x 2048:  43, 26, 23, 20 | 37, 23, 20, 18.5; 17.5 | 16.9
-//   512 x 1500 x 7168:  127, 75, 65, 41 | 129, 77, 65, 38
-//   2048 x 1500 x 7168: 127, 75, 67, 52 | 130, 76, 65, 52; 46 | 49
-//   1111 x 2000 x 1936: 43, 26, 23, 19 | 36, 24, 20, 18; 17.5 | 16.2
+// `shared` times as long.  Dense products, row-major, us (model | measured, 256 x
+// 256, 256 x 128, 128 x 128, 128 x 64; 128 x 128 of eight waves):
+//   8192 x 4096 x 7168: 250, 287, 321, 435; 343 | 240, 282, 281, 349; 341
+//   2048 x 4096 x 7168: 127, 75, 83, 112; 89 | 111, 74, 74, 95; 87
+//   1111 x 4096 x 7168: 118, 75, 75, 85; 89 | 104, 64, 66, 72; 79
+//   4096 x 7168 x 2048: 82, 92, 88, 117; 99 | 78, 91, 87, 105; 101
+//   512 x 7168 x 2048:  43, 26, 23, 20; 17.5 | 37, 24, 21, 18.6; 16.4
+//   512 x 1500 x 7168:  127, 75, 65, 40; 46 | 129, 77, 65, 38; 49
+//   2048 x 1500 x 7168: 127, 75, 65, 54; 46 | 130, 77, 65, 53; 49
+//   1111 x 2000 x 1936: 40, 26, 23, 18; 17.5 | 37, 25, 20, 18; 16
 // grouped, MFMA-tiled:
-//   256 groups of 256 rows, 7168 x 2048: 1403, 1545, 1686, 2000 | 1430, 1599, 1637, 1956
-//   128 of 256, 1536 x 2048: 170, 180, 184, 236 | 174, 188, 181, 218
-//   128 of 100, 1536 x 2048: 88, 70, 76, 101 | 99, 98, 97, 111 (its weights alone take 75)
-//   8 of 160, 4096 x 4096:   60, 41, 46, 51 | 60, 47, 47, 55
+//   256 groups of 256 rows, 7168 x 2048: 1403, 1545, 1687, 2035; 1897 | 1402, 1590, 1551, 1879; 1929
+//   128 of 256, 1536 x 2048: 171, 180, 184, 222; 207 | 178, 189, 183, 213; 221
+//   128 of 100, 1536 x 2048: 88, 70, 76, 109; 85 | 103, 101, 100, 114; 110 (its weights alone take 75)
+//   8 of 160, 4096 x 4096:   60, 41, 45, 51; 54 | 61, 48, 48, 55; 53
+//
+// The rate of memory: few rows of large weights take longer than the model says
+// with every kernel, and the one it picks is within a tenth of the best.  Row-major,
+// us of 1, 8, 33, 64 rows, streaming 32 weight rows in one part | 128 x 64 in the
+// parts that are picked:
+//   36864 x 7168 (43 at the rate of a long read): 49, 54, 100, 141 | 54, 55, 65, 72
+//   7168 x 18432 (22):                            27, 30, 49, 71   | 30, 31, 34, 38
+//   65536 x 2048 (22):                            28, 30, 58, 79   | 25, 26, 28, 30
+// The host: a call in parts makes two launches, which the model counts as the GPU
+// does.  512 x 7168, streaming 16 weight rows, one | four parts, us in a graph: one
+// row 7.0 | 6.1, MFMA-tiled 5.4 | 5.6; 16 rows 10.6 | 7.5, tiled 8.4 | 6.9; outside
+// of graphs 7.4 | 10.0, 7.2 | 10.0; 10.6 | 10.2, 8.4 | 10.2.
 struct TileCost {
   ProductShape shape;
   int tn, tm, wm, per_cu;

@@ -6,13 +6,14 @@
 // the order of the waves, so results do not depend on timing.
 //
 // What bounds it (one MI355X): 256 groups of two rows, 4096 x 7168, MFMA-tiled,
-// take 1035 us, 6.3 TB/s of weights, the rate of a long read; one row of 7168 x
-// 2048 5.8 us in a graph, of which 3 are a launch.  With more rows it is the
+// take 1037 us, 6.3 TB/s of weights, the rate of a long read; one row of 7168 x
+// 2048 5.9 us in a graph, of which 3 are a launch.  With more rows it is the
 // loads in MFMA order, 64 bytes of each of 16 rows, 38 B/ns a CU: 33 rows of
 // 1500 x 7168 take 12 us.  Whole lines, turned to MFMA order through LDS, were
 // faster in long rows (33 x 4096 x 7168: 15.6 -> 14.0 us), slower in short ones
-// (33 x 2000 x 1936: 5.7 -> 6.8) and are not taken: from 64 rows on the tile
-// kernels do that.
+// (33 x 2000 x 1936: 5.7 -> 6.8) and are not taken.  Dense products of up to 1024
+// rows stream where plan_product finds that faster than tiles: always with a few
+// rows and columns, up to about 1000 rows where there are few columns.
 #include "int8_common.h"
 #include "products.h"
 

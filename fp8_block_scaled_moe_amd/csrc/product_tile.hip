@@ -10,12 +10,12 @@
 // consecutive output columns of one row, and needs one scale a step and
 // sub-tile.
 //
-// What bounds it (one MI355X): 8192 x 4096 x 7168 in FP8 takes 230 us, 2.09
-// PFLOP/s, 1.9 us a step of a 256 x 256 tile.  The same step in a bare loop: its
+// What bounds it (one MI355X): 8192 x 4096 x 7168 in FP8 takes 236 us, 2.04
+// PFLOP/s, 2.0 us a step of a 256 x 256 tile.  The same step in a bare loop: its
 // products alone 1.43 us (a clock of 1.9 GHz, the card at its power limit), with
 // the folds 1.50, with the loads 1.49, with both 1.67 to 1.73: folds and loads
 // each hide under the products, not both.  Where groups have few rows the
-// weights' bytes are next: 256 groups of 256 rows, 7168 x 2048, 1.44 ms, 1.34
+// weights' bytes are next: 256 groups of 256 rows, 7168 x 2048, 1.48 ms, 1.30
 // PFLOP/s; half of them need a second tile for a few rows over 256.  bf16 (no
 // folds): 8192 x 8192 x 8192 864 us, 1.27 PFLOP/s.
 //

@@ -13,8 +13,8 @@
 // (far_silu_mul), and a block whose maximum is below 2^-60, where what is flushed
 // elsewhere could matter, is computed again in fp64.
 //
-// Bound by HBM: 65536 x 2048 gated bf16 takes 113 to 118 us on one MI355X, 5.7
-// to 5.9 TB/s, above a large copy's 5.2; one row of 7168 2.4 us, a launch.
+// Bound by HBM: 65536 x 2048 gated bf16 takes 117 to 121 us on one MI355X, 5.6
+// to 5.8 TB/s, above a large copy's 5.2; one row of 7168 2.4 us, a launch.
 #include "device_common.h"
 #include "launch_products.h"
 

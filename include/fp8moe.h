@@ -508,7 +508,8 @@ int moe_gemm2_weighted_int8(const void* q, const float* q_scale, const void* w2,
  * Each block of 128 values of K is summed by one MFMA and folded with the
  * product of its two scales in fp32; out is rounded once.  (The fp8 MFMA's own
  * sum of 128 products carries up to 5e-5 of the sum of their magnitudes;
- * typically 1e-6.)  NaN codes, infinite or NaN scales and products of scales
+ * typically 1e-6.  fp32 outputs of random operands are 3.3e-5 of their norm off,
+ * sums of fp32 products 1e-6; in bf16 outputs their rounding, 1.7e-3, hides it.)  NaN codes, infinite or NaN scales and products of scales
  * beyond fp32 give NaN or infinities in the rows and columns that they belong to.
  * K is a multiple of 16 and N any (MFMA_TILED: of 128 and 16; FP8MOE_ERR_ALIGN),
  * both at most FP8MOE_MAX_PRODUCT_DIM, M < 2^30 (FP8MOE_ERR_LIMIT).  a and b are
@@ -543,6 +544,9 @@ int gemm_fp8_blocks(const void* a, const float* a_scale, const void* b, const fl
  *            left as they were or hold any of those groups' results.
  *   out      bf16, or fp32 (out_f32 != 0) [rows, N]; rows of no group are not
  *            written
+ * The kernel is chosen by `rows`, the buffer's, since the host does not know how
+ * many of them the groups fill: a call on a mostly empty buffer runs that of a full
+ * one (1000 rows of 128 groups, 1536 x 2048: 78 us, in a buffer of 32000 rows 85).
  * Sums, types, sizes, alignment, overlap and errors as for gemm_fp8_blocks (in bf16 K is a
  * multiple of 8, MFMA_TILED of 64: moe_pack_weights takes bytes, 2 K).
  * 1 <= E <= FP8MOE_MAX_EXPERTS, rows < 2^30.  rows == 0 launches nothing.
