@@ -22,7 +22,7 @@ struct ProductArgs {
   int64_t rows;
   int N, E;
   int kbytes;              // bytes of a row of a or b, a multiple of 16; KT = ceil(kbytes / 128) steps
-  int splits;              // parts of K whose sums go to `partial` [splits][rows][N, whole groups of 8]; 1: straight to out
+  int splits;              // parts of K whose sums go to `partial` [splits][rows][N up to a multiple of 8]; 1: to out
   float* partial;
   bool bf16, packed, out_f32, vec;
 };

@@ -509,8 +509,9 @@ int moe_gemm2_weighted_int8(const void* q, const float* q_scale, const void* w2,
  * product of its two scales in fp32; out is rounded once.  (The fp8 MFMA's own
  * sum of 128 products carries up to 5e-5 of the sum of their magnitudes;
  * typically 1e-6.  fp32 outputs of random operands are 3.3e-5 of their norm off,
- * sums of fp32 products 1e-6; in bf16 outputs their rounding, 1.7e-3, hides it.)  NaN codes, infinite or NaN scales and products of scales
- * beyond fp32 give NaN or infinities in the rows and columns that they belong to.
+ * sums of fp32 products 1e-6; in bf16 outputs their rounding, 1.7e-3, hides it.)
+ * NaN codes, infinite or NaN scales and products of scales beyond fp32 give NaN or
+ * infinities in the rows and columns that they belong to.
  * K is a multiple of 16 and N any (MFMA_TILED: of 128 and 16; FP8MOE_ERR_ALIGN),
  * both at most FP8MOE_MAX_PRODUCT_DIM, M < 2^30 (FP8MOE_ERR_LIMIT).  a and b are
  * 16-byte aligned, the others to their elements (FP8MOE_ERR_ALIGN); out overlaps
